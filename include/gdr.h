@@ -30,9 +30,10 @@
  *     NULL is the legacy default stream).  Argument checks are synchronous and
  *     return before anything is launched.
  *   - Layouts are dense row-major, last index fastest.  Every pointer must be
- *     16-byte aligned.
+ *     16-byte aligned, unless its entry point says less.
  *   - Element types: q, k, v use `qkv_dtype`; o uses `out_dtype`; g, beta, theta,
- *     S0, S_T and the decode state S are always fp32.
+ *     S0, S_T and the decode state S are always fp32 (the scan, the layer norm and the
+ *     beam selection have descriptors of their own, below).
  *   - Errors: GDR_ERR_INVALID_ARG / GDR_ERR_UNSUPPORTED mean nothing was
  *     launched.  GDR_ERR_CUDA means a launch failed (see gdr_last_error_detail).
  *     No call aborts or throws.
@@ -46,7 +47,7 @@
 extern "C" {
 #endif
 
-#define GDR_ABI_VERSION 5
+#define GDR_ABI_VERSION 6
 
 #if defined(__GNUC__)
 #define GDR_API __attribute__((visibility("default")))
@@ -64,7 +65,9 @@ typedef enum {
     GDR_ERR_TIMEOUT = 4,     /* a kernel gave up on a bounded wait (device status word) */
     GDR_ERR_WORKSPACE = 5,   /* workspace pointer NULL or smaller than required */
     GDR_ERR_RANGE = 6,       /* a decay factor left the factored range (device status word) */
-    GDR_ERR_BOUNDS = 7       /* an index check of the debug build failed (device status word) */
+    GDR_ERR_BOUNDS = 7,      /* an index check of the debug build failed (device status word) */
+    GDR_ERR_INDEX = 8        /* an index that the caller passed in device memory was out of range
+                                (device status word; see gdr_state_reorder) */
 } gdr_status;
 
 typedef enum { GDR_F32 = 0, GDR_BF16 = 1 } gdr_dtype;
@@ -296,7 +299,8 @@ GDR_API gdr_status gdr_chunk_fwd_host(const gdr_fwd_desc* desc,
  * Synchronises `stream`, then reads and clears the device status word that
  * kernels set when a bounded wait gives up (GDR_ERR_TIMEOUT) or when the tensor-core
  * kernel meets a decay outside its factored range (GDR_ERR_RANGE; the outputs of that
- * call are not valid).  Returns GDR_OK, GDR_ERR_TIMEOUT, GDR_ERR_RANGE or GDR_ERR_CUDA
+ * call are not valid) or gdr_state_reorder an index outside its group (GDR_ERR_INDEX).
+ * Returns GDR_OK, GDR_ERR_TIMEOUT, GDR_ERR_RANGE, GDR_ERR_INDEX or GDR_ERR_CUDA
  * (a sticky CUDA error on the context).  Uses the current device.
  */
 GDR_API gdr_status gdr_query_device_status(gdr_stream_t stream);
@@ -450,6 +454,149 @@ GDR_API gdr_status gdr_raven_fwd(const gdr_raven_desc* desc, const void* q, cons
                                  const float* z, const float* g, const float* S0k, const float* S0v,
                                  void* o, float* Sk_T, float* Sv_T, void* workspace,
                                  size_t workspace_bytes, gdr_stream_t stream);
+
+/*
+ * Gated linear recurrence per channel (a scan over the sequence): the delta rule's decay without
+ * its matrix, for the layers of a recurrent model that keep one value per channel.  Per sequence b
+ * and channel c, tokens t = 1..T,
+ *
+ *     h_t = a_t h_{t-1} + w_t x_t
+ *
+ * with the decay a_t from the gate g_t by the library's gate modes (GDR_GATE_LOGDECAY: exp(g),
+ * GDR_GATE_NEG_SOFTPLUS: exp(-softplus(g)) = sigmoid(-g)) and w_t = 1, or w_t = 1 - a_t with
+ * tied = 1 (a moving average of x).  States, decays and sums are fp32; h, dx and dg are rounded
+ * once, when they are stored.  Every result is the same from run to run.
+ *
+ * lengths (device memory, int [B], 4-byte aligned, or NULL: all T): sequence b has min(max(lengths[b], 0), T)
+ * tokens.  What lies behind them in x, g and dh is not read; h, dx and dg are written as zero
+ * there, and h_T is the state after the last token (h0 for an empty sequence).
+ */
+#define GDR_SCAN_CKPT 64
+typedef struct {
+    int B, T, D;          /* sequences, tokens (T >= 0), channels */
+    long long x_row;      /* elements from one token of x to the next (>= D; 0: D); a sequence is   */
+    long long g_row;      /*   T rows, so x may be a slice of a wider [B,T,..] tensor; same for g   */
+    gdr_dtype x_dtype;    /* x and dx */
+    gdr_dtype g_dtype;    /* g and dg */
+    gdr_dtype out_dtype;  /* h and dh; o of the step */
+    gdr_gate_mode gate_mode;
+    int tied;             /* 0: w = 1, 1: w = 1 - a */
+} gdr_scan_desc;
+
+/*
+ * Forward.  x [B,T,D] x_dtype, g [B,T,D] g_dtype (rows x_row / g_row apart; these two pointers need
+ * only their element's alignment);  h0 [B,D] fp32 or NULL (zero);  h [B,T,D] out_dtype (written);
+ * h_T [B,D] fp32 or NULL (may alias h0);  ckpt [B, ceil(T/64), D] fp32 or NULL: the states before
+ * tokens 0, 64, 128, .. (the state after the last token where the sequence has ended), which
+ * gdr_scan_bwd starts from.  One launch, no workspace.
+ */
+GDR_API gdr_status gdr_scan_fwd(const gdr_scan_desc* desc, const void* x, const void* g, const float* h0,
+                                const int* lengths, void* h, float* h_T, float* ckpt, gdr_stream_t stream);
+/*
+ * Backward of gdr_scan_fwd, given ckpt from a forward of the same inputs, dh = dL/dh [B,T,D]
+ * out_dtype (or NULL: zero) and dh_T = dL/dh_T [B,D] fp32 (or NULL: zero):
+ *   lam_t = dh_t + a_{t+1} lam_{t+1}  (lam_T takes dh_T too),     dx_t = w_t lam_t,
+ *   dg_t = lam_t (h_{t-1} - [tied] x_t) da_t/dg_t,                dh0 = a_1 lam_1.
+ * The states h_{t-1} are formed again from ckpt in fp32, so h itself is not an input.
+ * dx [B,T,D] x_dtype and dg [B,T,D] g_dtype are dense (rows of D) and required when T > 0;
+ * dh0 [B,D] fp32 or NULL.  With T = 0, dh0 = dh_T.  One launch, no workspace.
+ */
+GDR_API gdr_status gdr_scan_bwd(const gdr_scan_desc* desc, const void* x, const void* g, const float* ckpt,
+                                const int* lengths, const void* dh, const float* dh_T, void* dx, void* dg,
+                                float* dh0, gdr_stream_t stream);
+/*
+ * One token of B sequences: h [B,D] fp32 is updated in place, o [B,D] out_dtype receives it (or
+ * NULL).  desc->T is ignored; x_row / g_row are the distances between sequences.
+ */
+GDR_API gdr_status gdr_scan_step(const gdr_scan_desc* desc, const void* x, const void* g, float* h, void* o,
+                                 gdr_stream_t stream);
+
+/*
+ * Layer norm of `rows` rows of D values, as a mixer block has it on its input (D = the model's
+ * width) and on each head's output (D = dv):
+ *
+ *     y = (x - mean) * rstd * weight + bias,    rstd = 1 / sqrt(mean((x - mean)^2) + eps)
+ *
+ * Statistics and sums are fp32, the variance from the centred values.
+ */
+typedef struct {
+    long long rows;       /* >= 0 */
+    int D;                /* 1 .. 2^20 */
+    gdr_dtype x_dtype;    /* x and dx */
+    gdr_dtype y_dtype;    /* y and dy */
+    gdr_dtype w_dtype;    /* weight and bias */
+    float eps;
+} gdr_norm_desc;
+
+/*
+ * x [rows,D], weight [D] or NULL (ones), bias [D] or NULL (zeros); y [rows,D] (written);
+ * mean, rstd [rows] fp32, or NULL where no backward follows.  One launch, no workspace.
+ */
+GDR_API gdr_status gdr_layernorm_fwd(const gdr_norm_desc* desc, const void* x, const void* weight,
+                                     const void* bias, void* y, float* mean, float* rstd, gdr_stream_t stream);
+/*
+ * Backward, given mean and rstd of the forward and dy = dL/dy [rows,D] (xh = (x - mean) rstd):
+ *   dx = rstd (w dy - mean_D(w dy) - xh mean_D(w dy xh)),   dweight = sum_rows dy xh,   dbias = sum_rows dy.
+ * dx [rows,D] x_dtype, or NULL; dweight, dbias [D] fp32, or NULL each.  The sums over rows run in
+ * a fixed order (the same result from run to run); the workspace holds every block's share of
+ * them (gdr_layernorm_bwd_workspace_bytes; 0 when neither is asked for).  Two launches (one
+ * without dweight and dbias).
+ */
+GDR_API size_t gdr_layernorm_bwd_workspace_bytes(const gdr_norm_desc* desc, int with_dweight, int with_dbias);
+GDR_API gdr_status gdr_layernorm_bwd(const gdr_norm_desc* desc, const void* x, const void* dy, const void* weight,
+                                     const float* mean, const float* rstd, void* dx, float* dweight, float* dbias,
+                                     void* workspace, size_t workspace_bytes, gdr_stream_t stream);
+
+/*
+ * Beam search's selection for the decode loop: of the K * V continuations of each of G groups of K
+ * beams, the M best, best first.  Candidate (k, v) has the score
+ *
+ *     scores[k] + logits[k, v] - log sum_u exp(logits[k, u])
+ *
+ * compared in 64 bits; equal ones go by the lowest k * V + v.  A beam with finished[k] != 0 has
+ * one candidate, token `eos` at its unchanged score.  A candidate that is not a number counts as
+ * -inf: so does every one of a beam whose score or logits hold a NaN or +inf, whose score is -inf,
+ * or whose logits are all -inf (with the first token, give all beams but one the score -inf).
+ * Where fewer than M candidates are above -inf, the list is filled with -inf ones by the lowest
+ * k * V + v.
+ *
+ * The sums run in fp32; where two neighbours of the list that belong to different beams are
+ * closer than that allows, the beams' sums are formed again in 64 bits before they are ordered.
+ */
+typedef struct {
+    int G, K, V, M;       /* groups, beams (1..64), vocabulary, candidates out (1..64, <= K * V); K * V < 2^31 */
+    long long row;        /* elements from one beam's logits to the next (>= V; 0: V) */
+    gdr_dtype x_dtype;    /* logits */
+    int eos;              /* 0 .. V - 1; read only with `finished` */
+} gdr_beam_desc;
+
+/*
+ * logits [G,K,V] x_dtype (rows `row` apart);  scores [G,K] fp32;  finished [G,K] bytes or NULL;
+ * out_scores [G,M] fp32, out_parent, out_token [G,M] int: the M candidates' scores, beams
+ * (0 .. K-1, in the group) and tokens.  These pointers need only their elements' alignment, the
+ * workspace 16 bytes.  Two launches.
+ */
+GDR_API size_t gdr_beam_select_workspace_bytes(const gdr_beam_desc* desc);
+GDR_API gdr_status gdr_beam_select(const gdr_beam_desc* desc, const void* logits, const float* scores,
+                                   const unsigned char* finished, float* out_scores, int* out_parent,
+                                   int* out_token, void* workspace, size_t workspace_bytes, gdr_stream_t stream);
+
+/*
+ * The recurrent states follow their beams, in place: for every layer l, group g and beam j,
+ *
+ *     S[l, g, j] <- S[l, g, parent[g, j]]   (the values before the call)
+ *
+ * S is [L, G, K] states of state_bytes each (decode states [N,H,dv,dk] with N = G * K, Raven's
+ * slots, the scan's h; any element type), parent [G,K] int (4-byte aligned).  Beams that keep their state are not
+ * moved.  A parent outside 0 .. K-1 leaves its beam as it is and sets the status word
+ * (gdr_query_device_status -> GDR_ERR_INDEX).  One launch, no workspace.
+ */
+typedef struct {
+    int L, G, K;          /* layers, groups, beams per group (1..64) */
+    size_t state_bytes;   /* bytes of one beam's state in one layer */
+} gdr_reorder_desc;
+
+GDR_API gdr_status gdr_state_reorder(const gdr_reorder_desc* desc, void* S, const int* parent, gdr_stream_t stream);
 
 /*
  * Test hook for the bounded waits of the tensor-core kernel (process-wide, not

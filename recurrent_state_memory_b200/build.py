@@ -5,6 +5,7 @@
 import os
 import subprocess
 import sys
+from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -14,7 +15,8 @@ LIB = os.path.join(PKG, "libgdr.so")
 LIB_DEBUG = os.path.join(PKG, "libgdr_debug.so")    # every kernel's computed indices checked
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 
-SOURCES = ["gdr.cu"]
+SOURCES = ["gdr.cu", "scan.cu", "norm.cu", "beam.cu"]
+OBJ = os.path.join(PKG, "_build")                   # object files, one folder per build kind
 
 
 def _deps():
@@ -22,6 +24,15 @@ def _deps():
     files.append(os.path.join(INCLUDE, "gdr.h"))
     files.append(os.path.abspath(__file__))
     return files
+
+
+def _fresh(out, dep):
+    """Whether the object file is newer than this file and every source it was made from."""
+    if not (os.path.exists(out) and os.path.exists(dep)):
+        return False
+    files = open(dep).read().replace("\\\n", " ").split(":", 1)[1].split()
+    made = os.path.getmtime(out)
+    return all(os.path.exists(f) and os.path.getmtime(f) <= made for f in files + [os.path.abspath(__file__)])
 
 
 def build(force: bool = False, verbose: bool = False, debug: bool = False) -> str:
@@ -33,16 +44,28 @@ def build(force: bool = False, verbose: bool = False, debug: bool = False) -> st
         newest = max(os.path.getmtime(f) for f in _deps())
         if os.path.getmtime(lib) >= newest:
             return lib
-    tmp = lib + ".tmp"
-    cmd = [NVCC, "-O3", "-std=c++17", "-gencode", "arch=compute_100a,code=sm_100a", "-lineinfo",
-           "-shared", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
-           "--expt-relaxed-constexpr", "-I", INCLUDE, "-I", CSRC,
-           "-o", tmp] + [os.path.join(CSRC, s) for s in SOURCES]
+    obj = os.path.join(OBJ, "debug" if debug else "default")
+    os.makedirs(obj, exist_ok=True)
+    common = [NVCC, "-O3", "-std=c++17", "-gencode", "arch=compute_100a,code=sm_100a", "-lineinfo",
+              "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
+              "--expt-relaxed-constexpr", "-I", INCLUDE, "-I", CSRC]
     if debug:
-        cmd.insert(1, "-DGDR_BOUNDS_CHECK")
+        common.append("-DGDR_BOUNDS_CHECK")
     if verbose:
-        cmd.insert(1, "-Xptxas=-v")
-    subprocess.run(cmd, check=True)
+        common.append("-Xptxas=-v")
+
+    def compile_one(src):
+        out = os.path.join(obj, src + ".o")
+        dep = out + ".d"
+        if not force and _fresh(out, dep):
+            return out
+        subprocess.run(common + ["-MD", "-MF", dep, "-c", "-o", out, os.path.join(CSRC, src)], check=True)
+        return out
+
+    with ThreadPoolExecutor(max_workers=len(SOURCES)) as pool:     # nvcc processes, side by side
+        objects = list(pool.map(compile_one, SOURCES))
+    tmp = lib + ".tmp"
+    subprocess.run(common[:6] + ["-shared", "-o", tmp] + objects, check=True)
     os.replace(tmp, lib)
     return lib
 

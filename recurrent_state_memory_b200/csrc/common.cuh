@@ -9,15 +9,16 @@ namespace gdr {
 
 // Device status word: kernels OR in a bit when a bounded wait gives up (bit 0) or a
 // decay factor leaves the range of the factored tensor-core form (bit 1).  Read and
-// cleared by gdr_query_device_status.  (All kernels live in one translation unit.)
-__device__ unsigned int g_device_status = 0;
+// cleared by gdr_query_device_status.  (Every translation unit has a word of its own.)
+static __device__ unsigned int g_device_status = 0;
 
 // Index checks of the debug build (compiled with -DGDR_BOUNDS_CHECK).  GDR_INB(cond, site)
 // guards one global-memory access: when cond fails, the site number goes to g_bounds_site (the
 // first failure is kept), bit 2 of the status word is set and the access is skipped.  In the
 // default build the macro is the constant true and costs nothing.
 constexpr unsigned STATUS_BOUNDS = 4u;
-__device__ unsigned int g_bounds_site = 0;
+constexpr unsigned STATUS_INDEX = 8u;      // an index that the caller passed in device memory is out of range
+static __device__ unsigned int g_bounds_site = 0;
 #ifdef GDR_BOUNDS_CHECK
 __device__ __forceinline__ bool in_bounds(bool c, unsigned site) {
     if (!c) {
@@ -30,6 +31,21 @@ __device__ __forceinline__ bool in_bounds(bool c, unsigned site) {
 #else
 #define GDR_INB(cond, site) true
 #endif
+
+// Read and clear this translation unit's status word / first bounds site (NULL: not asked for).
+static inline cudaError_t take_status_here(unsigned int* word, unsigned int* site) {
+    const unsigned int zero = 0;
+    cudaError_t e = cudaSuccess;
+    if (word) {
+        e = cudaMemcpyFromSymbol(word, g_device_status, sizeof(zero));
+        if (e == cudaSuccess && *word) e = cudaMemcpyToSymbol(g_device_status, &zero, sizeof(zero));
+    }
+    if (site && e == cudaSuccess) {
+        e = cudaMemcpyFromSymbol(site, g_bounds_site, sizeof(zero));
+        if (e == cudaSuccess && *site) e = cudaMemcpyToSymbol(g_bounds_site, &zero, sizeof(zero));
+    }
+    return e;
+}
 
 // Element loads/stores with the storage type chosen at compile time.
 template <typename T> __device__ __forceinline__ float ld_f32(const T* p);
@@ -56,6 +72,22 @@ __device__ __forceinline__ float log_decay(float a, int gate_mode) {
 __device__ __forceinline__ float decay_factor(float a, int gate_mode) {
     if (gate_mode == 1) return 1.f / (1.f + expf(a));
     return expf(a);
+}
+
+// The decay a = exp(g) of one gate value and 1 - a, both to full relative precision (1 - a from
+// the difference would lose it where a is near one).  gate_mode 1: sigmoid(-v) and sigmoid(v),
+// formed from e^{-|v|} <= 1 so that neither overflows.
+__device__ __forceinline__ void decay_pair(float v, int gate_mode, float& a, float& rest) {
+    if (gate_mode == 1) {
+        const float e = expf(-fabsf(v));
+        const float r = 1.f / (1.f + e), er = e * r;
+        a = v >= 0.f ? er : r;
+        rest = v >= 0.f ? r : er;
+        if (v != v) a = rest = v;
+    } else {
+        a = expf(v);
+        rest = -expm1f(v);
+    }
 }
 
 // Reduce an angle to [-pi, pi] so that sums of many angles keep full accuracy.

@@ -1,12 +1,13 @@
-// gdr.cu -- the C ABI declared in include/gdr.h: argument checks and kernel dispatch.
-//
-// All kernels are compiled into this one translation unit so that the device
-// status word below is a single symbol per loaded module.
+// gdr.cu -- the delta rule's and Raven's part of the C ABI declared in include/gdr.h: argument
+// checks and kernel dispatch.  (scan.cu, norm.cu and beam.cu hold the other entry points; each
+// translation unit has a device status word of its own, read together below.)
 #include <cstdio>
 #include <cstring>
+#include <initializer_list>
 #include <mutex>
 
 #include "gdr.h"
+#include "host.cuh"
 #include "common.cuh"
 #include "simt_fwd.cuh"
 #include "decode.cuh"
@@ -23,21 +24,7 @@ namespace gdr {
 static unsigned long long s_wait_limit_ns = 2000000000ull;
 static int s_fault_skip_commit = 0;
 
-static thread_local char t_detail[256] = "";
-
-static gdr_status fail(gdr_status s, const char* fmt, const char* what = "") {
-    snprintf(t_detail, sizeof(t_detail), fmt, what);
-    return s;
-}
-
-static gdr_status cuda_fail(cudaError_t e, const char* where) {
-    snprintf(t_detail, sizeof(t_detail), "%s: %s", where, cudaGetErrorString(e));
-    return GDR_ERR_CUDA;
-}
-
-static bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 static bool head_dim_ok(int d) { return d == 32 || d == 64 || d == 128; }
-static bool dtype_ok(gdr_dtype t) { return t == GDR_F32 || t == GDR_BF16; }
 
 // ---------------------------------------------------------------- forward ----
 
@@ -74,13 +61,6 @@ static gdr_status dispatch_simt_dk(const gdr_fwd_desc* d, const FwdParams& p, cu
 
 static bool tc_supported(const gdr_fwd_desc* d) {
     return d->qkv_dtype == GDR_BF16 && d->dk == 128 && d->dv == 128 && d->chunk == 64;
-}
-
-static int device_sm_count() {
-    int dev = 0, n = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) { cudaGetLastError(); return 148; }
-    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) { cudaGetLastError(); return 148; }
-    return n;
 }
 
 // The split kernel runs the state chains on `nc` SMs and prepares chunks on the others; with
@@ -858,6 +838,7 @@ const char* gdr_status_string(gdr_status s) {
         case GDR_ERR_WORKSPACE: return "GDR_ERR_WORKSPACE";
         case GDR_ERR_RANGE: return "GDR_ERR_RANGE";
         case GDR_ERR_BOUNDS: return "GDR_ERR_BOUNDS";
+        case GDR_ERR_INDEX: return "GDR_ERR_INDEX";
     }
     return "GDR_ERR_UNKNOWN";
 }
@@ -1024,9 +1005,18 @@ gdr_status gdr_query_device_status(gdr_stream_t stream) {
     if (word != 0) {
         e = cudaMemcpyToSymbol(g_device_status, &zero, sizeof(zero));
         if (e != cudaSuccess) return cuda_fail(e, "cudaMemcpyToSymbol(status)");
+    }
+    for (auto take : {scan_take_status, norm_take_status, beam_take_status}) {
+        unsigned int more = 0;
+        e = take(&more, nullptr);
+        if (e != cudaSuccess) return cuda_fail(e, "status of scan.cu, norm.cu, beam.cu");
+        word |= more;
+    }
+    if (word != 0) {
         snprintf(t_detail, sizeof(t_detail), "device status word 0x%08x", word);
         if (word & tcf::STATUS_TIMEOUT) return GDR_ERR_TIMEOUT;
-        return (word & STATUS_BOUNDS) ? GDR_ERR_BOUNDS : GDR_ERR_RANGE;
+        if (word & STATUS_BOUNDS) return GDR_ERR_BOUNDS;
+        return (word & STATUS_INDEX) ? GDR_ERR_INDEX : GDR_ERR_RANGE;
     }
     return GDR_OK;
 }
@@ -1038,6 +1028,11 @@ int gdr_debug_bounds_site(void) {
         cudaMemcpyToSymbol(g_bounds_site, &zero, sizeof(zero)) != cudaSuccess) {
         cudaGetLastError();
         return -2;
+    }
+    for (auto take : {scan_take_status, norm_take_status, beam_take_status}) {
+        unsigned int more = 0;
+        if (take(nullptr, &more) != cudaSuccess) { cudaGetLastError(); return -2; }
+        if (site == 0) site = more;
     }
     return (int)site;
 #else

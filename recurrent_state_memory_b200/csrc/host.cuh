@@ -1,0 +1,44 @@
+// host.cuh -- host-side helpers shared by the library's translation units: the error detail of
+// the calling thread, argument predicates, the SM count, and the device status words.
+#pragma once
+
+#include <cstdint>
+#include <cstdio>
+
+#include <cuda_runtime.h>
+
+#include "gdr.h"
+
+namespace gdr {
+
+inline thread_local char t_detail[256] = "";
+
+inline gdr_status fail(gdr_status s, const char* fmt, const char* what = "") {
+    snprintf(t_detail, sizeof(t_detail), fmt, what);
+    return s;
+}
+
+inline gdr_status cuda_fail(cudaError_t e, const char* where) {
+    snprintf(t_detail, sizeof(t_detail), "%s: %s", where, cudaGetErrorString(e));
+    return GDR_ERR_CUDA;
+}
+
+inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+inline bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+inline bool dtype_ok(gdr_dtype t) { return t == GDR_F32 || t == GDR_BF16; }
+inline size_t dtype_bytes(gdr_dtype t) { return t == GDR_BF16 ? 2 : 4; }
+
+inline int device_sm_count() {
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) { cudaGetLastError(); return 148; }
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) { cudaGetLastError(); return 148; }
+    return n;
+}
+
+// Every translation unit has a status word and a bounds site of its own (common.cuh); these read
+// and clear the ones of the files named.  *site is only written in the debug build.
+cudaError_t scan_take_status(unsigned int* word, unsigned int* site);
+cudaError_t norm_take_status(unsigned int* word, unsigned int* site);
+cudaError_t beam_take_status(unsigned int* word, unsigned int* site);
+
+}  // namespace gdr

@@ -21,7 +21,8 @@ LIB_PATH = os.path.join(_HERE, "libgdr.so")
 HEADER_PATH = os.path.join(os.path.dirname(_HERE), "include", "gdr.h")
 
 (GDR_OK, GDR_ERR_INVALID_ARG, GDR_ERR_UNSUPPORTED, GDR_ERR_CUDA, GDR_ERR_TIMEOUT, GDR_ERR_WORKSPACE,
- GDR_ERR_RANGE, GDR_ERR_BOUNDS) = range(8)
+ GDR_ERR_RANGE, GDR_ERR_BOUNDS, GDR_ERR_INDEX) = range(9)
+SCAN_CKPT = 64              # tokens between two saved states of the scan (GDR_SCAN_CKPT)
 GDR_F32, GDR_BF16 = 0, 1
 GATE_LOGDECAY, GATE_NEG_SOFTPLUS = 0, 1
 ALGOS = {"auto": 0, "simt": 1, "tcgen05": 2, "tcgen05_split": 3, "tcgen05_waves": 4, "tcgen05_segments": 5,
@@ -50,6 +51,26 @@ class RavenDesc(ctypes.Structure):
                 ("slots", ctypes.c_int), ("topk", ctypes.c_int), ("qkv_dtype", ctypes.c_int),
                 ("out_dtype", ctypes.c_int), ("gate_mode", ctypes.c_int), ("scale", ctypes.c_float),
                 ("segments", ctypes.c_int)]
+
+
+class ScanDesc(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int), ("T", ctypes.c_int), ("D", ctypes.c_int), ("x_row", ctypes.c_longlong),
+                ("g_row", ctypes.c_longlong), ("x_dtype", ctypes.c_int), ("g_dtype", ctypes.c_int),
+                ("out_dtype", ctypes.c_int), ("gate_mode", ctypes.c_int), ("tied", ctypes.c_int)]
+
+
+class NormDesc(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_longlong), ("D", ctypes.c_int), ("x_dtype", ctypes.c_int),
+                ("y_dtype", ctypes.c_int), ("w_dtype", ctypes.c_int), ("eps", ctypes.c_float)]
+
+
+class BeamDesc(ctypes.Structure):
+    _fields_ = [("G", ctypes.c_int), ("K", ctypes.c_int), ("V", ctypes.c_int), ("M", ctypes.c_int),
+                ("row", ctypes.c_longlong), ("x_dtype", ctypes.c_int), ("eos", ctypes.c_int)]
+
+
+class ReorderDesc(ctypes.Structure):
+    _fields_ = [("L", ctypes.c_int), ("G", ctypes.c_int), ("K", ctypes.c_int), ("state_bytes", ctypes.c_size_t)]
 
 
 class GdrError(RuntimeError):
@@ -112,9 +133,27 @@ def lib() -> ctypes.CDLL:
                                     ctypes.c_size_t, vp]
         L.gdr_chunk_fwd_noalloc.restype = ctypes.c_int
         L.gdr_chunk_fwd_noalloc.argtypes = [ctypes.POINTER(FwdDesc), vp, vp, vp, fp, fp, fp, fp, vp, fp, vp]
+        L.gdr_scan_fwd.restype = ctypes.c_int
+        L.gdr_scan_fwd.argtypes = [ctypes.POINTER(ScanDesc), vp, vp, fp, vp, vp, fp, fp, vp]
+        L.gdr_scan_bwd.restype = ctypes.c_int
+        L.gdr_scan_bwd.argtypes = [ctypes.POINTER(ScanDesc), vp, vp, fp, vp, vp, fp, vp, vp, fp, vp]
+        L.gdr_scan_step.restype = ctypes.c_int
+        L.gdr_scan_step.argtypes = [ctypes.POINTER(ScanDesc), vp, vp, fp, vp, vp]
+        L.gdr_layernorm_fwd.restype = ctypes.c_int
+        L.gdr_layernorm_fwd.argtypes = [ctypes.POINTER(NormDesc), vp, vp, vp, vp, fp, fp, vp]
+        L.gdr_layernorm_bwd_workspace_bytes.restype = sz
+        L.gdr_layernorm_bwd_workspace_bytes.argtypes = [ctypes.POINTER(NormDesc), ctypes.c_int, ctypes.c_int]
+        L.gdr_layernorm_bwd.restype = ctypes.c_int
+        L.gdr_layernorm_bwd.argtypes = [ctypes.POINTER(NormDesc), vp, vp, vp, fp, fp, vp, fp, fp, vp, sz, vp]
+        L.gdr_beam_select_workspace_bytes.restype = sz
+        L.gdr_beam_select_workspace_bytes.argtypes = [ctypes.POINTER(BeamDesc)]
+        L.gdr_beam_select.restype = ctypes.c_int
+        L.gdr_beam_select.argtypes = [ctypes.POINTER(BeamDesc), vp, fp, vp, fp, vp, vp, vp, sz, vp]
+        L.gdr_state_reorder.restype = ctypes.c_int
+        L.gdr_state_reorder.argtypes = [ctypes.POINTER(ReorderDesc), vp, vp, vp]
         L.gdr_debug_set_tc_fault.restype = None
         L.gdr_debug_set_tc_fault.argtypes = [ctypes.c_int, ctypes.c_ulonglong]
-        if L.gdr_abi_version() != 5:
+        if L.gdr_abi_version() != 6:
             raise RuntimeError("libgdr.so ABI version mismatch")
         _lib = L
     return _lib
@@ -452,7 +491,234 @@ def decode_step(q, k, v, g, beta, S, theta=None, *, gate_mode=GATE_NEG_SOFTPLUS,
     return o
 
 
+# ------------------------------------------------ scan, layer norm, beam search ----
+
+
+def _on_device(t: torch.Tensor, name: str):
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return t.device
+
+
+def _check_shape(t, name, shape, dtype, dev):
+    _need(t, name, dtype, dev)
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} must have the shape {shape}, got {tuple(t.shape)}")
+
+
+def _row_stride(t: torch.Tensor, name: str) -> int:
+    """Elements between the rows of t (dense: 0), whose rows are dense and evenly spaced (a slice
+    along the last dimension of a wider contiguous tensor is)."""
+    if t.is_contiguous():
+        return 0
+    st, sh = t.stride(), t.shape
+    row = st[-2]
+    ok = st[-1] == 1 and row >= sh[-1]
+    for d in range(t.dim() - 3, -1, -1):
+        ok = ok and (sh[d] == 1 or st[d] == st[d + 1] * sh[d + 1])
+    if not ok:
+        raise ValueError(f"{name} must be contiguous, or a slice of a contiguous tensor along its last dimension")
+    return row
+
+
+def _call(fn, where, dev, stream, *args):
+    """One library call on `stream` (default: dev's current stream) with dev current."""
+    if dev.index == torch.cuda.current_device():
+        st = fn(*args, _stream_handle(stream, dev))
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, _stream_handle(stream, dev))
+    _check(st, where)
+
+
+def _scan_args(x, g, dims, lengths=None):
+    dev = _on_device(x, "x")
+    if x.dim() != dims or g.shape != x.shape:
+        raise ValueError("x and g must have the same shape, " + ("[B, T, D]" if dims == 3 else "[N, D]"))
+    if g.device != dev:
+        raise ValueError(f"g is on {g.device}, expected {dev}")
+    if lengths is not None:
+        _check_shape(lengths, "lengths", (x.shape[0],), torch.int32, dev)
+    return dev
+
+
+def scan_desc(B, T, D, x_dtype, g_dtype, out_dtype, gate_mode=GATE_NEG_SOFTPLUS, tied=False, x_row=0,
+              g_row=0) -> ScanDesc:
+    return ScanDesc(B, T, D, x_row, g_row, _dtype_code(x_dtype), _dtype_code(g_dtype), _dtype_code(out_dtype),
+                    int(gate_mode), int(bool(tied)))
+
+
+def scan_fwd(x, g, h0=None, *, gate_mode=GATE_NEG_SOFTPLUS, tied=False, lengths=None, out_dtype=None,
+             want_state=True, want_ckpt=False, stream=None):
+    """Gated linear recurrence per channel, h_t = a_t h_{t-1} + w_t x_t (``gdr_scan_fwd``).
+
+    x, g [B,T,D] (bf16 or fp32 each; slices of wider tensors along the last dimension are taken as
+    they are), a from the gate g by gate_mode, w = 1 or, tied, 1 - a; h0 [B,D] fp32 or None (zero);
+    lengths [B] int32 or None: tokens of each sequence (h is zero behind them).  Returns
+    (h [B,T,D], h_T [B,D] fp32), or (h, h_T, ckpt) with want_ckpt: the states that ``scan_bwd``
+    starts from.  h_T is None unless want_state.  Asynchronous on `stream` (default: current)."""
+    dev = _scan_args(x, g, 3, lengths)
+    B, T, D = x.shape
+    out_dtype = out_dtype or x.dtype
+    if h0 is not None:
+        _check_shape(h0, "h0", (B, D), torch.float32, dev)
+    desc = scan_desc(B, T, D, x.dtype, g.dtype, out_dtype, gate_mode, tied, _row_stride(x, "x"), _row_stride(g, "g"))
+    h = torch.empty((B, T, D), dtype=out_dtype, device=dev)
+    h_T = torch.empty((B, D), dtype=torch.float32, device=dev) if want_state else None
+    ckpt = torch.empty((B, -(-T // SCAN_CKPT), D), dtype=torch.float32, device=dev) if want_ckpt else None
+    _call(lib().gdr_scan_fwd, "gdr_scan_fwd", dev, stream, desc, _ptr(x), _ptr(g), _ptr(h0), _ptr(lengths), _ptr(h),
+          _ptr(h_T), _ptr(ckpt))
+    return (h, h_T, ckpt) if want_ckpt else (h, h_T)
+
+
+def scan_bwd(x, g, ckpt, dh=None, dh_T=None, *, gate_mode=GATE_NEG_SOFTPLUS, tied=False, lengths=None,
+             want_dh0=True, stream=None):
+    """Backward of ``scan_fwd``: the gradients of x, g and h0 given ckpt (from the forward of the same
+    inputs), dh [B,T,D] (like h) and dh_T [B,D] fp32; either may be None (zero).  Returns a dict
+    "x" (x's dtype), "g" (g's dtype), "h0" (fp32; None unless want_dh0)."""
+    dev = _scan_args(x, g, 3, lengths)
+    B, T, D = x.shape
+    _check_shape(ckpt, "ckpt", (B, -(-T // SCAN_CKPT), D), torch.float32, dev)
+    if dh is not None:
+        _check_shape(dh, "dh", (B, T, D), None, dev)
+    if dh_T is not None:
+        _check_shape(dh_T, "dh_T", (B, D), torch.float32, dev)
+    desc = scan_desc(B, T, D, x.dtype, g.dtype, x.dtype if dh is None else dh.dtype, gate_mode, tied,
+                     _row_stride(x, "x"), _row_stride(g, "g"))
+    out = {"x": torch.empty((B, T, D), dtype=x.dtype, device=dev), "g": torch.empty((B, T, D), dtype=g.dtype, device=dev),
+           "h0": torch.empty((B, D), dtype=torch.float32, device=dev) if want_dh0 else None}
+    _call(lib().gdr_scan_bwd, "gdr_scan_bwd", dev, stream, desc, _ptr(x), _ptr(g), _ptr(ckpt), _ptr(lengths), _ptr(dh),
+          _ptr(dh_T), _ptr(out["x"]), _ptr(out["g"]), _ptr(out["h0"]))
+    return out
+
+
+def scan_step(x, g, h, *, gate_mode=GATE_NEG_SOFTPLUS, tied=False, out_dtype=None, o=None, stream=None):
+    """One token of ``scan_fwd`` for N sequences: x, g [N,D]; h [N,D] fp32 is updated in place.
+    Returns o [N,D], the new state in out_dtype (default: x's)."""
+    dev = _scan_args(x, g, 2)
+    N, D = x.shape
+    out_dtype = out_dtype or x.dtype
+    _check_shape(h, "h", (N, D), torch.float32, dev)
+    if o is None:
+        o = torch.empty((N, D), dtype=out_dtype, device=dev)
+    else:
+        _check_shape(o, "o", (N, D), out_dtype, dev)
+    desc = scan_desc(N, 1, D, x.dtype, g.dtype, out_dtype, gate_mode, tied, _row_stride(x, "x"), _row_stride(g, "g"))
+    _call(lib().gdr_scan_step, "gdr_scan_step", dev, stream, desc, _ptr(x), _ptr(g), _ptr(h), _ptr(o))
+    return o
+
+
+def norm_desc(rows, D, x_dtype, y_dtype, w_dtype=torch.float32, eps=1e-5) -> NormDesc:
+    return NormDesc(rows, D, _dtype_code(x_dtype), _dtype_code(y_dtype), _dtype_code(w_dtype), float(eps))
+
+
+def _norm_weights(weight, bias, D, dev):
+    w_dtype = next((t.dtype for t in (weight, bias) if t is not None), torch.float32)
+    for t, n in ((weight, "weight"), (bias, "bias")):
+        if t is not None:
+            _check_shape(t, n, (D,), w_dtype, dev)
+    return w_dtype
+
+
+def layernorm_fwd(x, weight=None, bias=None, *, eps=1e-5, out_dtype=None, want_stats=True, stream=None):
+    """Layer norm over the last dimension (``gdr_layernorm_fwd``): x [..., D] bf16 or fp32, weight and
+    bias [D] (one dtype) or None.  Returns (y [..., D] out_dtype, mean [...], rstd [...] fp32); the
+    statistics are None unless want_stats."""
+    dev = _on_device(x, "x")
+    if x.dim() < 1:
+        raise ValueError("x must have at least one dimension")
+    _need(x, "x")
+    D = x.shape[-1]
+    out_dtype = out_dtype or x.dtype
+    w_dtype = _norm_weights(weight, bias, D, dev)
+    desc = norm_desc(x.numel() // max(D, 1), D, x.dtype, out_dtype, w_dtype, eps)
+    y = torch.empty(x.shape, dtype=out_dtype, device=dev)
+    mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=dev) if want_stats else None
+    rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=dev) if want_stats else None
+    _call(lib().gdr_layernorm_fwd, "gdr_layernorm_fwd", dev, stream, desc, _ptr(x), _ptr(weight), _ptr(bias), _ptr(y),
+          _ptr(mean), _ptr(rstd))
+    return y, mean, rstd
+
+
+def layernorm_bwd(x, dy, mean, rstd, weight=None, *, with_bias=True, want_dx=True, workspace=None, stream=None):
+    """Backward of ``layernorm_fwd`` given dy (like y) and the forward's mean and rstd.  Returns a dict
+    "x" (x's dtype; None unless want_dx), "weight" (fp32; None without weight) and "bias" (fp32; None
+    unless with_bias)."""
+    dev = _on_device(x, "x")
+    _need(x, "x")
+    D = x.shape[-1]
+    _check_shape(dy, "dy", tuple(x.shape), None, dev)
+    for t, n in ((mean, "mean"), (rstd, "rstd")):
+        _check_shape(t, n, tuple(x.shape[:-1]), torch.float32, dev)
+    w_dtype = _norm_weights(weight, None, D, dev)
+    desc = norm_desc(x.numel() // max(D, 1), D, x.dtype, dy.dtype, w_dtype, 0.0)
+    dx = torch.empty(x.shape, dtype=x.dtype, device=dev) if want_dx else None
+    dw = torch.empty(D, dtype=torch.float32, device=dev) if weight is not None else None
+    db = torch.empty(D, dtype=torch.float32, device=dev) if with_bias else None
+    need = int(lib().gdr_layernorm_bwd_workspace_bytes(desc, int(dw is not None), int(with_bias)))
+    if need and workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _call(lib().gdr_layernorm_bwd, "gdr_layernorm_bwd", dev, stream, desc, _ptr(x), _ptr(dy), _ptr(weight), _ptr(mean),
+          _ptr(rstd), _ptr(dx), _ptr(dw), _ptr(db), _ptr(workspace), ws_bytes)
+    return {"x": dx, "weight": dw, "bias": db}
+
+
+def beam_desc(G, K, V, M, x_dtype, row=0, eos=0) -> BeamDesc:
+    return BeamDesc(G, K, V, M, row, _dtype_code(x_dtype), int(eos))
+
+
+def beam_workspace_bytes(desc: BeamDesc) -> int:
+    return int(lib().gdr_beam_select_workspace_bytes(desc))
+
+
+def beam_select(logits, scores, n_out=None, *, finished=None, eos=0, workspace=None, stream=None):
+    """The n_out (default K) best of every group's K * V continuations (``gdr_beam_select``): logits
+    [G,K,V] bf16 or fp32 (rows may be slices of wider ones), scores [G,K] fp32 summed log
+    probabilities, finished [G,K] bool or None.  Returns (scores fp32, parent int32, token int32),
+    each [G, n_out], best first; parent is the beam within its group, as ``state_reorder`` takes it."""
+    dev = _on_device(logits, "logits")
+    if logits.dim() != 3:
+        raise ValueError("logits must be [G, K, V]")
+    G, K, V = logits.shape
+    M = K if n_out is None else int(n_out)
+    _check_shape(scores, "scores", (G, K), torch.float32, dev)
+    if finished is not None:
+        _check_shape(finished, "finished", (G, K), torch.bool, dev)
+    desc = beam_desc(G, K, V, M, logits.dtype, _row_stride(logits, "logits"), eos)
+    out = torch.empty((G, M), dtype=torch.float32, device=dev)
+    parent = torch.empty((G, M), dtype=torch.int32, device=dev)
+    token = torch.empty((G, M), dtype=torch.int32, device=dev)
+    need = beam_workspace_bytes(desc)
+    if need and workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _call(lib().gdr_beam_select, "gdr_beam_select", dev, stream, desc, _ptr(logits), _ptr(scores), _ptr(finished),
+          _ptr(out), _ptr(parent), _ptr(token), _ptr(workspace), ws_bytes)
+    return out, parent, token
+
+
+def state_reorder(S, parent, *, layers=False, stream=None):
+    """S[g * K + j] <- S[g * K + parent[g, j]] for every beam, in place (``gdr_state_reorder``).  S is
+    [G * K, ...] (decode_step's states, scan_step's, Raven's slots), or [L, G * K, ...] with layers;
+    parent [G,K] int32.  Returns S.  A parent outside 0 .. K - 1 keeps its beam's state and shows as
+    GDR_ERR_INDEX in query_device_status."""
+    dev = _on_device(S, "S")
+    _need(S, "S")
+    _need(parent, "parent", torch.int32, dev)
+    if parent.dim() != 2 or S.dim() < 1 + int(bool(layers)):
+        raise ValueError("parent must be [G, K] and S [G * K, ...] (layers: [L, G * K, ...])")
+    G, K = parent.shape
+    L = S.shape[0] if layers else 1
+    if S.shape[int(bool(layers))] != G * K:
+        raise ValueError(f"S must hold G * K = {G * K} states, got {S.shape[int(bool(layers))]}")
+    n = L * G * K
+    desc = ReorderDesc(L, G, K, S.numel() * S.element_size() // n if n else 0)
+    _call(lib().gdr_state_reorder, "gdr_state_reorder", dev, stream, desc, _ptr(S), _ptr(parent))
+    return S
+
+
 def query_device_status(stream=None) -> int:
-    """Synchronise and read/clear the device status word (GDR_OK or GDR_ERR_TIMEOUT)."""
+    """Synchronise and read/clear the device status word (GDR_OK, or what the kernels left there)."""
     dev = torch.device("cuda", torch.cuda.current_device())
     return int(lib().gdr_query_device_status(_stream_handle(stream, dev)))
