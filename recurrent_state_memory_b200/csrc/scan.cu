@@ -5,128 +5,61 @@
 #include "gdr.h"
 #include "host.cuh"
 #include "common.cuh"
+#include "scan.cuh"
 
 namespace gdr {
 namespace scn {
 
-struct ScanParams {
-    int B, T, D;
-    long long x_row, g_row;
-    int gate_mode, tied;
-    const void* x;
-    const void* g;
-    const float* h0;
-    const int* lengths;
-    void* h;
-    float* h_T;
-    float* ckpt;
-    const void* dh;
-    const float* dh_T;
-    void* dx;
-    void* dg;
-    float* dh0;
-};
-
-constexpr int CKPT = GDR_SCAN_CKPT;
-constexpr int NT = 64;
-
-__device__ __forceinline__ int seq_len(const ScanParams& p, int b) {
-    return p.lengths ? min(max(p.lengths[b], 0), p.T) : p.T;
-}
-
-// One thread per channel walks the sequence.
-template <typename XT, typename GT, typename OT>
-__global__ void __launch_bounds__(NT) scan_fwd_kernel(ScanParams p) {
-    const int c = blockIdx.x * NT + threadIdx.x, b = blockIdx.y;
-    if (c >= p.D) return;
-    const int len = seq_len(p, b), nck = (p.T + CKPT - 1) / CKPT;
-    const XT* x = static_cast<const XT*>(p.x) + (size_t)b * p.T * p.x_row + c;
-    const GT* g = static_cast<const GT*>(p.g) + (size_t)b * p.T * p.g_row + c;
-    OT* h = static_cast<OT*>(p.h) + (size_t)b * p.T * p.D + c;
-    float s = p.h0 ? p.h0[(size_t)b * p.D + c] : 0.f;
-    for (int t = 0; t < p.T; ++t) {
-        if (p.ckpt && t % CKPT == 0) p.ckpt[((size_t)b * nck + t / CKPT) * p.D + c] = s;
-        float out = 0.f;
-        if (t < len) {
-            float a, rest;
-            decay_pair(ld_f32(g + (size_t)t * p.g_row), p.gate_mode, a, rest);
-            const float xv = ld_f32(x + (size_t)t * p.x_row);
-            s = fmaf(a, s, p.tied ? rest * xv : xv);
-            out = s;
-        }
-        st_from_f32(h + (size_t)t * p.D, out);
-    }
-    if (p.h_T) p.h_T[(size_t)b * p.D + c] = s;
-}
-
-template <typename XT, typename GT, typename OT>
-__global__ void __launch_bounds__(NT) scan_bwd_kernel(ScanParams p) {
-    __shared__ float before[CKPT][NT];           // the states before the tokens of one piece
-    const int c = blockIdx.x * NT + threadIdx.x, b = blockIdx.y;
-    if (c >= p.D) return;
-    const int len = seq_len(p, b), nck = (p.T + CKPT - 1) / CKPT;
-    const XT* x = static_cast<const XT*>(p.x) + (size_t)b * p.T * p.x_row + c;
-    const GT* g = static_cast<const GT*>(p.g) + (size_t)b * p.T * p.g_row + c;
-    const OT* dh = p.dh ? static_cast<const OT*>(p.dh) + (size_t)b * p.T * p.D + c : nullptr;
-    XT* dx = static_cast<XT*>(p.dx) + (size_t)b * p.T * p.D + c;
-    GT* dg = static_cast<GT*>(p.dg) + (size_t)b * p.T * p.D + c;
-    float m = p.dh_T ? p.dh_T[(size_t)b * p.D + c] : 0.f;     // a_{t+1} lam_{t+1}
-    for (int j = nck - 1; j >= 0; --j) {
-        const int t0 = j * CKPT, t1 = min(t0 + CKPT, p.T);
-        float s = p.ckpt[((size_t)b * nck + j) * p.D + c];
-        for (int t = t0; t < min(t1, len); ++t) {
-            before[t - t0][threadIdx.x] = s;
-            float a, rest;
-            decay_pair(ld_f32(g + (size_t)t * p.g_row), p.gate_mode, a, rest);
-            const float xv = ld_f32(x + (size_t)t * p.x_row);
-            s = fmaf(a, s, p.tied ? rest * xv : xv);
-        }
-        for (int t = t1 - 1; t >= t0; --t) {
-            float ox = 0.f, og = 0.f;
-            if (t < len) {
-                float a, rest;
-                decay_pair(ld_f32(g + (size_t)t * p.g_row), p.gate_mode, a, rest);
-                const float xv = ld_f32(x + (size_t)t * p.x_row);
-                const float lam = m + (dh ? ld_f32(dh + (size_t)t * p.D) : 0.f);
-                ox = p.tied ? rest * lam : lam;
-                const float da = lam * (before[t - t0][threadIdx.x] - (p.tied ? xv : 0.f));
-                og = p.gate_mode == 1 ? -da * (a * rest) : da * a;
-                m = a * lam;
-            }
-            st_from_f32(dx + (size_t)t * p.D, ox);
-            st_from_f32(dg + (size_t)t * p.D, og);
-        }
-    }
-    if (p.dh0) p.dh0[(size_t)b * p.D + c] = m;
-}
-
-template <typename XT, typename GT, typename OT>
-__global__ void __launch_bounds__(256) scan_step_kernel(ScanParams p) {
-    const size_t n = (size_t)p.B * p.D;
-    for (size_t i = (size_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (size_t)gridDim.x * 256) {
-        const size_t b = i / p.D, c = i % p.D;
-        float a, rest;
-        decay_pair(ld_f32(static_cast<const GT*>(p.g) + b * p.g_row + c), p.gate_mode, a, rest);
-        const float xv = ld_f32(static_cast<const XT*>(p.x) + b * p.x_row + c);
-        const float s = fmaf(a, p.h_T[i], p.tied ? rest * xv : xv);
-        p.h_T[i] = s;
-        if (p.h) st_from_f32(static_cast<OT*>(p.h) + i, s);
-    }
-}
-
 enum Pass { FWD, BWD, STEP };
 
+// Blocks of a cluster (along the tokens): enough that the grid has about two blocks per SM, as far as
+// the sequence has tiles for them.
+static int cluster_of(long long tiles, int T, int tok, int sms) {
+    int n = 1;
+    while (n < MAX_CLUSTER && tiles * n * 2 <= 2LL * sms && n * tok < T) n *= 2;
+    return n;
+}
+
+template <typename KERN>
+static gdr_status launch_clusters(KERN kern, const ScanParams& p, int tok, size_t smem, cudaStream_t st) {
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(scan)");
+    const unsigned ct = (unsigned)((p.D + CH - 1) / CH);
+    const int ncl = cluster_of((long long)ct * p.B, p.T, tok, device_sm_count());
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(ncl, ct, p.B);
+    cfg.blockDim = dim3(NT);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = ncl; at[0].val.clusterDim.y = 1; at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, kern, p);
+    return e == cudaSuccess ? GDR_OK : cuda_fail(e, "launch(scan)");
+}
+
+template <typename XT, typename GT, typename OT, int V>
+static gdr_status launch_v(Pass pass, const ScanParams& p, cudaStream_t st) {
+    if (pass == FWD)
+        return launch_clusters(scan_fwd_kernel<XT, GT, OT, V>, p, Tile<V, FWD_ELEMS>::TOK, sizeof(FwdSmem<XT, GT, V>), st);
+    if (pass == BWD)
+        return launch_clusters(scan_bwd_kernel<XT, GT, OT, V>, p, Tile<V, BWD_ELEMS>::TOK, sizeof(BwdSmem<XT, GT, OT, V>), st);
+    const size_t blocks = ((size_t)p.B * (p.D / V) + NT - 1) / NT, cap = (size_t)device_sm_count() * 8;
+    scan_step_kernel<XT, GT, OT, V><<<(unsigned)(blocks < cap ? blocks : cap), NT, 0, st>>>(p);
+    const cudaError_t e = cudaGetLastError();
+    return e == cudaSuccess ? GDR_OK : cuda_fail(e, "launch(scan step)");
+}
+
+// Four channels per thread where every row of every tensor is aligned to four elements, else one.
 template <typename XT, typename GT, typename OT>
 static gdr_status launch(Pass pass, const ScanParams& p, cudaStream_t st) {
-    const dim3 grid((p.D + NT - 1) / NT, p.B);
-    if (pass == FWD) scan_fwd_kernel<XT, GT, OT><<<grid, NT, 0, st>>>(p);
-    else if (pass == BWD) scan_bwd_kernel<XT, GT, OT><<<grid, NT, 0, st>>>(p);
-    else {
-        const size_t blocks = ((size_t)p.B * p.D + 255) / 256, cap = (size_t)device_sm_count() * 8;
-        scan_step_kernel<XT, GT, OT><<<(unsigned)(blocks < cap ? blocks : cap), 256, 0, st>>>(p);
-    }
-    const cudaError_t e = cudaGetLastError();
-    return e == cudaSuccess ? GDR_OK : cuda_fail(e, "launch(scan)");
+    auto fits = [](const void* q, long long row, size_t el) {
+        return reinterpret_cast<uintptr_t>(q) % (4 * el) == 0 && row % 4 == 0;
+    };
+    const bool vec = p.D % 4 == 0 && fits(p.x, p.x_row, sizeof(XT)) && fits(p.g, p.g_row, sizeof(GT));
+    return vec ? launch_v<XT, GT, OT, 4>(pass, p, st) : launch_v<XT, GT, OT, 1>(pass, p, st);
 }
 
 template <typename XT, typename GT>
@@ -151,7 +84,8 @@ static gdr_status check_desc(const gdr_scan_desc* d) {
     if (d->tied != 0 && d->tied != 1) return fail(GDR_ERR_INVALID_ARG, "tied must be 0 or 1%s");
     if ((d->x_row != 0 && d->x_row < d->D) || (d->g_row != 0 && d->g_row < d->D))
         return fail(GDR_ERR_INVALID_ARG, "x_row and g_row must be 0 or at least D%s");
-    if (d->B > 65535) return fail(GDR_ERR_UNSUPPORTED, "B must be at most 65535%s");
+    if (d->B > 65535 || d->T > (1 << 30) || d->D > 65535 * CH)
+        return fail(GDR_ERR_UNSUPPORTED, "B must be at most 65535, T 2^30, D 4194240%s");
     return GDR_OK;
 }
 

@@ -1,0 +1,514 @@
+// scan.cuh -- kernels of the per-channel gated linear recurrence h_t = a_t h_{t-1} + b_t.
+//
+// Mathematics.  A run of tokens maps the state before it to the state after it by s -> A s + H,
+// with A the product of its decays and H its end state from zero; two neighbouring runs compose
+// to (A2 A1, A2 H1 + H2).  So a tile of tokens is cut into short runs, one per thread; each
+// thread forms its run's (A, H) in registers, the runs' start states come from composing what
+// lies before them, and a second sweep over the same registers gives every h_t.  x and g are
+// read once.  The backward adds the state's gradient, which runs the same way from the end:
+// mu_t = a_t (dh_t + mu_{t+1}), with the same A and an M in place of H.
+//
+// Bound: HBM (a forward moves 6 to 12 bytes per element for about 20 instructions).
+//
+// Split.  A block of 8 warps owns 64 channels x TOK tokens per turn; a cluster of up to 8 blocks
+// takes that many neighbouring tiles of the same channels and walks the sequence in turns, so
+// that few channels with long sequences still fill the GPU.  Per turn the blocks exchange their
+// tiles' (A, H) through distributed shared memory and one cluster barrier; every block then
+// folds them in the same order, so the result does not depend on timing, and there is neither a
+// workspace nor a wait on another block outside the cluster's barrier.  The next turns' inputs
+// are copied to shared memory (cp.async; each thread copies and reads its own slots, so the
+// copies need no barrier) while the current turn is computed.
+#pragma once
+
+#include "common.cuh"
+
+namespace gdr {
+namespace scn {
+
+struct ScanParams {
+    int B, T, D;
+    long long x_row, g_row;
+    int gate_mode, tied;
+    const void* x;
+    const void* g;
+    const float* h0;
+    const int* lengths;
+    void* h;
+    float* h_T;
+    float* ckpt;
+    const void* dh;
+    const float* dh_T;
+    void* dx;
+    void* dg;
+    float* dh0;
+};
+
+constexpr int CKPT = GDR_SCAN_CKPT;
+constexpr int NT = 256;
+constexpr int CH = 64;                  // channels of a block
+constexpr int WT = 4;                   // warps along the tokens (2 along the channels)
+constexpr int MAX_CLUSTER = 8;
+constexpr int STAGES = 2;
+
+__device__ __forceinline__ int seq_len(const ScanParams& p, int b) {
+    return p.lengths ? min(max(p.lengths[b], 0), p.T) : p.T;
+}
+
+__device__ __forceinline__ uint32_t smem_addr(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
+
+// Copy N bytes (8 or 16) to shared memory, or fill them with zero.
+template <int N> __device__ __forceinline__ void copy_async(void* dst, const void* src, bool on) {
+    static_assert(N == 8 || N == 16, "bytes");
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(smem_addr(dst)), "l"(src), "n"(N), "r"(on ? N : 0)
+                 : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+__device__ __forceinline__ uint32_t cluster_rank() { uint32_t r; asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r)); return r; }
+__device__ __forceinline__ uint32_t cluster_size() { uint32_t r; asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r)); return r; }
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// Store to the same shared-memory place of block `rank` of the cluster.
+__device__ __forceinline__ void store_peer(float2* p, float2 v, uint32_t rank) {
+    uint32_t a;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_addr(p)), "r"(rank));
+    asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(a), "f"(v.x), "f"(v.y) : "memory");
+}
+
+// V values of one thread as stored: loads from global or shared memory, and the rounding store.
+template <typename T, int V> struct Pack;
+template <> struct Pack<float, 4> {
+    using Raw = float4;
+    static __device__ __forceinline__ void get(const Raw& r, float (&v)[4]) { v[0] = r.x; v[1] = r.y; v[2] = r.z; v[3] = r.w; }
+    static __device__ __forceinline__ Raw put(const float (&v)[4]) { return make_float4(v[0], v[1], v[2], v[3]); }
+};
+template <> struct Pack<__nv_bfloat16, 4> {
+    using Raw = uint2;
+    static __device__ __forceinline__ void get(const Raw& r, float (&v)[4]) {
+        v[0] = __uint_as_float(r.x << 16); v[1] = __uint_as_float(r.x & 0xffff0000u);
+        v[2] = __uint_as_float(r.y << 16); v[3] = __uint_as_float(r.y & 0xffff0000u);
+    }
+    static __device__ __forceinline__ Raw put(const float (&v)[4]) {
+        const __nv_bfloat162 a = __floats2bfloat162_rn(v[0], v[1]), b = __floats2bfloat162_rn(v[2], v[3]);
+        return make_uint2(*reinterpret_cast<const unsigned*>(&a), *reinterpret_cast<const unsigned*>(&b));
+    }
+};
+template <typename T> struct Pack<T, 1> {
+    using Raw = T;
+    static __device__ __forceinline__ void get(const Raw& r, float (&v)[1]) { v[0] = ld_f32(&r); }
+    static __device__ __forceinline__ Raw put(const float (&v)[1]) { Raw r; st_from_f32(&r, v[0]); return r; }
+};
+
+// How a block's threads lie over its tile.  V = 4: 8 lanes x 4 channels and 4 runs per warp
+// (vector access: rows and pointers aligned to 4 elements); V = 1: 32 lanes x 1 channel.
+template <int V, int ELEMS> struct Tile {
+    static constexpr int LC = 32 / V;           // lanes along the channels
+    static constexpr int TL = 32 / LC;          // runs in a warp
+    static constexpr int R = ELEMS / V;         // tokens of a run
+    static constexpr int TOK = WT * TL * R;     // tokens of a block
+    int lane_t, warp_t, c;                      // run in the warp, warp along the tokens, first channel in the block
+    __device__ __forceinline__ Tile() {
+        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+        lane_t = lane / LC;
+        warp_t = warp & (WT - 1);
+        c = (warp / WT) * 32 + (lane % LC) * V;
+    }
+    __device__ __forceinline__ int first_token() const { return (warp_t * TL + lane_t) * R; }
+};
+
+// Compose a warp's runs: in (A, H) of this thread's run; out the composition of the runs before
+// it (ex_*) and, in the warp's last run's lanes, of all of them (A, H).  UP = false: from the end.
+template <int V, int LC, int TL, bool UP>
+__device__ __forceinline__ void warp_runs(float (&A)[V], float (&H)[V], float (&exA)[V], float (&exH)[V], int lane_t) {
+    const int at = UP ? lane_t : TL - 1 - lane_t;
+#pragma unroll
+    for (int o = 1; o < TL; o <<= 1) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const float a = UP ? __shfl_up_sync(0xffffffffu, A[i], o * LC) : __shfl_down_sync(0xffffffffu, A[i], o * LC);
+            const float h = UP ? __shfl_up_sync(0xffffffffu, H[i], o * LC) : __shfl_down_sync(0xffffffffu, H[i], o * LC);
+            if (at >= o) { H[i] = fmaf(A[i], h, H[i]); A[i] *= a; }
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        if constexpr (TL > 1) {
+            const float a = UP ? __shfl_up_sync(0xffffffffu, A[i], LC) : __shfl_down_sync(0xffffffffu, A[i], LC);
+            const float h = UP ? __shfl_up_sync(0xffffffffu, H[i], LC) : __shfl_down_sync(0xffffffffu, H[i], LC);
+            exA[i] = at > 0 ? a : 1.f;
+            exH[i] = at > 0 ? h : 0.f;
+        } else {
+            exA[i] = 1.f; exH[i] = 0.f;
+        }
+    }
+}
+
+// The start of this block's tile along the scan's direction.  agg: the block's warps' (A, H);
+// xch: the cluster's blocks' (A, H), this turn's; carry: the state at the cluster's turn start,
+// held by the first CH threads of every block alike, moved on by the turn.  Leaves the tile's start
+// state in start[CH] and synchronises the block (which must have synchronised after writing agg).
+template <bool UP>
+__device__ __forceinline__ void tile_start(const float2 (*agg)[CH], float2 (*xch)[CH], float* start, float& carry,
+                                           int rank, int ncl) {
+    const int c = threadIdx.x & (CH - 1), q = threadIdx.x / CH;
+    float A = 1.f, H = 0.f;
+#pragma unroll
+    for (int w = 0; w < WT; ++w) {
+        const float2 e = agg[UP ? w : WT - 1 - w][c];
+        H = fmaf(e.x, H, e.y);
+        A *= e.x;
+    }
+    if (ncl > 1) {
+        for (int r = q; r < ncl; r += NT / CH) store_peer(&xch[rank][c], make_float2(A, H), r);
+        cluster_sync();
+    }
+    if (q == 0) {
+        float s = carry;
+        if (ncl > 1) {
+            for (int i = 0; i < ncl; ++i) {
+                const int r = UP ? i : ncl - 1 - i;
+                if (r == rank) start[c] = s;
+                const float2 e = xch[r][c];
+                s = fmaf(e.x, s, e.y);
+            }
+        } else {
+            start[c] = s;
+            s = fmaf(A, s, H);
+        }
+        carry = s;
+    }
+    __syncthreads();
+}
+
+// The state before this thread's run: the tile's start through the warps before it and the
+// runs before it in its warp.
+template <int V, bool UP>
+__device__ __forceinline__ void run_start(const float2 (*agg)[CH], const float* start, const float (&exA)[V],
+                                          const float (&exH)[V], int warp_t, int c, float (&s)[V]) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) s[i] = start[c + i];
+#pragma unroll
+    for (int w = 0; w < WT - 1; ++w) {
+        const int at = UP ? w : WT - 1 - w;
+        if (UP ? at < warp_t : at > warp_t) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) { const float2 e = agg[at][c + i]; s[i] = fmaf(e.x, s[i], e.y); }
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) s[i] = fmaf(exA[i], s[i], exH[i]);
+}
+
+constexpr int FWD_ELEMS = 32;           // elements of a thread: 2 registers each (decay, input)
+constexpr int BWD_ELEMS = 16;           // 5 registers each
+
+template <typename XT, typename GT, int V> struct FwdSmem {
+    static constexpr int R = FWD_ELEMS / V;
+    typename Pack<GT, V>::Raw g[V > 1 ? STAGES : 1][V > 1 ? R : 1][V > 1 ? NT : 1];
+    typename Pack<XT, V>::Raw x[V > 1 ? STAGES : 1][V > 1 ? R : 1][V > 1 ? NT : 1];
+    float2 agg[2][WT][CH];
+    float2 xch[2][MAX_CLUSTER][CH];
+    float start[CH];
+};
+
+template <typename XT, typename GT, typename OT, int V>
+__global__ void __launch_bounds__(NT, 2) scan_fwd_kernel(ScanParams p) {
+    using L = Tile<V, FWD_ELEMS>;
+    using S = FwdSmem<XT, GT, V>;
+    constexpr int R = L::R;
+    extern __shared__ __align__(16) unsigned char raw[];
+    S& sm = *reinterpret_cast<S*>(raw);
+    const L l;
+    const int rank = (int)cluster_rank(), ncl = (int)cluster_size();
+    const int b = blockIdx.z, c0 = blockIdx.y * CH, c = c0 + l.c;
+    const bool on = c < p.D;                              // V divides D, or V = 1
+    const int len = seq_len(p, b), nck = (p.T + CKPT - 1) / CKPT;
+    const XT* x = static_cast<const XT*>(p.x) + (size_t)b * p.T * p.x_row + c;
+    const GT* g = static_cast<const GT*>(p.g) + (size_t)b * p.T * p.g_row + c;
+    OT* h = static_cast<OT*>(p.h) + (size_t)b * p.T * p.D + c;
+    const int turn = L::TOK * ncl, turns = (p.T + turn - 1) / turn;
+    const int first = rank * L::TOK + l.first_token();    // this thread's run in turn 0
+
+    auto fetch = [&](int k) {                             // turn k's inputs of this thread
+        if constexpr (V > 1) {
+            if (k < turns) {
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
+                    const int t = k * turn + first + r;
+                    const bool in = on && t < len;
+                    copy_async<sizeof(typename Pack<GT, V>::Raw)>(&sm.g[k % STAGES][r][threadIdx.x],
+                                                                  in ? g + (size_t)t * p.g_row : p.g, in);
+                    copy_async<sizeof(typename Pack<XT, V>::Raw)>(&sm.x[k % STAGES][r][threadIdx.x],
+                                                                  in ? x + (size_t)t * p.x_row : p.x, in);
+                }
+            }
+            copy_commit();
+        }
+    };
+#pragma unroll
+    for (int k = 0; k < STAGES; ++k) fetch(k);
+
+    float carry = 0.f;
+    if (threadIdx.x < CH && c0 + (int)threadIdx.x < p.D && p.h0) carry = p.h0[(size_t)b * p.D + c0 + threadIdx.x];
+
+    if (ncl > 1) cluster_sync();                          // the peers' shared memory exists
+    for (int k = 0; k < turns; ++k) {
+        const int t0 = k * turn + first;
+        float a[R][V], bb[R][V], A[V], H[V], exA[V], exH[V];
+        if constexpr (V > 1) {
+            copy_wait<STAGES - 1>();
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                Pack<GT, V>::get(sm.g[k % STAGES][r][threadIdx.x], a[r]);
+                Pack<XT, V>::get(sm.x[k % STAGES][r][threadIdx.x], bb[r]);
+            }
+        } else {
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                const bool in = on && t0 + r < len;
+                a[r][0] = in ? ld_f32(g + (size_t)(t0 + r) * p.g_row) : 0.f;
+                bb[r][0] = in ? ld_f32(x + (size_t)(t0 + r) * p.x_row) : 0.f;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < V; ++i) { A[i] = 1.f; H[i] = 0.f; }
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const bool in = t0 + r < len;
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                float dec, rest;
+                decay_pair(a[r][i], p.gate_mode, dec, rest);
+                bb[r][i] = in ? (p.tied ? rest * bb[r][i] : bb[r][i]) : 0.f;
+                a[r][i] = in ? dec : 1.f;
+                H[i] = fmaf(a[r][i], H[i], bb[r][i]);
+                A[i] *= a[r][i];
+            }
+        }
+        warp_runs<V, L::LC, L::TL, true>(A, H, exA, exH, l.lane_t);
+        float2 (*agg)[CH] = sm.agg[k & 1];
+        if (l.lane_t == L::TL - 1) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) agg[l.warp_t][l.c + i] = make_float2(A[i], H[i]);
+        }
+        __syncthreads();
+        fetch(k + STAGES);                                // the slots of turn k are in registers
+        tile_start<true>(agg, sm.xch[k & 1], sm.start, carry, rank, ncl);
+        float s[V];
+        run_start<V, true>(agg, sm.start, exA, exH, l.warp_t, l.c, s);
+        if (on && p.ckpt && t0 % CKPT == 0 && t0 < p.T) {
+            float* ck = p.ckpt + ((size_t)b * nck + t0 / CKPT) * p.D + c;
+            if (GDR_INB(t0 / CKPT < nck && c + V <= p.D, 801)) {
+                if constexpr (V == 4) *reinterpret_cast<float4*>(ck) = make_float4(s[0], s[1], s[2], s[3]);
+                else ck[0] = s[0];
+            }
+        }
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const int t = t0 + r;
+            float o[V];
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                s[i] = fmaf(a[r][i], s[i], bb[r][i]);
+                o[i] = t < len ? s[i] : 0.f;
+            }
+            if (on && t < p.T && GDR_INB(c + V <= p.D, 802))
+                *reinterpret_cast<typename Pack<OT, V>::Raw*>(h + (size_t)t * p.D) = Pack<OT, V>::put(o);
+        }
+    }
+    if (p.h_T && rank == 0 && threadIdx.x < CH && c0 + (int)threadIdx.x < p.D)
+        p.h_T[(size_t)b * p.D + c0 + threadIdx.x] = carry;
+}
+
+template <typename XT, typename GT, typename OT, int V> struct BwdSmem {
+    static constexpr int R = BWD_ELEMS / V;
+    typename Pack<GT, V>::Raw g[V > 1 ? STAGES : 1][V > 1 ? R : 1][V > 1 ? NT : 1];
+    typename Pack<XT, V>::Raw x[V > 1 ? STAGES : 1][V > 1 ? R : 1][V > 1 ? NT : 1];
+    typename Pack<OT, V>::Raw dh[V > 1 ? STAGES : 1][V > 1 ? R : 1][V > 1 ? NT : 1];
+    float ck[STAGES][CH];
+    float2 up[2][WT][CH];
+    float2 down[2][WT][CH];
+    float2 xch[2][MAX_CLUSTER][CH];
+    float start[CH];
+};
+
+// The states inside a tile come from its checkpoint (a block's tile is CKPT tokens), so only the
+// gradient's direction goes through the cluster.
+template <typename XT, typename GT, typename OT, int V>
+__global__ void __launch_bounds__(NT, 2) scan_bwd_kernel(ScanParams p) {
+    using L = Tile<V, BWD_ELEMS>;
+    using S = BwdSmem<XT, GT, OT, V>;
+    constexpr int R = L::R;
+    static_assert(L::TOK == CKPT, "a tile starts at a checkpoint");
+    extern __shared__ __align__(16) unsigned char raw[];
+    S& sm = *reinterpret_cast<S*>(raw);
+    const L l;
+    const int rank = (int)cluster_rank(), ncl = (int)cluster_size();
+    const int b = blockIdx.z, c0 = blockIdx.y * CH, c = c0 + l.c;
+    const bool on = c < p.D;
+    const int len = seq_len(p, b), nck = (p.T + CKPT - 1) / CKPT;
+    const XT* x = static_cast<const XT*>(p.x) + (size_t)b * p.T * p.x_row + c;
+    const GT* g = static_cast<const GT*>(p.g) + (size_t)b * p.T * p.g_row + c;
+    const OT* dh = static_cast<const OT*>(p.dh) + (size_t)b * p.T * p.D + c;
+    XT* dx = static_cast<XT*>(p.dx) + (size_t)b * p.T * p.D + c;
+    GT* dg = static_cast<GT*>(p.dg) + (size_t)b * p.T * p.D + c;
+    const int turn = L::TOK * ncl, turns = (p.T + turn - 1) / turn;
+    const int first = rank * L::TOK + l.first_token();
+    const bool with_dh = p.dh != nullptr;
+
+    // turn k walks from the end: its tokens start at (turns - 1 - k) * turn
+    auto fetch = [&](int k) {
+        if (k < turns) {
+            const int base = (turns - 1 - k) * turn;
+            if constexpr (V > 1) {
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
+                    const int t = base + first + r;
+                    const bool in = on && t < len;
+                    copy_async<sizeof(typename Pack<GT, V>::Raw)>(&sm.g[k % STAGES][r][threadIdx.x],
+                                                                  in ? g + (size_t)t * p.g_row : p.g, in);
+                    copy_async<sizeof(typename Pack<XT, V>::Raw)>(&sm.x[k % STAGES][r][threadIdx.x],
+                                                                  in ? x + (size_t)t * p.x_row : p.x, in);
+                    copy_async<sizeof(typename Pack<OT, V>::Raw)>(&sm.dh[k % STAGES][r][threadIdx.x],
+                                                                  in && with_dh ? (const void*)(dh + (size_t)t * p.D) : p.ckpt,
+                                                                  in && with_dh);
+                }
+            }
+            // the tile's checkpoint; read behind the turn's first barrier
+            const int j = base / CKPT + rank;
+            if constexpr (V > 1) {
+                if (threadIdx.x < CH / 4) {
+                    const bool in = j < nck && c0 + (int)threadIdx.x * 4 < p.D;
+                    copy_async<16>(&sm.ck[k % STAGES][threadIdx.x * 4],
+                                   in ? p.ckpt + ((size_t)b * nck + j) * p.D + c0 + threadIdx.x * 4 : p.ckpt, in);
+                }
+            } else if (threadIdx.x < CH) {
+                const bool in = j < nck && c0 + (int)threadIdx.x < p.D;
+                sm.ck[k % STAGES][threadIdx.x] = in ? p.ckpt[((size_t)b * nck + j) * p.D + c0 + threadIdx.x] : 0.f;
+            }
+        }
+        if constexpr (V > 1) copy_commit();
+    };
+#pragma unroll
+    for (int k = 0; k < STAGES; ++k) fetch(k);
+
+    float carry = 0.f;
+    if (threadIdx.x < CH && c0 + (int)threadIdx.x < p.D && p.dh_T) carry = p.dh_T[(size_t)b * p.D + c0 + threadIdx.x];
+
+    if (ncl > 1) cluster_sync();                          // the peers' shared memory exists
+    for (int k = 0; k < turns; ++k) {
+        const int t0 = (turns - 1 - k) * turn + first;
+        float a[R][V], rest[R][V], xv[R][V], d[R][V];
+        if constexpr (V > 1) {
+            copy_wait<STAGES - 1>();
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                Pack<GT, V>::get(sm.g[k % STAGES][r][threadIdx.x], a[r]);
+                Pack<XT, V>::get(sm.x[k % STAGES][r][threadIdx.x], xv[r]);
+                Pack<OT, V>::get(sm.dh[k % STAGES][r][threadIdx.x], d[r]);
+            }
+        } else {
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                const bool in = on && t0 + r < len;
+                a[r][0] = in ? ld_f32(g + (size_t)(t0 + r) * p.g_row) : 0.f;
+                xv[r][0] = in ? ld_f32(x + (size_t)(t0 + r) * p.x_row) : 0.f;
+                d[r][0] = in && with_dh ? ld_f32(dh + (size_t)(t0 + r) * p.D) : 0.f;
+            }
+        }
+        float A[V], H[V], M[V], dA[V], exA[V], exH[V], exD[V], exM[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) { A[i] = 1.f; H[i] = 0.f; M[i] = 0.f; }
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const bool in = t0 + r < len;
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                decay_pair(a[r][i], p.gate_mode, a[r][i], rest[r][i]);
+                if (!in) { a[r][i] = 1.f; rest[r][i] = 0.f; }
+                H[i] = fmaf(a[r][i], H[i], in ? (p.tied ? rest[r][i] * xv[r][i] : xv[r][i]) : 0.f);
+                A[i] *= a[r][i];
+            }
+        }
+#pragma unroll
+        for (int r = R - 1; r >= 0; --r) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) M[i] = a[r][i] * (d[r][i] + M[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < V; ++i) dA[i] = A[i];
+        warp_runs<V, L::LC, L::TL, true>(A, H, exA, exH, l.lane_t);
+        warp_runs<V, L::LC, L::TL, false>(dA, M, exD, exM, l.lane_t);
+        if (l.lane_t == L::TL - 1) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) sm.up[k & 1][l.warp_t][l.c + i] = make_float2(A[i], H[i]);
+        }
+        if (l.lane_t == 0) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) sm.down[k & 1][l.warp_t][l.c + i] = make_float2(dA[i], M[i]);
+        }
+        __syncthreads();
+        float s[V], m[V], before[R][V];
+        run_start<V, true>(sm.up[k & 1], sm.ck[k % STAGES], exA, exH, l.warp_t, l.c, s);
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const bool in = t0 + r < len;
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                before[r][i] = s[i];
+                s[i] = fmaf(a[r][i], s[i], in ? (p.tied ? rest[r][i] * xv[r][i] : xv[r][i]) : 0.f);
+            }
+        }
+        tile_start<false>(sm.down[k & 1], sm.xch[k & 1], sm.start, carry, rank, ncl);
+        fetch(k + STAGES);                                // behind the barrier: the checkpoint's slot is read
+        run_start<V, false>(sm.down[k & 1], sm.start, exD, exM, l.warp_t, l.c, m);
+#pragma unroll
+        for (int r = R - 1; r >= 0; --r) {
+            const int t = t0 + r;
+            float ox[V], og[V];
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const float lam = d[r][i] + m[i];
+                const float da = lam * (p.tied ? before[r][i] - xv[r][i] : before[r][i]);
+                ox[i] = t < len ? (p.tied ? rest[r][i] * lam : lam) : 0.f;
+                og[i] = t < len ? (p.gate_mode == 1 ? -da * (a[r][i] * rest[r][i]) : da * a[r][i]) : 0.f;
+                m[i] = a[r][i] * lam;
+            }
+            if (on && t < p.T && GDR_INB(c + V <= p.D, 811)) {
+                *reinterpret_cast<typename Pack<XT, V>::Raw*>(dx + (size_t)t * p.D) = Pack<XT, V>::put(ox);
+                *reinterpret_cast<typename Pack<GT, V>::Raw*>(dg + (size_t)t * p.D) = Pack<GT, V>::put(og);
+            }
+        }
+    }
+    if (p.dh0 && rank == 0 && threadIdx.x < CH && c0 + (int)threadIdx.x < p.D)
+        p.dh0[(size_t)b * p.D + c0 + threadIdx.x] = carry;
+}
+
+// One token per sequence: elementwise, V channels per thread.
+template <typename XT, typename GT, typename OT, int V>
+__global__ void __launch_bounds__(NT) scan_step_kernel(ScanParams p) {
+    const int per = p.D / V;                              // V divides D
+    const size_t n = (size_t)p.B * per;
+    for (size_t i = (size_t)blockIdx.x * NT + threadIdx.x; i < n; i += (size_t)gridDim.x * NT) {
+        const size_t b = i / per, c = (i % per) * V;
+        float a[V], x[V], s[V];
+        Pack<GT, V>::get(*reinterpret_cast<const typename Pack<GT, V>::Raw*>(static_cast<const GT*>(p.g) + b * p.g_row + c), a);
+        Pack<XT, V>::get(*reinterpret_cast<const typename Pack<XT, V>::Raw*>(static_cast<const XT*>(p.x) + b * p.x_row + c), x);
+        typename Pack<float, V>::Raw* h = reinterpret_cast<typename Pack<float, V>::Raw*>(p.h_T + b * p.D + c);
+        if (!GDR_INB(b < (size_t)p.B && c + V <= (size_t)p.D, 821)) break;
+        Pack<float, V>::get(*h, s);
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            float dec, rest;
+            decay_pair(a[j], p.gate_mode, dec, rest);
+            s[j] = fmaf(dec, s[j], p.tied ? rest * x[j] : x[j]);
+        }
+        *h = Pack<float, V>::put(s);
+        if (p.h) *reinterpret_cast<typename Pack<OT, V>::Raw*>(static_cast<OT*>(p.h) + b * p.D + c) = Pack<OT, V>::put(s);
+    }
+}
+
+}  // namespace scn
+}  // namespace gdr
