@@ -22,10 +22,12 @@ static int cluster_of(long long tiles, int T, int tok, int sms) {
 
 template <typename KERN>
 static gdr_status launch_clusters(KERN kern, const ScanParams& p, int tok, size_t smem, cudaStream_t st) {
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(scan)");
     const unsigned ct = (unsigned)((p.D + CH - 1) / CH);
     const int ncl = cluster_of((long long)ct * p.B, p.T, tok, device_sm_count());
+    smem += (size_t)(2 * ncl - 1) * CH * sizeof(float2);
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e == cudaSuccess && ncl > 8) e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(scan)");
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(ncl, ct, p.B);
     cfg.blockDim = dim3(NT);

@@ -10,7 +10,7 @@
 //
 // Bound: HBM (a forward moves 6 to 12 bytes per element for about 20 instructions).
 //
-// Split.  A block of 8 warps owns 64 channels x TOK tokens per turn; a cluster of up to 8 blocks
+// Split.  A block of 8 warps owns 64 channels x TOK tokens per turn; a cluster of up to 16 blocks
 // takes that many neighbouring tiles of the same channels and walks the sequence in turns, so
 // that few channels with long sequences still fill the GPU.  Per turn the blocks exchange their
 // tiles' (A, H) through distributed shared memory and one cluster barrier; every block then
@@ -19,6 +19,8 @@
 // are copied to shared memory (cp.async; each thread copies and reads its own slots, so the
 // copies need no barrier) while the current turn is computed.
 #pragma once
+
+#include <type_traits>
 
 #include "common.cuh"
 
@@ -47,11 +49,21 @@ constexpr int CKPT = GDR_SCAN_CKPT;
 constexpr int NT = 256;
 constexpr int CH = 64;                  // channels of a block
 constexpr int WT = 4;                   // warps along the tokens (2 along the channels)
-constexpr int MAX_CLUSTER = 8;
+constexpr int MAX_CLUSTER = 16;
 constexpr int STAGES = 2;
 
 __device__ __forceinline__ int seq_len(const ScanParams& p, int b) {
     return p.lengths ? min(max(p.lengths[b], 0), p.T) : p.T;
+}
+
+// f(mode, tied) with the call's gate mode and form as compile-time constants: the branch is taken
+// once per sweep instead of once per element.
+template <typename F> __device__ __forceinline__ void with_mode(const ScanParams& p, F f) {
+    if (p.gate_mode == 1) {
+        if (p.tied) f(std::integral_constant<int, 1>(), std::true_type()); else f(std::integral_constant<int, 1>(), std::false_type());
+    } else {
+        if (p.tied) f(std::integral_constant<int, 0>(), std::true_type()); else f(std::integral_constant<int, 0>(), std::false_type());
+    }
 }
 
 __device__ __forceinline__ uint32_t smem_addr(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
@@ -209,8 +221,8 @@ template <typename XT, typename GT, int V> struct FwdSmem {
     typename Pack<GT, V>::Raw g[V > 1 ? STAGES : 1][V > 1 ? R : 1][V > 1 ? NT : 1];
     typename Pack<XT, V>::Raw x[V > 1 ? STAGES : 1][V > 1 ? R : 1][V > 1 ? NT : 1];
     float2 agg[2][WT][CH];
-    float2 xch[2][MAX_CLUSTER][CH];
     float start[CH];
+    float2 xch[1][CH];                  // [2][cluster][CH]: the launch adds the rest
 };
 
 template <typename XT, typename GT, typename OT, int V>
@@ -272,17 +284,32 @@ __global__ void __launch_bounds__(NT, 2) scan_fwd_kernel(ScanParams p) {
                 bb[r][0] = in ? ld_f32(x + (size_t)(t0 + r) * p.x_row) : 0.f;
             }
         }
+        with_mode(p, [&](auto mode, auto tied) {
 #pragma unroll
-        for (int i = 0; i < V; ++i) { A[i] = 1.f; H[i] = 0.f; }
+            for (int r = 0; r < R; ++r) {
 #pragma unroll
-        for (int r = 0; r < R; ++r) {
-            const bool in = t0 + r < len;
+                for (int i = 0; i < V; ++i) {
+                    float rest = 1.f;
+                    decay_pair<mode.value, tied.value>(a[r][i], a[r][i], rest);
+                    if (tied.value) bb[r][i] *= rest;
+                }
+            }
+        });
+        const bool whole = t0 + R <= len;
+        if (!whole) {                                     // tokens behind the end keep the state
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+#pragma unroll
+                for (int i = 0; i < V; ++i)
+                    if (t0 + r >= len) { a[r][i] = 1.f; bb[r][i] = 0.f; }
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < V; ++i) { A[i] = a[0][i]; H[i] = bb[0][i]; }
+#pragma unroll
+        for (int r = 1; r < R; ++r) {
 #pragma unroll
             for (int i = 0; i < V; ++i) {
-                float dec, rest;
-                decay_pair(a[r][i], p.gate_mode, dec, rest);
-                bb[r][i] = in ? (p.tied ? rest * bb[r][i] : bb[r][i]) : 0.f;
-                a[r][i] = in ? dec : 1.f;
                 H[i] = fmaf(a[r][i], H[i], bb[r][i]);
                 A[i] *= a[r][i];
             }
@@ -295,7 +322,7 @@ __global__ void __launch_bounds__(NT, 2) scan_fwd_kernel(ScanParams p) {
         }
         __syncthreads();
         fetch(k + STAGES);                                // the slots of turn k are in registers
-        tile_start<true>(agg, sm.xch[k & 1], sm.start, carry, rank, ncl);
+        tile_start<true>(agg, sm.xch + (k & 1) * ncl, sm.start, carry, rank, ncl);
         float s[V];
         run_start<V, true>(agg, sm.start, exA, exH, l.warp_t, l.c, s);
         if (on && p.ckpt && t0 % CKPT == 0 && t0 < p.T) {
@@ -312,7 +339,7 @@ __global__ void __launch_bounds__(NT, 2) scan_fwd_kernel(ScanParams p) {
 #pragma unroll
             for (int i = 0; i < V; ++i) {
                 s[i] = fmaf(a[r][i], s[i], bb[r][i]);
-                o[i] = t < len ? s[i] : 0.f;
+                o[i] = whole || t < len ? s[i] : 0.f;
             }
             if (on && t < p.T && GDR_INB(c + V <= p.D, 802))
                 *reinterpret_cast<typename Pack<OT, V>::Raw*>(h + (size_t)t * p.D) = Pack<OT, V>::put(o);
@@ -330,8 +357,8 @@ template <typename XT, typename GT, typename OT, int V> struct BwdSmem {
     float ck[STAGES][CH];
     float2 up[2][WT][CH];
     float2 down[2][WT][CH];
-    float2 xch[2][MAX_CLUSTER][CH];
     float start[CH];
+    float2 xch[1][CH];                  // [2][cluster][CH]: the launch adds the rest
 };
 
 // The states inside a tile come from its checkpoint (a block's tile is CKPT tokens), so only the
@@ -419,16 +446,33 @@ __global__ void __launch_bounds__(NT, 2) scan_bwd_kernel(ScanParams p) {
             }
         }
         float A[V], H[V], M[V], dA[V], exA[V], exH[V], exD[V], exM[V];
+        // rest: 1 - a; bb: the input w x
+        with_mode(p, [&](auto mode, auto tied) {
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    rest[r][i] = 0.f;
+                    decay_pair<mode.value, mode.value == 1 || tied.value>(a[r][i], a[r][i], rest[r][i]);
+                }
+            }
+        });
+        const bool whole = t0 + R <= len;
+        if (!whole) {
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+#pragma unroll
+                for (int i = 0; i < V; ++i)
+                    if (t0 + r >= len) { a[r][i] = 1.f; rest[r][i] = 0.f; }
+            }
+        }
 #pragma unroll
         for (int i = 0; i < V; ++i) { A[i] = 1.f; H[i] = 0.f; M[i] = 0.f; }
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-            const bool in = t0 + r < len;
 #pragma unroll
             for (int i = 0; i < V; ++i) {
-                decay_pair(a[r][i], p.gate_mode, a[r][i], rest[r][i]);
-                if (!in) { a[r][i] = 1.f; rest[r][i] = 0.f; }
-                H[i] = fmaf(a[r][i], H[i], in ? (p.tied ? rest[r][i] * xv[r][i] : xv[r][i]) : 0.f);
+                H[i] = fmaf(a[r][i], H[i], p.tied ? rest[r][i] * xv[r][i] : xv[r][i]);
                 A[i] *= a[r][i];
             }
         }
@@ -454,14 +498,13 @@ __global__ void __launch_bounds__(NT, 2) scan_bwd_kernel(ScanParams p) {
         run_start<V, true>(sm.up[k & 1], sm.ck[k % STAGES], exA, exH, l.warp_t, l.c, s);
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-            const bool in = t0 + r < len;
 #pragma unroll
             for (int i = 0; i < V; ++i) {
                 before[r][i] = s[i];
-                s[i] = fmaf(a[r][i], s[i], in ? (p.tied ? rest[r][i] * xv[r][i] : xv[r][i]) : 0.f);
+                s[i] = fmaf(a[r][i], s[i], p.tied ? rest[r][i] * xv[r][i] : xv[r][i]);
             }
         }
-        tile_start<false>(sm.down[k & 1], sm.xch[k & 1], sm.start, carry, rank, ncl);
+        tile_start<false>(sm.down[k & 1], sm.xch + (k & 1) * ncl, sm.start, carry, rank, ncl);
         fetch(k + STAGES);                                // behind the barrier: the checkpoint's slot is read
         run_start<V, false>(sm.down[k & 1], sm.start, exD, exM, l.warp_t, l.c, m);
 #pragma unroll
@@ -472,8 +515,8 @@ __global__ void __launch_bounds__(NT, 2) scan_bwd_kernel(ScanParams p) {
             for (int i = 0; i < V; ++i) {
                 const float lam = d[r][i] + m[i];
                 const float da = lam * (p.tied ? before[r][i] - xv[r][i] : before[r][i]);
-                ox[i] = t < len ? (p.tied ? rest[r][i] * lam : lam) : 0.f;
-                og[i] = t < len ? (p.gate_mode == 1 ? -da * (a[r][i] * rest[r][i]) : da * a[r][i]) : 0.f;
+                ox[i] = whole || t < len ? (p.tied ? rest[r][i] * lam : lam) : 0.f;
+                og[i] = whole || t < len ? (p.gate_mode == 1 ? -da * (a[r][i] * rest[r][i]) : da * a[r][i]) : 0.f;
                 m[i] = a[r][i] * lam;
             }
             if (on && t < p.T && GDR_INB(c + V <= p.D, 811)) {
@@ -499,12 +542,14 @@ __global__ void __launch_bounds__(NT) scan_step_kernel(ScanParams p) {
         typename Pack<float, V>::Raw* h = reinterpret_cast<typename Pack<float, V>::Raw*>(p.h_T + b * p.D + c);
         if (!GDR_INB(b < (size_t)p.B && c + V <= (size_t)p.D, 821)) break;
         Pack<float, V>::get(*h, s);
+        with_mode(p, [&](auto mode, auto tied) {
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-            float dec, rest;
-            decay_pair(a[j], p.gate_mode, dec, rest);
-            s[j] = fmaf(dec, s[j], p.tied ? rest * x[j] : x[j]);
-        }
+            for (int j = 0; j < V; ++j) {
+                float dec, rest = 1.f;
+                decay_pair<mode.value, tied.value>(a[j], dec, rest);
+                s[j] = fmaf(dec, s[j], tied.value ? rest * x[j] : x[j]);
+            }
+        });
         *h = Pack<float, V>::put(s);
         if (p.h) *reinterpret_cast<typename Pack<OT, V>::Raw*>(static_cast<OT*>(p.h) + b * p.D + c) = Pack<OT, V>::put(s);
     }
