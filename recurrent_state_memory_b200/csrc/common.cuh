@@ -74,33 +74,21 @@ __device__ __forceinline__ float decay_factor(float a, int gate_mode) {
     return expf(a);
 }
 
-// e^x for x <= 88 (below -87 the result is 0; NaN stays).  e^x = 2^(x log2 e), the
-// product's rounding and the constant's second word put back to first order, so that the error
-// does not grow with |x|: within 4 steps of 2^-24, mostly the exponential instruction's.
-__device__ __forceinline__ float exp_f32(float x) {
-    const float log2e = 1.44269502f, log2e_lo = 1.92596303e-8f, ln2 = 0.693147182f;
-    float y, e;
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(x) : "f"(x), "f"(-104.f));
-    y = x * log2e;
-    const float lost = fmaf(x, log2e_lo, fmaf(x, log2e, -y));
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(y));
-    return fmaf(e * lost, ln2, e);
-}
-
-// The decay a = exp(g) of one gate value and 1 - a, both to full relative precision (1 - a from
-// the difference would lose it where a is near one).  Mode 1: sigmoid(-v) and sigmoid(v), formed
-// from e^{-|v|} <= 1 so that neither overflows.  REST false: 1 - a is not formed.
+// The decay a = exp(g) of one gate value v, and 1 - a (REST) without taking a difference, which
+// would lose it where a is near one.  Mode 1 with e = e^v: a = 1 / (1 + e), 1 - a = e a, and e is
+// held at 2^126 where it would reach the product as infinity.  The product v log2(e) is rounded
+// once and its error left in place: it moves the gate by 1.25 steps of 2^-24 of its own value, as
+// storing the gate in fp32 does already.  NaN stays NaN.
 template <int MODE, bool REST>
 __device__ __forceinline__ void decay_pair(float v, float& a, float& rest) {
+    float e;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(v * 1.44269502f));
     if constexpr (MODE == 1) {
-        const float e = exp_f32(-fabsf(v));
-        float r;
-        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
-        const float er = e * r;
-        a = v >= 0.f ? er : r;
-        if constexpr (REST) rest = v >= 0.f ? r : er;
+        if constexpr (REST) asm("min.NaN.f32 %0, %1, %2;" : "=f"(e) : "f"(e), "f"(8.50705917e37f));
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(a) : "f"(1.f + e));
+        if constexpr (REST) rest = e * a;
     } else {
-        a = expf(v);
+        a = e;
         if constexpr (REST) rest = -expm1f(v);
     }
 }

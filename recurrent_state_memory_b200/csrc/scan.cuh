@@ -68,27 +68,6 @@ template <typename F> __device__ __forceinline__ void with_mode(const ScanParams
 
 __device__ __forceinline__ uint32_t smem_addr(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
 
-// Copy N bytes (8 or 16) to shared memory, or fill them with zero.
-template <int N> __device__ __forceinline__ void copy_async(void* dst, const void* src, bool on) {
-    static_assert(N == 8 || N == 16, "bytes");
-    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(smem_addr(dst)), "l"(src), "n"(N), "r"(on ? N : 0)
-                 : "memory");
-}
-__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N> __device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
-
-__device__ __forceinline__ uint32_t cluster_rank() { uint32_t r; asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r)); return r; }
-__device__ __forceinline__ uint32_t cluster_size() { uint32_t r; asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r)); return r; }
-__device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-// Store to the same shared-memory place of block `rank` of the cluster.
-__device__ __forceinline__ void store_peer(float2* p, float2 v, uint32_t rank) {
-    uint32_t a;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_addr(p)), "r"(rank));
-    asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(a), "f"(v.x), "f"(v.y) : "memory");
-}
-
 // V values of one thread as stored: loads from global or shared memory, and the rounding store.
 template <typename T, int V> struct Pack;
 template <> struct Pack<float, 4> {
@@ -112,6 +91,46 @@ template <typename T> struct Pack<T, 1> {
     static __device__ __forceinline__ void get(const Raw& r, float (&v)[1]) { v[0] = ld_f32(&r); }
     static __device__ __forceinline__ Raw put(const float (&v)[1]) { Raw r; st_from_f32(&r, v[0]); return r; }
 };
+
+// Copy N bytes (8 or 16) to shared memory (address dst), or fill them with zero.
+template <int N> __device__ __forceinline__ void copy_async(uint32_t dst, const void* src) {
+    static_assert(N == 8 || N == 16, "bytes");
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(N) : "memory");
+}
+template <int N> __device__ __forceinline__ void copy_async(uint32_t dst, const void* src, bool on) {
+    static_assert(N == 8 || N == 16, "bytes");
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(N), "r"(on ? N : 0) : "memory");
+}
+// A run's R rows (row elements of T apart, src at the first) to slots of one thread, NT slots apart;
+// rows from `have` on are filled with zero and not read (none: an address that may be named).
+template <typename T, int V, int R>
+__device__ __forceinline__ void copy_run(uint32_t dst, const T* src, long long row, int have, const void* none) {
+    constexpr int N = sizeof(typename Pack<T, V>::Raw);
+    if (have >= R) {
+        const char* q = reinterpret_cast<const char*>(src);
+        const long long step = row * (long long)sizeof(T);
+#pragma unroll
+        for (int r = 0; r < R; ++r) { copy_async<N>(dst + r * NT * N, q); q += step; }
+    } else {
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+            copy_async<N>(dst + r * NT * N, r < have ? (const void*)(src + r * row) : none, r < have);
+    }
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+__device__ __forceinline__ uint32_t cluster_rank() { uint32_t r; asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r)); return r; }
+__device__ __forceinline__ uint32_t cluster_size() { uint32_t r; asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r)); return r; }
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// Store to the same shared-memory place of block `rank` of the cluster.
+__device__ __forceinline__ void store_peer(float2* p, float2 v, uint32_t rank) {
+    uint32_t a;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_addr(p)), "r"(rank));
+    asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(a), "f"(v.x), "f"(v.y) : "memory");
+}
 
 // How a block's threads lie over its tile.  V = 4: 8 lanes x 4 channels and 4 runs per warp
 // (vector access: rows and pointers aligned to 4 elements); V = 1: 32 lanes x 1 channel.
@@ -246,15 +265,9 @@ __global__ void __launch_bounds__(NT, 2) scan_fwd_kernel(ScanParams p) {
     auto fetch = [&](int k) {                             // turn k's inputs of this thread
         if constexpr (V > 1) {
             if (k < turns) {
-#pragma unroll
-                for (int r = 0; r < R; ++r) {
-                    const int t = k * turn + first + r;
-                    const bool in = on && t < len;
-                    copy_async<sizeof(typename Pack<GT, V>::Raw)>(&sm.g[k % STAGES][r][threadIdx.x],
-                                                                  in ? g + (size_t)t * p.g_row : p.g, in);
-                    copy_async<sizeof(typename Pack<XT, V>::Raw)>(&sm.x[k % STAGES][r][threadIdx.x],
-                                                                  in ? x + (size_t)t * p.x_row : p.x, in);
-                }
+                const int t = k * turn + first, have = on ? len - t : 0;
+                copy_run<GT, V, R>(smem_addr(&sm.g[k % STAGES][0][threadIdx.x]), g + t * p.g_row, p.g_row, have, p.g);
+                copy_run<XT, V, R>(smem_addr(&sm.x[k % STAGES][0][threadIdx.x]), x + t * p.x_row, p.x_row, have, p.x);
             }
             copy_commit();
         }
@@ -332,17 +345,29 @@ __global__ void __launch_bounds__(NT, 2) scan_fwd_kernel(ScanParams p) {
                 else ck[0] = s[0];
             }
         }
+        OT* out = h + (size_t)t0 * p.D;
+        if (on && whole) {
 #pragma unroll
-        for (int r = 0; r < R; ++r) {
-            const int t = t0 + r;
-            float o[V];
+            for (int r = 0; r < R; ++r) {
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-                s[i] = fmaf(a[r][i], s[i], bb[r][i]);
-                o[i] = whole || t < len ? s[i] : 0.f;
+                for (int i = 0; i < V; ++i) s[i] = fmaf(a[r][i], s[i], bb[r][i]);
+                if (GDR_INB(t0 + r < p.T && c + V <= p.D, 802))
+                    *reinterpret_cast<typename Pack<OT, V>::Raw*>(out) = Pack<OT, V>::put(s);
+                out += p.D;
             }
-            if (on && t < p.T && GDR_INB(c + V <= p.D, 802))
-                *reinterpret_cast<typename Pack<OT, V>::Raw*>(h + (size_t)t * p.D) = Pack<OT, V>::put(o);
+        } else if (on) {
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                float o[V];
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    s[i] = fmaf(a[r][i], s[i], bb[r][i]);
+                    o[i] = t0 + r < len ? s[i] : 0.f;
+                }
+                if (t0 + r < p.T && GDR_INB(c + V <= p.D, 803))
+                    *reinterpret_cast<typename Pack<OT, V>::Raw*>(out) = Pack<OT, V>::put(o);
+                out += p.D;
+            }
         }
     }
     if (p.h_T && rank == 0 && threadIdx.x < CH && c0 + (int)threadIdx.x < p.D)
@@ -390,25 +415,18 @@ __global__ void __launch_bounds__(NT, 2) scan_bwd_kernel(ScanParams p) {
         if (k < turns) {
             const int base = (turns - 1 - k) * turn;
             if constexpr (V > 1) {
-#pragma unroll
-                for (int r = 0; r < R; ++r) {
-                    const int t = base + first + r;
-                    const bool in = on && t < len;
-                    copy_async<sizeof(typename Pack<GT, V>::Raw)>(&sm.g[k % STAGES][r][threadIdx.x],
-                                                                  in ? g + (size_t)t * p.g_row : p.g, in);
-                    copy_async<sizeof(typename Pack<XT, V>::Raw)>(&sm.x[k % STAGES][r][threadIdx.x],
-                                                                  in ? x + (size_t)t * p.x_row : p.x, in);
-                    copy_async<sizeof(typename Pack<OT, V>::Raw)>(&sm.dh[k % STAGES][r][threadIdx.x],
-                                                                  in && with_dh ? (const void*)(dh + (size_t)t * p.D) : p.ckpt,
-                                                                  in && with_dh);
-                }
+                const int t = base + first, have = on ? len - t : 0;
+                copy_run<GT, V, R>(smem_addr(&sm.g[k % STAGES][0][threadIdx.x]), g + t * p.g_row, p.g_row, have, p.g);
+                copy_run<XT, V, R>(smem_addr(&sm.x[k % STAGES][0][threadIdx.x]), x + t * p.x_row, p.x_row, have, p.x);
+                copy_run<OT, V, R>(smem_addr(&sm.dh[k % STAGES][0][threadIdx.x]), dh + (size_t)t * p.D, p.D,
+                                   with_dh ? have : 0, p.ckpt);
             }
             // the tile's checkpoint; read behind the turn's first barrier
             const int j = base / CKPT + rank;
             if constexpr (V > 1) {
                 if (threadIdx.x < CH / 4) {
                     const bool in = j < nck && c0 + (int)threadIdx.x * 4 < p.D;
-                    copy_async<16>(&sm.ck[k % STAGES][threadIdx.x * 4],
+                    copy_async<16>(smem_addr(&sm.ck[k % STAGES][threadIdx.x * 4]),
                                    in ? p.ckpt + ((size_t)b * nck + j) * p.D + c0 + threadIdx.x * 4 : p.ckpt, in);
                 }
             } else if (threadIdx.x < CH) {
@@ -446,7 +464,7 @@ __global__ void __launch_bounds__(NT, 2) scan_bwd_kernel(ScanParams p) {
             }
         }
         float A[V], H[V], M[V], dA[V], exA[V], exH[V], exD[V], exM[V];
-        // rest: 1 - a; bb: the input w x
+        // rest: 1 - a
         with_mode(p, [&](auto mode, auto tied) {
 #pragma unroll
             for (int r = 0; r < R; ++r) {
@@ -507,23 +525,33 @@ __global__ void __launch_bounds__(NT, 2) scan_bwd_kernel(ScanParams p) {
         tile_start<false>(sm.down[k & 1], sm.xch + (k & 1) * ncl, sm.start, carry, rank, ncl);
         fetch(k + STAGES);                                // behind the barrier: the checkpoint's slot is read
         run_start<V, false>(sm.down[k & 1], sm.start, exD, exM, l.warp_t, l.c, m);
+        // the gradient of the gate: lam (h_{t-1} - [tied] x) a', a' = a or -a (1 - a)
+        XT* out_x = dx + (size_t)t0 * p.D + (size_t)(R - 1) * p.D;
+        GT* out_g = dg + (size_t)t0 * p.D + (size_t)(R - 1) * p.D;
+        with_mode(p, [&](auto mode, auto tied) {
 #pragma unroll
-        for (int r = R - 1; r >= 0; --r) {
-            const int t = t0 + r;
-            float ox[V], og[V];
+            for (int r = R - 1; r >= 0; --r) {
+                float ox[V], og[V];
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-                const float lam = d[r][i] + m[i];
-                const float da = lam * (p.tied ? before[r][i] - xv[r][i] : before[r][i]);
-                ox[i] = whole || t < len ? (p.tied ? rest[r][i] * lam : lam) : 0.f;
-                og[i] = whole || t < len ? (p.gate_mode == 1 ? -da * (a[r][i] * rest[r][i]) : da * a[r][i]) : 0.f;
-                m[i] = a[r][i] * lam;
+                for (int i = 0; i < V; ++i) {
+                    const float lam = d[r][i] + m[i];
+                    m[i] = a[r][i] * lam;
+                    ox[i] = tied.value ? rest[r][i] * lam : lam;
+                    const float da = m[i] * (tied.value ? before[r][i] - xv[r][i] : before[r][i]);
+                    og[i] = mode.value == 1 ? -da * rest[r][i] : da;
+                }
+                if (!whole && t0 + r >= len) {
+#pragma unroll
+                    for (int i = 0; i < V; ++i) ox[i] = og[i] = 0.f;
+                }
+                if (on && t0 + r < p.T && GDR_INB(c + V <= p.D, 811)) {
+                    *reinterpret_cast<typename Pack<XT, V>::Raw*>(out_x) = Pack<XT, V>::put(ox);
+                    *reinterpret_cast<typename Pack<GT, V>::Raw*>(out_g) = Pack<GT, V>::put(og);
+                }
+                out_x -= p.D;
+                out_g -= p.D;
             }
-            if (on && t < p.T && GDR_INB(c + V <= p.D, 811)) {
-                *reinterpret_cast<typename Pack<XT, V>::Raw*>(dx + (size_t)t * p.D) = Pack<XT, V>::put(ox);
-                *reinterpret_cast<typename Pack<GT, V>::Raw*>(dg + (size_t)t * p.D) = Pack<GT, V>::put(og);
-            }
-        }
+        });
     }
     if (p.dh0 && rank == 0 && threadIdx.x < CH && c0 + (int)threadIdx.x < p.D)
         p.dh0[(size_t)b * p.D + c0 + threadIdx.x] = carry;

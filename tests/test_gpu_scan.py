@@ -2,11 +2,16 @@
 definition (oracle/block.py).
 
 Tolerances are error bounds, element by element, from the fp64 quantities.  With u = 2^-24: the
-decay a (one exponential within 2u, one sum, one quotient, one product: 6u), its product with the
-state and the sum (2u), and in the chunked form two more products (2u + 2u) put at most C = 12u of
-the two terms' magnitudes into each step, and what is there already is carried on by a.  So
-E_t = a_t E_{t-1} + C (a_t H_{t-1} + |w_t x_t|), with H the recurrence of the magnitudes, bounds the
-error of h_t; the gradients follow by the product rule.  A 16-bit output adds half a step."""
+decay a (one exponential within 3u, one sum, one reciprocal within 2u, one product: 7u), its product
+with the state and the sum (2u), and in the chunked form the run's products (3u) put at most 12u of
+the two terms' magnitudes into each step.  The exponent g log2(e) is one rounded product with a
+rounded constant: u |g| and 0.25 u |g| in a and in 1 - a, relatively.  fp32 has no normal value
+below 2^-126: a decay or 1 - a smaller than that comes out as any value up to it, so FLOOR = 2^-126
+is added to their absolute errors (beyond |g| = 90 the smaller of the two is all FLOOR, and the other
+one does not move).  So, with C = 12u + 1.25u min(|g|, 90) a step and what is there already carried
+on by a, E_t = a_t E_{t-1} + (C a_t + FLOOR) H_{t-1} + (C w_t + FLOOR) |x_t|, with H the recurrence of
+the magnitudes, bounds the error of h_t; the gradients follow by the product rule.  A 16-bit output
+adds half a step."""
 import numpy as np
 import pytest
 
@@ -14,8 +19,8 @@ from oracle import block as O
 
 pytestmark = pytest.mark.gpu
 U = 2.0 ** -24
-C = 12 * U
 HALF = {"bf16": 2.0 ** -8, "f32": U}
+FLOOR = 2.0 ** -126
 TINY = 1e-37                # results below the normal range may be flushed
 
 
@@ -94,22 +99,24 @@ def _bounds(c):
     a = np.where(inside, a, 1.0)
     wx = np.where(inside, np.abs(x) * (rest if c.tied else 1.0), 0.0)
     h0 = np.zeros((B, D)) if h0 is None else h0
+    C = U * (12 + 1.25 * np.minimum(np.abs(g), 90))
     _, before = _walk(a, wx, np.abs(h0))
-    err, err_before = _walk(a, np.where(inside, C * (a * before + wx), 0.0), np.zeros((B, D)))
+    err, err_before = _walk(a, np.where(inside, C * (a * before + wx) + FLOOR * (before + np.abs(x)), 0.0), np.zeros((B, D)))
     # the state's gradient, from the end
     rev = lambda v: v[:, ::-1]
     up = np.concatenate([np.ones((B, 1, D)), rev(a)[:, :-1]], 1)        # a_{t+1}
     mag = np.where(inside, np.abs(dh), 0.0)
     mag[:, -1] += np.abs(dhT)
     lam, _ = _walk(up, rev(mag), np.zeros((B, D)))
-    lam_err, _ = _walk(up, C * lam, np.zeros((B, D)))
+    Cup = np.concatenate([C[:, -1:], rev(C)[:, :-1]], 1)                # a_{t+1}'s
+    lam_err, _ = _walk(up, Cup * lam + 2 * FLOOR * lam, np.zeros((B, D)))
     lam, lam_err = rev(lam), rev(lam_err)
     w = rest if c.tied else 1.0
-    dx_err = np.where(inside, w * (lam_err + 8 * U * lam), 0.0)
+    dx_err = np.where(inside, w * (lam_err + C * lam) + FLOOR * lam, 0.0)
     slope = np.abs(a * rest if c.gate_mode == 1 else a)
     size = before + (np.abs(x) if c.tied else 0.0)
-    dg_err = np.where(inside, slope * (lam_err * size + lam * err_before + 20 * U * lam * size), 0.0)
-    h0_err = a[:, 0] * (lam_err[:, 0] + C * lam[:, 0])
+    dg_err = np.where(inside, slope * (lam_err * size + lam * err_before + (8 * U + 2 * C) * lam * size) + 2 * FLOOR * lam * size, 0.0)
+    h0_err = a[:, 0] * (lam_err[:, 0] + C[:, 0] * lam[:, 0]) + FLOOR * lam[:, 0]
     return err, err_before, dx_err, dg_err, h0_err
 
 
