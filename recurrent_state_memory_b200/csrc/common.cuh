@@ -16,6 +16,7 @@ static __device__ unsigned int g_device_status = 0;
 // guards one global-memory access: when cond fails, the site number goes to g_bounds_site (the
 // first failure is kept), bit 2 of the status word is set and the access is skipped.  In the
 // default build the macro is the constant true and costs nothing.
+constexpr unsigned STATUS_TIMEOUT = 1u;
 constexpr unsigned STATUS_BOUNDS = 4u;
 constexpr unsigned STATUS_INDEX = 8u;      // an index that the caller passed in device memory is out of range
 static __device__ unsigned int g_bounds_site = 0;

@@ -12,10 +12,11 @@
 //
 // Split.  A block of 8 warps owns 64 channels x TOK tokens per turn; a cluster of up to 16 blocks
 // takes that many neighbouring tiles of the same channels and walks the sequence in turns, so
-// that few channels with long sequences still fill the GPU.  Per turn the blocks exchange their
-// tiles' (A, H) through distributed shared memory and one cluster barrier; every block then
-// folds them in the same order, so the result does not depend on timing, and there is neither a
-// workspace nor a wait on another block outside the cluster's barrier.  The next turns' inputs
+// that few channels with long sequences still fill the GPU.  Per turn the blocks send one another
+// their tiles' (A, H) by asynchronous stores into distributed shared memory, which an mbarrier
+// counts (a cluster barrier per turn would also wait for the turn's output stores); every block
+// then folds them in the same order, so the result does not depend on timing, and there is
+// neither a workspace nor a wait on a block outside the cluster.  The next turns' inputs
 // are copied to shared memory (cp.async; each thread copies and reads its own slots, so the
 // copies need no barrier) while the current turn is computed.
 #pragma once
@@ -23,6 +24,7 @@
 #include <type_traits>
 
 #include "common.cuh"
+#include "tc_ptx.cuh"
 
 namespace gdr {
 namespace scn {
@@ -125,11 +127,35 @@ __device__ __forceinline__ uint32_t cluster_size() { uint32_t r; asm volatile("m
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-// Store to the same shared-memory place of block `rank` of the cluster.
-__device__ __forceinline__ void store_peer(float2* p, float2 v, uint32_t rank) {
-    uint32_t a;
+// The same without ordering memory (it does not wait for stores on their way).
+__device__ __forceinline__ void cluster_sync_relaxed() {
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+}
+// Store to the same shared-memory place of block `rank` of the cluster; the 8 bytes count towards
+// the phase of that block's barrier.
+__device__ __forceinline__ void store_peer(float2* p, float2 v, uint64_t* bar, uint32_t rank) {
+    uint32_t a, m;
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_addr(p)), "r"(rank));
-    asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(a), "f"(v.x), "f"(v.y) : "memory");
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(m) : "r"(smem_addr(bar)), "r"(rank));
+    asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v2.f32 [%0], {%1, %2}, [%3];"
+                 ::"r"(a), "f"(v.x), "f"(v.y), "r"(m) : "memory");
+}
+__device__ __forceinline__ void expect_bytes(uint64_t* bar, uint32_t n) {
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_addr(bar)), "r"(n) : "memory");
+}
+__device__ __forceinline__ bool phase_done(uint64_t* bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile("{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+                 "selp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok) : "r"(smem_addr(bar)), "r"(parity) : "memory");
+    return ok != 0;
+}
+// Wait for a phase, for at most 2 s; false (and the status word's timeout bit) when it did not come.
+__device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity) {
+    if (phase_done(bar, parity)) return true;
+    const uint64_t t0 = tc::globaltimer_ns();
+    while (!phase_done(bar, parity))
+        if (tc::globaltimer_ns() - t0 > 2000000000ull) { atomicOr(&g_device_status, STATUS_TIMEOUT); return false; }
+    return true;
 }
 
 // How a block's threads lie over its tile.  V = 4: 8 lanes x 4 channels and 4 runs per warp
@@ -177,12 +203,14 @@ __device__ __forceinline__ void warp_runs(float (&A)[V], float (&H)[V], float (&
 }
 
 // The start of this block's tile along the scan's direction.  agg: the block's warps' (A, H);
-// xch: the cluster's blocks' (A, H), this turn's; carry: the state at the cluster's turn start,
-// held by the first CH threads of every block alike, moved on by the turn.  Leaves the tile's start
-// state in start[CH] and synchronises the block (which must have synchronised after writing agg).
+// carry: the state at the cluster's turn start, held by the first CH threads of every block
+// alike, moved on by the turn.  Leaves the tile's start state in start[CH] and synchronises the
+// block (which must have synchronised after writing agg).  xch and bars hold two turns' worth: a
+// block sends turn k + 2's only when it has turn k + 1's from every peer, each of which sent it
+// behind its last read of turn k's.  lost: a wait ran out; the block goes on without waiting.
 template <bool UP>
-__device__ __forceinline__ void tile_start(const float2 (*agg)[CH], float2 (*xch)[CH], float* start, float& carry,
-                                           int rank, int ncl) {
+__device__ __forceinline__ void tile_start(const float2 (*agg)[CH], float2 (*xch)[CH], uint64_t* bars, float* start,
+                                           float& carry, bool& lost, int k, int rank, int ncl) {
     const int c = threadIdx.x & (CH - 1), q = threadIdx.x / CH;
     float A = 1.f, H = 0.f;
 #pragma unroll
@@ -192,25 +220,37 @@ __device__ __forceinline__ void tile_start(const float2 (*agg)[CH], float2 (*xch
         A *= e.x;
     }
     if (ncl > 1) {
-        for (int r = q; r < ncl; r += NT / CH) store_peer(&xch[rank][c], make_float2(A, H), r);
-        cluster_sync();
-    }
-    if (q == 0) {
-        float s = carry;
-        if (ncl > 1) {
+        xch += (k & 1) * ncl;
+        uint64_t* bar = bars + (k & 1);
+        if (threadIdx.x == 0) expect_bytes(bar, (uint32_t)(ncl * CH * sizeof(float2)));
+        for (int r = q; r < ncl; r += NT / CH) store_peer(&xch[rank][c], make_float2(A, H), bar, r);
+        if (q == 0) {
+            if (!lost) lost = !wait_phase(bar, (uint32_t)(k >> 1) & 1u);
+            float s = carry;
             for (int i = 0; i < ncl; ++i) {
                 const int r = UP ? i : ncl - 1 - i;
                 if (r == rank) start[c] = s;
                 const float2 e = xch[r][c];
                 s = fmaf(e.x, s, e.y);
             }
-        } else {
-            start[c] = s;
-            s = fmaf(A, s, H);
+            carry = s;
         }
-        carry = s;
+    } else if (q == 0) {
+        start[c] = carry;
+        carry = fmaf(A, carry, H);
     }
     __syncthreads();
+}
+
+// Before the first turn: the barriers, and the peers' shared memory exists.
+__device__ __forceinline__ void exchange_begin(uint64_t* bars, int ncl) {
+    if (ncl == 1) return;
+    if (threadIdx.x == 0) {
+        tc::mbar_init(&bars[0], 1);
+        tc::mbar_init(&bars[1], 1);
+        tc::fence_mbar_init();
+    }
+    cluster_sync();
 }
 
 // The state before this thread's run: the tile's start through the warps before it and the
@@ -241,6 +281,7 @@ template <typename XT, typename GT, int V> struct FwdSmem {
     typename Pack<XT, V>::Raw x[V > 1 ? STAGES : 1][V > 1 ? R : 1][V > 1 ? NT : 1];
     float2 agg[2][WT][CH];
     float start[CH];
+    uint64_t bars[2];
     float2 xch[1][CH];                  // [2][cluster][CH]: the launch adds the rest
 };
 
@@ -278,7 +319,8 @@ __global__ void __launch_bounds__(NT, 2) scan_fwd_kernel(ScanParams p) {
     float carry = 0.f;
     if (threadIdx.x < CH && c0 + (int)threadIdx.x < p.D && p.h0) carry = p.h0[(size_t)b * p.D + c0 + threadIdx.x];
 
-    if (ncl > 1) cluster_sync();                          // the peers' shared memory exists
+    bool lost = false;
+    exchange_begin(sm.bars, ncl);
     for (int k = 0; k < turns; ++k) {
         const int t0 = k * turn + first;
         float a[R][V], bb[R][V], A[V], H[V], exA[V], exH[V];
@@ -335,7 +377,7 @@ __global__ void __launch_bounds__(NT, 2) scan_fwd_kernel(ScanParams p) {
         }
         __syncthreads();
         fetch(k + STAGES);                                // the slots of turn k are in registers
-        tile_start<true>(agg, sm.xch + (k & 1) * ncl, sm.start, carry, rank, ncl);
+        tile_start<true>(agg, sm.xch, sm.bars, sm.start, carry, lost, k, rank, ncl);
         float s[V];
         run_start<V, true>(agg, sm.start, exA, exH, l.warp_t, l.c, s);
         if (on && p.ckpt && t0 % CKPT == 0 && t0 < p.T) {
@@ -370,6 +412,7 @@ __global__ void __launch_bounds__(NT, 2) scan_fwd_kernel(ScanParams p) {
             }
         }
     }
+    if (ncl > 1) cluster_sync_relaxed();                  // no peer still sends here
     if (p.h_T && rank == 0 && threadIdx.x < CH && c0 + (int)threadIdx.x < p.D)
         p.h_T[(size_t)b * p.D + c0 + threadIdx.x] = carry;
 }
@@ -383,6 +426,7 @@ template <typename XT, typename GT, typename OT, int V> struct BwdSmem {
     float2 up[2][WT][CH];
     float2 down[2][WT][CH];
     float start[CH];
+    uint64_t bars[2];
     float2 xch[1][CH];                  // [2][cluster][CH]: the launch adds the rest
 };
 
@@ -442,7 +486,8 @@ __global__ void __launch_bounds__(NT, 2) scan_bwd_kernel(ScanParams p) {
     float carry = 0.f;
     if (threadIdx.x < CH && c0 + (int)threadIdx.x < p.D && p.dh_T) carry = p.dh_T[(size_t)b * p.D + c0 + threadIdx.x];
 
-    if (ncl > 1) cluster_sync();                          // the peers' shared memory exists
+    bool lost = false;
+    exchange_begin(sm.bars, ncl);
     for (int k = 0; k < turns; ++k) {
         const int t0 = (turns - 1 - k) * turn + first;
         float a[R][V], rest[R][V], xv[R][V], d[R][V];
@@ -522,7 +567,7 @@ __global__ void __launch_bounds__(NT, 2) scan_bwd_kernel(ScanParams p) {
                 s[i] = fmaf(a[r][i], s[i], p.tied ? rest[r][i] * xv[r][i] : xv[r][i]);
             }
         }
-        tile_start<false>(sm.down[k & 1], sm.xch + (k & 1) * ncl, sm.start, carry, rank, ncl);
+        tile_start<false>(sm.down[k & 1], sm.xch, sm.bars, sm.start, carry, lost, k, rank, ncl);
         fetch(k + STAGES);                                // behind the barrier: the checkpoint's slot is read
         run_start<V, false>(sm.down[k & 1], sm.start, exD, exM, l.warp_t, l.c, m);
         // the gradient of the gate: lam (h_{t-1} - [tied] x) a', a' = a or -a (1 - a)
@@ -553,6 +598,7 @@ __global__ void __launch_bounds__(NT, 2) scan_bwd_kernel(ScanParams p) {
             }
         });
     }
+    if (ncl > 1) cluster_sync_relaxed();
     if (p.dh0 && rank == 0 && threadIdx.x < CH && c0 + (int)threadIdx.x < p.D)
         p.dh0[(size_t)b * p.D + c0 + threadIdx.x] = carry;
 }
