@@ -237,29 +237,6 @@ static gdr_status check_fwd_desc(const gdr_fwd_desc* d) {
 }
 
 // ---- tensor maps of the split kernel ---------------------------------------------------
-// cuTensorMapEncodeTiled is a driver call; it is looked up through the runtime so that the
-// library does not link libcuda itself.
-typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-static gdr_status encode_fn(EncodeTiledFn* out) {
-    static std::mutex mu;
-    static EncodeTiledFn fn = nullptr;
-    std::lock_guard<std::mutex> lock(mu);
-    if (!fn) {
-        void* ptr = nullptr;
-        cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
-        cudaError_t e = cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &ptr, cudaEnableDefault, &q);
-        if (e != cudaSuccess) return cuda_fail(e, "cudaGetDriverEntryPoint(cuTensorMapEncodeTiled)");
-        if (q != cudaDriverEntryPointSuccess || !ptr)
-            return fail(GDR_ERR_CUDA, "the driver has no cuTensorMapEncodeTiled%s");
-        fn = reinterpret_cast<EncodeTiledFn>(ptr);
-    }
-    *out = fn;
-    return GDR_OK;
-}
-
 // A [B][T][H][inner] row-major tensor as the 4-D map {inner, H, T, B}; boxes cover `box_inner`
 // elements of one head for 64 consecutive tokens.  Out-of-range tokens read as zero and are
 // not written by stores.

@@ -4,7 +4,9 @@
 
 #include <cstdint>
 #include <cstdio>
+#include <mutex>
 
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include "gdr.h"
@@ -33,6 +35,29 @@ inline int device_sm_count() {
     if (cudaGetDevice(&dev) != cudaSuccess) { cudaGetLastError(); return 148; }
     if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) { cudaGetLastError(); return 148; }
     return n;
+}
+
+// cuTensorMapEncodeTiled is a driver call; it is looked up through the runtime so that the
+// library does not link libcuda itself.
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+inline gdr_status encode_fn(EncodeTiledFn* out) {
+    static std::mutex mu;
+    static EncodeTiledFn fn = nullptr;
+    std::lock_guard<std::mutex> lock(mu);
+    if (!fn) {
+        void* ptr = nullptr;
+        cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
+        cudaError_t e = cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &ptr, cudaEnableDefault, &q);
+        if (e != cudaSuccess) return cuda_fail(e, "cudaGetDriverEntryPoint(cuTensorMapEncodeTiled)");
+        if (q != cudaDriverEntryPointSuccess || !ptr)
+            return fail(GDR_ERR_CUDA, "the driver has no cuTensorMapEncodeTiled%s");
+        fn = reinterpret_cast<EncodeTiledFn>(ptr);
+    }
+    *out = fn;
+    return GDR_OK;
 }
 
 // Every translation unit has a status word and a bounds site of its own (common.cuh); these read

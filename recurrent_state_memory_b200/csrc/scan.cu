@@ -21,7 +21,8 @@ static int cluster_of(long long tiles, int T, int tok, int sms) {
 }
 
 template <typename KERN>
-static gdr_status launch_clusters(KERN kern, const ScanParams& p, int tok, size_t smem, cudaStream_t st) {
+static gdr_status launch_clusters(KERN kern, const ScanParams& p, const ScanMaps& maps, int tok, size_t smem,
+                                  cudaStream_t st) {
     const unsigned ct = (unsigned)((p.D + CH - 1) / CH);
     const int ncl = cluster_of((long long)ct * p.B, p.T, tok, device_sm_count());
     smem += (size_t)(2 * ncl - 1) * CH * sizeof(float2);
@@ -38,29 +39,62 @@ static gdr_status launch_clusters(KERN kern, const ScanParams& p, int tok, size_
     at[0].val.clusterDim.x = ncl; at[0].val.clusterDim.y = 1; at[0].val.clusterDim.z = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, kern, p);
+    e = cudaLaunchKernelEx(&cfg, kern, p, maps);
     return e == cudaSuccess ? GDR_OK : cuda_fail(e, "launch(scan)");
+}
+
+// A [B][T] tensor of rows `row` elements apart, the first D of each row: the map {D, 1, T, B} with
+// boxes of CH channels x tok tokens.  What lies outside reads as zero.
+template <typename T>
+static gdr_status encode_rows(CUtensorMap* m, const void* base, const ScanParams& p, long long row, int tok) {
+    EncodeTiledFn fn = nullptr;
+    const gdr_status s = encode_fn(&fn);
+    if (s != GDR_OK) return s;
+    const cuuint64_t dims[4] = {(cuuint64_t)p.D, 1u, (cuuint64_t)p.T, (cuuint64_t)p.B};
+    const cuuint64_t bytes = (cuuint64_t)row * sizeof(T);
+    const cuuint64_t strides[3] = {bytes, bytes, bytes * (cuuint64_t)p.T};
+    const cuuint32_t box[4] = {CH, 1u, (cuuint32_t)tok, 1u}, estr[4] = {1u, 1u, 1u, 1u};
+    const CUresult r = fn(m, sizeof(T) == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4,
+                          const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                          CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r == CUDA_SUCCESS) return GDR_OK;
+    snprintf(t_detail, sizeof(t_detail), "cuTensorMapEncodeTiled failed (%d)", (int)r);
+    return GDR_ERR_CUDA;
 }
 
 template <typename XT, typename GT, typename OT, int V>
 static gdr_status launch_v(Pass pass, const ScanParams& p, cudaStream_t st) {
+    if (pass == STEP) {
+        const size_t blocks = ((size_t)p.B * (p.D / V) + NT - 1) / NT, cap = (size_t)device_sm_count() * 8;
+        scan_step_kernel<XT, GT, OT, V><<<(unsigned)(blocks < cap ? blocks : cap), NT, 0, st>>>(p);
+        const cudaError_t e = cudaGetLastError();
+        return e == cudaSuccess ? GDR_OK : cuda_fail(e, "launch(scan step)");
+    }
+    const int tok = pass == FWD ? Tile<V, FWD_ELEMS>::TOK : Tile<V, BWD_ELEMS>::TOK;
+    ScanMaps maps = {};
+    if (V > 1) {
+        gdr_status s = encode_rows<XT>(&maps.x, p.x, p, p.x_row, tok);
+        if (s == GDR_OK) s = encode_rows<GT>(&maps.g, p.g, p, p.g_row, tok);
+        if (s == GDR_OK && pass == BWD && p.dh) s = encode_rows<OT>(&maps.dh, p.dh, p, p.D, tok);
+        if (s != GDR_OK) return s;
+    }
     if (pass == FWD)
-        return launch_clusters(scan_fwd_kernel<XT, GT, OT, V>, p, Tile<V, FWD_ELEMS>::TOK, sizeof(FwdSmem<XT, GT, V>), st);
-    if (pass == BWD)
-        return launch_clusters(scan_bwd_kernel<XT, GT, OT, V>, p, Tile<V, BWD_ELEMS>::TOK, sizeof(BwdSmem<XT, GT, OT, V>), st);
-    const size_t blocks = ((size_t)p.B * (p.D / V) + NT - 1) / NT, cap = (size_t)device_sm_count() * 8;
-    scan_step_kernel<XT, GT, OT, V><<<(unsigned)(blocks < cap ? blocks : cap), NT, 0, st>>>(p);
-    const cudaError_t e = cudaGetLastError();
-    return e == cudaSuccess ? GDR_OK : cuda_fail(e, "launch(scan step)");
+        return launch_clusters(scan_fwd_kernel<XT, GT, OT, V>, p, maps, tok, sizeof(FwdSmem<XT, GT, V>), st);
+    return launch_clusters(scan_bwd_kernel<XT, GT, OT, V>, p, maps, tok, sizeof(BwdSmem<XT, GT, OT, V>), st);
 }
 
-// Four channels per thread where every row of every tensor is aligned to four elements, else one.
+// Four channels per thread (and tiles by TMA) where every row of every tensor starts on 16 bytes,
+// one channel per thread otherwise.  The step only needs four elements' alignment.
 template <typename XT, typename GT, typename OT>
 static gdr_status launch(Pass pass, const ScanParams& p, cudaStream_t st) {
-    auto fits = [](const void* q, long long row, size_t el) {
-        return reinterpret_cast<uintptr_t>(q) % (4 * el) == 0 && row % 4 == 0;
+    auto fits = [&](const void* q, long long row, size_t el) {
+        const size_t by = pass == STEP ? 4 * el : 16;
+        return reinterpret_cast<uintptr_t>(q) % by == 0 && row * el % by == 0 &&
+               (unsigned long long)p.T * row * el < (1ull << 40);
     };
-    const bool vec = p.D % 4 == 0 && fits(p.x, p.x_row, sizeof(XT)) && fits(p.g, p.g_row, sizeof(GT));
+    const bool vec = p.D % 4 == 0 && fits(p.x, p.x_row, sizeof(XT)) && fits(p.g, p.g_row, sizeof(GT)) &&
+                     (pass != BWD || fits(p.dh, p.D, sizeof(OT)));
     return vec ? launch_v<XT, GT, OT, 4>(pass, p, st) : launch_v<XT, GT, OT, 1>(pass, p, st);
 }
 

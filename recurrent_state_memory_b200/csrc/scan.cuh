@@ -10,18 +10,20 @@
 //
 // Bound: HBM (a forward moves 6 to 12 bytes per element for about 20 instructions).
 //
-// Split.  A block of 8 warps owns 64 channels x TOK tokens per turn; a cluster of up to 16 blocks
-// takes that many neighbouring tiles of the same channels and walks the sequence in turns, so
-// that few channels with long sequences still fill the GPU.  Per turn the blocks send one another
-// their tiles' (A, H) by asynchronous stores into distributed shared memory, which an mbarrier
-// counts (a cluster barrier per turn would also wait for the turn's output stores); every block
-// then folds them in the same order, so the result does not depend on timing, and there is
-// neither a workspace nor a wait on a block outside the cluster.  The next turns' inputs
-// are copied to shared memory (cp.async; each thread copies and reads its own slots, so the
-// copies need no barrier) while the current turn is computed.
+// Split.  A block of 8 warps owns 32 channels x TOK tokens per turn and walks the sequence in
+// turns.  Where the channels alone do not fill the GPU, a cluster of up to 16 blocks takes that
+// many neighbouring tiles per turn: the blocks send one another their tiles' (A, H) by
+// asynchronous stores into distributed shared memory, which an mbarrier counts (a cluster barrier
+// per turn would also wait for the turn's output stores: 96 against 90 us); every block folds them
+// in the same order, so the result does not depend on timing, and there is neither a workspace nor
+// a wait on a block outside the cluster.  The next turns' tiles come by tensor-map copies (TMA)
+// into a ring of shared-memory stages while the current one is computed (per-thread cp.async
+// spent a quarter of the time in issuing).
 #pragma once
 
 #include <type_traits>
+
+#include <cuda.h>
 
 #include "common.cuh"
 #include "tc_ptx.cuh"
@@ -49,8 +51,8 @@ struct ScanParams {
 
 constexpr int CKPT = GDR_SCAN_CKPT;
 constexpr int NT = 256;
-constexpr int CH = 64;                  // channels of a block
-constexpr int WT = 4;                   // warps along the tokens (2 along the channels)
+constexpr int CH = 32;                  // channels of a block
+constexpr int WT = NT / 32;             // warps, along the tokens
 constexpr int MAX_CLUSTER = 16;
 constexpr int STAGES = 2;
 
@@ -94,34 +96,6 @@ template <typename T> struct Pack<T, 1> {
     static __device__ __forceinline__ Raw put(const float (&v)[1]) { Raw r; st_from_f32(&r, v[0]); return r; }
 };
 
-// Copy N bytes (8 or 16) to shared memory (address dst), or fill them with zero.
-template <int N> __device__ __forceinline__ void copy_async(uint32_t dst, const void* src) {
-    static_assert(N == 8 || N == 16, "bytes");
-    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(N) : "memory");
-}
-template <int N> __device__ __forceinline__ void copy_async(uint32_t dst, const void* src, bool on) {
-    static_assert(N == 8 || N == 16, "bytes");
-    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(N), "r"(on ? N : 0) : "memory");
-}
-// A run's R rows (row elements of T apart, src at the first) to slots of one thread, NT slots apart;
-// rows from `have` on are filled with zero and not read (none: an address that may be named).
-template <typename T, int V, int R>
-__device__ __forceinline__ void copy_run(uint32_t dst, const T* src, long long row, int have, const void* none) {
-    constexpr int N = sizeof(typename Pack<T, V>::Raw);
-    if (have >= R) {
-        const char* q = reinterpret_cast<const char*>(src);
-        const long long step = row * (long long)sizeof(T);
-#pragma unroll
-        for (int r = 0; r < R; ++r) { copy_async<N>(dst + r * NT * N, q); q += step; }
-    } else {
-#pragma unroll
-        for (int r = 0; r < R; ++r)
-            copy_async<N>(dst + r * NT * N, r < have ? (const void*)(src + r * row) : none, r < have);
-    }
-}
-__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N> __device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
-
 __device__ __forceinline__ uint32_t cluster_rank() { uint32_t r; asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r)); return r; }
 __device__ __forceinline__ uint32_t cluster_size() { uint32_t r; asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r)); return r; }
 __device__ __forceinline__ void cluster_sync() {
@@ -158,21 +132,17 @@ __device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity) {
     return true;
 }
 
-// How a block's threads lie over its tile.  V = 4: 8 lanes x 4 channels and 4 runs per warp
-// (vector access: rows and pointers aligned to 4 elements); V = 1: 32 lanes x 1 channel.
+// How a block's threads lie over its tile.  V = 4: 8 lanes x 4 channels and 4 runs per warp, tiles
+// by TMA; V = 1 (rows that TMA does not take): 32 lanes x 1 channel, loads into registers.
 template <int V, int ELEMS> struct Tile {
     static constexpr int LC = 32 / V;           // lanes along the channels
     static constexpr int TL = 32 / LC;          // runs in a warp
     static constexpr int R = ELEMS / V;         // tokens of a run
     static constexpr int TOK = WT * TL * R;     // tokens of a block
-    int lane_t, warp_t, c;                      // run in the warp, warp along the tokens, first channel in the block
-    __device__ __forceinline__ Tile() {
-        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-        lane_t = lane / LC;
-        warp_t = warp & (WT - 1);
-        c = (warp / WT) * 32 + (lane % LC) * V;
-    }
-    __device__ __forceinline__ int first_token() const { return (warp_t * TL + lane_t) * R; }
+    int warp, lane_t, c;                        // warp, run in the warp, first channel in the block
+    __device__ __forceinline__ Tile() : warp(threadIdx.x >> 5), lane_t((threadIdx.x & 31) / LC),
+                                        c(((threadIdx.x & 31) % LC) * V) {}
+    __device__ __forceinline__ int first_token() const { return (warp * TL + lane_t) * R; }
 };
 
 // Compose a warp's runs: in (A, H) of this thread's run; out the composition of the runs before
@@ -202,95 +172,84 @@ __device__ __forceinline__ void warp_runs(float (&A)[V], float (&H)[V], float (&
     }
 }
 
-// The start of this block's tile along the scan's direction.  agg: the block's warps' (A, H);
-// carry: the state at the cluster's turn start, held by the first CH threads of every block
-// alike, moved on by the turn.  Leaves the tile's start state in start[CH] and synchronises the
-// block (which must have synchronised after writing agg).  xch and bars hold two turns' worth: a
-// block sends turn k + 2's only when it has turn k + 1's from every peer, each of which sent it
-// behind its last read of turn k's.  lost: a wait ran out; the block goes on without waiting.
+// The state before every warp's runs, along the scan's direction, by one warp (lane = channel).
+// agg: the block's warps' (A, H); carry: the state at the cluster's turn start, which every block
+// holds alike and moves on by the turn.  xch and bars hold two turns' worth: a block sends turn
+// k + 2's only when it has turn k + 1's from every peer, each of which sent it behind its last
+// read of turn k's.  lost: a wait ran out (status word); the block goes on without waiting.
 template <bool UP>
-__device__ __forceinline__ void tile_start(const float2 (*agg)[CH], float2 (*xch)[CH], uint64_t* bars, float* start,
-                                           float& carry, bool& lost, int k, int rank, int ncl) {
-    const int c = threadIdx.x & (CH - 1), q = threadIdx.x / CH;
-    float A = 1.f, H = 0.f;
+__device__ __forceinline__ void warp_starts(const float2 (*agg)[CH], float2 (*xch)[CH], uint64_t* bars,
+                                            float (*start)[CH], float& carry, bool& lost, int k, int rank, int ncl) {
+    const int c = threadIdx.x & 31;
+    float2 e[WT];
 #pragma unroll
-    for (int w = 0; w < WT; ++w) {
-        const float2 e = agg[UP ? w : WT - 1 - w][c];
-        H = fmaf(e.x, H, e.y);
-        A *= e.x;
-    }
+    for (int w = 0; w < WT; ++w) e[w] = agg[UP ? w : WT - 1 - w][c];
+    float s = carry;
     if (ncl > 1) {
+        float A = 1.f, H = 0.f;
+#pragma unroll
+        for (int w = 0; w < WT; ++w) { H = fmaf(e[w].x, H, e[w].y); A *= e[w].x; }
         xch += (k & 1) * ncl;
         uint64_t* bar = bars + (k & 1);
-        if (threadIdx.x == 0) expect_bytes(bar, (uint32_t)(ncl * CH * sizeof(float2)));
-        for (int r = q; r < ncl; r += NT / CH) store_peer(&xch[rank][c], make_float2(A, H), bar, r);
-        if (q == 0) {
-            if (!lost) lost = !wait_phase(bar, (uint32_t)(k >> 1) & 1u);
-            float s = carry;
-            for (int i = 0; i < ncl; ++i) {
-                const int r = UP ? i : ncl - 1 - i;
-                if (r == rank) start[c] = s;
-                const float2 e = xch[r][c];
-                s = fmaf(e.x, s, e.y);
-            }
-            carry = s;
+        if (c == 0) expect_bytes(bar, (uint32_t)(ncl * CH * sizeof(float2)));
+        for (int r = 0; r < ncl; ++r) store_peer(&xch[rank][c], make_float2(A, H), bar, r);
+        if (!lost) lost = !wait_phase(bar, (uint32_t)(k >> 1) & 1u);
+        float all = carry;
+        for (int i = 0; i < ncl; ++i) {
+            const int r = UP ? i : ncl - 1 - i;
+            if (r == rank) s = all;
+            const float2 x = xch[r][c];
+            all = fmaf(x.x, all, x.y);
         }
-    } else if (q == 0) {
-        start[c] = carry;
-        carry = fmaf(A, carry, H);
+        carry = all;
     }
-    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < WT; ++w) {
+        start[UP ? w : WT - 1 - w][c] = s;
+        s = fmaf(e[w].x, s, e[w].y);
+    }
+    if (ncl == 1) carry = s;
 }
 
-// Before the first turn: the barriers, and the peers' shared memory exists.
-__device__ __forceinline__ void exchange_begin(uint64_t* bars, int ncl) {
-    if (ncl == 1) return;
+// Before the first turn: the barriers (n of them), and the peers' shared memory exists.
+__device__ __forceinline__ void barriers_begin(uint64_t* bars, int n, int ncl) {
     if (threadIdx.x == 0) {
-        tc::mbar_init(&bars[0], 1);
-        tc::mbar_init(&bars[1], 1);
+        for (int i = 0; i < n; ++i) tc::mbar_init(&bars[i], 1);
         tc::fence_mbar_init();
     }
-    cluster_sync();
+    if (ncl > 1) cluster_sync();
+    else __syncthreads();
 }
 
-// The state before this thread's run: the tile's start through the warps before it and the
-// runs before it in its warp.
-template <int V, bool UP>
-__device__ __forceinline__ void run_start(const float2 (*agg)[CH], const float* start, const float (&exA)[V],
-                                          const float (&exH)[V], int warp_t, int c, float (&s)[V]) {
+// The state before this thread's run: its warp's start through the runs before it.
+template <int V>
+__device__ __forceinline__ void run_start(const float* start, const float (&exA)[V], const float (&exH)[V], float (&s)[V]) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) s[i] = start[c + i];
-#pragma unroll
-    for (int w = 0; w < WT - 1; ++w) {
-        const int at = UP ? w : WT - 1 - w;
-        if (UP ? at < warp_t : at > warp_t) {
-#pragma unroll
-            for (int i = 0; i < V; ++i) { const float2 e = agg[at][c + i]; s[i] = fmaf(e.x, s[i], e.y); }
-        }
-    }
-#pragma unroll
-    for (int i = 0; i < V; ++i) s[i] = fmaf(exA[i], s[i], exH[i]);
+    for (int i = 0; i < V; ++i) s[i] = fmaf(exA[i], start[i], exH[i]);
 }
+
+// The tensor maps of a call ({D, 1, T, B}, boxes of CH channels x TOK tokens).
+struct ScanMaps { CUtensorMap x, g, dh; };
 
 constexpr int FWD_ELEMS = 32;           // elements of a thread: 2 registers each (decay, input)
 constexpr int BWD_ELEMS = 16;           // 5 registers each
 
 template <typename XT, typename GT, int V> struct FwdSmem {
-    static constexpr int R = FWD_ELEMS / V;
-    typename Pack<GT, V>::Raw g[V > 1 ? STAGES : 1][V > 1 ? R : 1][V > 1 ? NT : 1];
-    typename Pack<XT, V>::Raw x[V > 1 ? STAGES : 1][V > 1 ? R : 1][V > 1 ? NT : 1];
-    float2 agg[2][WT][CH];
-    float start[CH];
-    uint64_t bars[2];
+    static constexpr int TOK = Tile<V, FWD_ELEMS>::TOK, N = V > 1 ? STAGES : 1;
+    alignas(128) GT g[N][V > 1 ? TOK : 1][CH];
+    alignas(128) XT x[N][V > 1 ? TOK : 1][CH];
+    float2 agg[WT][CH];
+    float start[WT][CH];
+    uint64_t bars[2 + STAGES];          // the exchange's, the stages'
     float2 xch[1][CH];                  // [2][cluster][CH]: the launch adds the rest
 };
 
 template <typename XT, typename GT, typename OT, int V>
-__global__ void __launch_bounds__(NT, 2) scan_fwd_kernel(ScanParams p) {
+__global__ void __launch_bounds__(NT, 2) scan_fwd_kernel(ScanParams p, const __grid_constant__ ScanMaps maps) {
     using L = Tile<V, FWD_ELEMS>;
     using S = FwdSmem<XT, GT, V>;
     constexpr int R = L::R;
-    extern __shared__ __align__(16) unsigned char raw[];
+    extern __shared__ __align__(128) unsigned char raw[];
     S& sm = *reinterpret_cast<S*>(raw);
     const L l;
     const int rank = (int)cluster_rank(), ncl = (int)cluster_size();
@@ -301,42 +260,42 @@ __global__ void __launch_bounds__(NT, 2) scan_fwd_kernel(ScanParams p) {
     const GT* g = static_cast<const GT*>(p.g) + (size_t)b * p.T * p.g_row + c;
     OT* h = static_cast<OT*>(p.h) + (size_t)b * p.T * p.D + c;
     const int turn = L::TOK * ncl, turns = (p.T + turn - 1) / turn;
-    const int first = rank * L::TOK + l.first_token();    // this thread's run in turn 0
+    const int tile = rank * L::TOK, first = tile + l.first_token();     // of turn 0: this block's, this thread's
+    bool lost = false;
 
-    auto fetch = [&](int k) {                             // turn k's inputs of this thread
-        if constexpr (V > 1) {
-            if (k < turns) {
-                const int t = k * turn + first, have = on ? len - t : 0;
-                copy_run<GT, V, R>(smem_addr(&sm.g[k % STAGES][0][threadIdx.x]), g + t * p.g_row, p.g_row, have, p.g);
-                copy_run<XT, V, R>(smem_addr(&sm.x[k % STAGES][0][threadIdx.x]), x + t * p.x_row, p.x_row, have, p.x);
-            }
-            copy_commit();
-        }
+    barriers_begin(sm.bars, 2 + STAGES, ncl);
+    auto fetch = [&](int k) {                             // turn k's tile, unless it lies behind the sequence
+        const int t = k * turn + tile;
+        if (V == 1 || threadIdx.x != 0 || k >= turns || t >= len) return;
+        uint64_t* bar = &sm.bars[2 + k % STAGES];
+        expect_bytes(bar, sizeof(sm.g[0]) + sizeof(sm.x[0]));
+        tc::tma_load_4d(smem_addr(sm.g[k % STAGES]), &maps.g, c0, 0, t, b, bar);
+        tc::tma_load_4d(smem_addr(sm.x[k % STAGES]), &maps.x, c0, 0, t, b, bar);
     };
 #pragma unroll
     for (int k = 0; k < STAGES; ++k) fetch(k);
 
-    float carry = 0.f;
+    float carry = 0.f;                                    // of warp 0: the state at the turn's start
     if (threadIdx.x < CH && c0 + (int)threadIdx.x < p.D && p.h0) carry = p.h0[(size_t)b * p.D + c0 + threadIdx.x];
 
-    bool lost = false;
-    exchange_begin(sm.bars, ncl);
     for (int k = 0; k < turns; ++k) {
         const int t0 = k * turn + first;
         float a[R][V], bb[R][V], A[V], H[V], exA[V], exH[V];
         if constexpr (V > 1) {
-            copy_wait<STAGES - 1>();
+            if (k * turn + tile < len) {
+                if (!lost) lost = !wait_phase(&sm.bars[2 + k % STAGES], (uint32_t)(k / STAGES) & 1u);
 #pragma unroll
-            for (int r = 0; r < R; ++r) {
-                Pack<GT, V>::get(sm.g[k % STAGES][r][threadIdx.x], a[r]);
-                Pack<XT, V>::get(sm.x[k % STAGES][r][threadIdx.x], bb[r]);
+                for (int r = 0; r < R; ++r) {
+                    Pack<GT, V>::get(*reinterpret_cast<const typename Pack<GT, V>::Raw*>(&sm.g[k % STAGES][l.first_token() + r][l.c]), a[r]);
+                    Pack<XT, V>::get(*reinterpret_cast<const typename Pack<XT, V>::Raw*>(&sm.x[k % STAGES][l.first_token() + r][l.c]), bb[r]);
+                }
             }
         } else {
 #pragma unroll
             for (int r = 0; r < R; ++r) {
                 const bool in = on && t0 + r < len;
-                a[r][0] = in ? ld_f32(g + (size_t)(t0 + r) * p.g_row) : 0.f;
-                bb[r][0] = in ? ld_f32(x + (size_t)(t0 + r) * p.x_row) : 0.f;
+                a[r][0] = in ? ld_f32(g + (t0 + r) * p.g_row) : 0.f;
+                bb[r][0] = in ? ld_f32(x + (t0 + r) * p.x_row) : 0.f;
             }
         }
         with_mode(p, [&](auto mode, auto tied) {
@@ -370,22 +329,20 @@ __global__ void __launch_bounds__(NT, 2) scan_fwd_kernel(ScanParams p) {
             }
         }
         warp_runs<V, L::LC, L::TL, true>(A, H, exA, exH, l.lane_t);
-        float2 (*agg)[CH] = sm.agg[k & 1];
         if (l.lane_t == L::TL - 1) {
 #pragma unroll
-            for (int i = 0; i < V; ++i) agg[l.warp_t][l.c + i] = make_float2(A[i], H[i]);
+            for (int i = 0; i < V; ++i) sm.agg[l.warp][l.c + i] = make_float2(A[i], H[i]);
         }
         __syncthreads();
-        fetch(k + STAGES);                                // the slots of turn k are in registers
-        tile_start<true>(agg, sm.xch, sm.bars, sm.start, carry, lost, k, rank, ncl);
+        fetch(k + STAGES);                                // the stage of turn k is in registers
+        if (l.warp == 0) warp_starts<true>(sm.agg, sm.xch, sm.bars, sm.start, carry, lost, k, rank, ncl);
+        __syncthreads();
         float s[V];
-        run_start<V, true>(agg, sm.start, exA, exH, l.warp_t, l.c, s);
+        run_start<V>(&sm.start[l.warp][l.c], exA, exH, s);
         if (on && p.ckpt && t0 % CKPT == 0 && t0 < p.T) {
             float* ck = p.ckpt + ((size_t)b * nck + t0 / CKPT) * p.D + c;
-            if (GDR_INB(t0 / CKPT < nck && c + V <= p.D, 801)) {
-                if constexpr (V == 4) *reinterpret_cast<float4*>(ck) = make_float4(s[0], s[1], s[2], s[3]);
-                else ck[0] = s[0];
-            }
+            if (GDR_INB(t0 / CKPT < nck && c + V <= p.D, 801))
+                *reinterpret_cast<typename Pack<float, V>::Raw*>(ck) = Pack<float, V>::put(s);
         }
         OT* out = h + (size_t)t0 * p.D;
         if (on && whole) {
@@ -418,27 +375,27 @@ __global__ void __launch_bounds__(NT, 2) scan_fwd_kernel(ScanParams p) {
 }
 
 template <typename XT, typename GT, typename OT, int V> struct BwdSmem {
-    static constexpr int R = BWD_ELEMS / V;
-    typename Pack<GT, V>::Raw g[V > 1 ? STAGES : 1][V > 1 ? R : 1][V > 1 ? NT : 1];
-    typename Pack<XT, V>::Raw x[V > 1 ? STAGES : 1][V > 1 ? R : 1][V > 1 ? NT : 1];
-    typename Pack<OT, V>::Raw dh[V > 1 ? STAGES : 1][V > 1 ? R : 1][V > 1 ? NT : 1];
-    float ck[STAGES][CH];
-    float2 up[2][WT][CH];
-    float2 down[2][WT][CH];
-    float start[CH];
-    uint64_t bars[2];
-    float2 xch[1][CH];                  // [2][cluster][CH]: the launch adds the rest
+    static constexpr int TOK = Tile<V, BWD_ELEMS>::TOK, N = V > 1 ? STAGES : 1;
+    alignas(128) GT g[N][V > 1 ? TOK : 1][CH];
+    alignas(128) XT x[N][V > 1 ? TOK : 1][CH];
+    alignas(128) OT dh[N][V > 1 ? TOK : 1][CH];
+    float2 up[WT][CH];
+    float2 down[WT][CH];
+    float before[WT][CH];
+    float start[WT][CH];
+    uint64_t bars[2 + STAGES];
+    float2 xch[1][CH];
 };
 
-// The states inside a tile come from its checkpoint (a block's tile is CKPT tokens), so only the
-// gradient's direction goes through the cluster.
+// The states inside a tile come from the checkpoint at its first token (a tile is a whole number of
+// CKPT tokens), so only the gradient's direction goes through the cluster.
 template <typename XT, typename GT, typename OT, int V>
-__global__ void __launch_bounds__(NT, 2) scan_bwd_kernel(ScanParams p) {
+__global__ void __launch_bounds__(NT, 2) scan_bwd_kernel(ScanParams p, const __grid_constant__ ScanMaps maps) {
     using L = Tile<V, BWD_ELEMS>;
     using S = BwdSmem<XT, GT, OT, V>;
     constexpr int R = L::R;
-    static_assert(L::TOK == CKPT, "a tile starts at a checkpoint");
-    extern __shared__ __align__(16) unsigned char raw[];
+    static_assert(L::TOK % CKPT == 0, "a tile starts at a checkpoint");
+    extern __shared__ __align__(128) unsigned char raw[];
     S& sm = *reinterpret_cast<S*>(raw);
     const L l;
     const int rank = (int)cluster_rank(), ncl = (int)cluster_size();
@@ -451,60 +408,61 @@ __global__ void __launch_bounds__(NT, 2) scan_bwd_kernel(ScanParams p) {
     XT* dx = static_cast<XT*>(p.dx) + (size_t)b * p.T * p.D + c;
     GT* dg = static_cast<GT*>(p.dg) + (size_t)b * p.T * p.D + c;
     const int turn = L::TOK * ncl, turns = (p.T + turn - 1) / turn;
-    const int first = rank * L::TOK + l.first_token();
+    const int tile = rank * L::TOK, first = tile + l.first_token();
     const bool with_dh = p.dh != nullptr;
+    bool lost = false;
 
-    // turn k walks from the end: its tokens start at (turns - 1 - k) * turn
+    barriers_begin(sm.bars, 2 + STAGES, ncl);
+    // turn k walks from the end: its tokens start at (turns - 1 - k) * turn.  Tiles behind the
+    // sequence are not fetched, so the stages count the fetched ones, from turn `skip` on.
+    const int live = (len - tile + turn - 1) / turn;      // turns of this block with tokens (len > tile), else <= 0
+    const int skip = turns - max(live, 0);
     auto fetch = [&](int k) {
-        if (k < turns) {
-            const int base = (turns - 1 - k) * turn;
-            if constexpr (V > 1) {
-                const int t = base + first, have = on ? len - t : 0;
-                copy_run<GT, V, R>(smem_addr(&sm.g[k % STAGES][0][threadIdx.x]), g + t * p.g_row, p.g_row, have, p.g);
-                copy_run<XT, V, R>(smem_addr(&sm.x[k % STAGES][0][threadIdx.x]), x + t * p.x_row, p.x_row, have, p.x);
-                copy_run<OT, V, R>(smem_addr(&sm.dh[k % STAGES][0][threadIdx.x]), dh + (size_t)t * p.D, p.D,
-                                   with_dh ? have : 0, p.ckpt);
-            }
-            // the tile's checkpoint; read behind the turn's first barrier
-            const int j = base / CKPT + rank;
-            if constexpr (V > 1) {
-                if (threadIdx.x < CH / 4) {
-                    const bool in = j < nck && c0 + (int)threadIdx.x * 4 < p.D;
-                    copy_async<16>(smem_addr(&sm.ck[k % STAGES][threadIdx.x * 4]),
-                                   in ? p.ckpt + ((size_t)b * nck + j) * p.D + c0 + threadIdx.x * 4 : p.ckpt, in);
-                }
-            } else if (threadIdx.x < CH) {
-                const bool in = j < nck && c0 + (int)threadIdx.x < p.D;
-                sm.ck[k % STAGES][threadIdx.x] = in ? p.ckpt[((size_t)b * nck + j) * p.D + c0 + threadIdx.x] : 0.f;
-            }
-        }
-        if constexpr (V > 1) copy_commit();
+        if (V == 1 || threadIdx.x != 0 || k < skip || k >= turns) return;
+        const int t = (turns - 1 - k) * turn + tile, st = (k - skip) % STAGES;
+        uint64_t* bar = &sm.bars[2 + st];
+        expect_bytes(bar, sizeof(sm.g[0]) + sizeof(sm.x[0]) + (with_dh ? sizeof(sm.dh[0]) : 0));
+        tc::tma_load_4d(smem_addr(sm.g[st]), &maps.g, c0, 0, t, b, bar);
+        tc::tma_load_4d(smem_addr(sm.x[st]), &maps.x, c0, 0, t, b, bar);
+        if (with_dh) tc::tma_load_4d(smem_addr(sm.dh[st]), &maps.dh, c0, 0, t, b, bar);
     };
 #pragma unroll
-    for (int k = 0; k < STAGES; ++k) fetch(k);
+    for (int k = 0; k < STAGES; ++k) fetch(skip + k);
 
-    float carry = 0.f;
+    float carry = 0.f;                                    // of warp 0: a_{t+1} lam_{t+1} behind the turn
     if (threadIdx.x < CH && c0 + (int)threadIdx.x < p.D && p.dh_T) carry = p.dh_T[(size_t)b * p.D + c0 + threadIdx.x];
 
-    bool lost = false;
-    exchange_begin(sm.bars, ncl);
     for (int k = 0; k < turns; ++k) {
-        const int t0 = (turns - 1 - k) * turn + first;
+        const int base = (turns - 1 - k) * turn, t0 = base + first;
+        // of warp 1: the state before the tile
+        float state = 0.f;
+        if (l.warp == 1) {
+            const int j = (base + tile) / CKPT, ch = c0 + (threadIdx.x & 31);
+            if (j < nck && ch < p.D) state = p.ckpt[((size_t)b * nck + j) * p.D + ch];
+        }
         float a[R][V], rest[R][V], xv[R][V], d[R][V];
         if constexpr (V > 1) {
-            copy_wait<STAGES - 1>();
+            if (k >= skip) {
+                const int st = (k - skip) % STAGES;
+                if (!lost) lost = !wait_phase(&sm.bars[2 + st], (uint32_t)((k - skip) / STAGES) & 1u);
 #pragma unroll
-            for (int r = 0; r < R; ++r) {
-                Pack<GT, V>::get(sm.g[k % STAGES][r][threadIdx.x], a[r]);
-                Pack<XT, V>::get(sm.x[k % STAGES][r][threadIdx.x], xv[r]);
-                Pack<OT, V>::get(sm.dh[k % STAGES][r][threadIdx.x], d[r]);
+                for (int r = 0; r < R; ++r) {
+                    const int t = l.first_token() + r;
+                    Pack<GT, V>::get(*reinterpret_cast<const typename Pack<GT, V>::Raw*>(&sm.g[st][t][l.c]), a[r]);
+                    Pack<XT, V>::get(*reinterpret_cast<const typename Pack<XT, V>::Raw*>(&sm.x[st][t][l.c]), xv[r]);
+                    if (with_dh) Pack<OT, V>::get(*reinterpret_cast<const typename Pack<OT, V>::Raw*>(&sm.dh[st][t][l.c]), d[r]);
+                    else {
+#pragma unroll
+                        for (int i = 0; i < V; ++i) d[r][i] = 0.f;
+                    }
+                }
             }
         } else {
 #pragma unroll
             for (int r = 0; r < R; ++r) {
                 const bool in = on && t0 + r < len;
-                a[r][0] = in ? ld_f32(g + (size_t)(t0 + r) * p.g_row) : 0.f;
-                xv[r][0] = in ? ld_f32(x + (size_t)(t0 + r) * p.x_row) : 0.f;
+                a[r][0] = in ? ld_f32(g + (t0 + r) * p.g_row) : 0.f;
+                xv[r][0] = in ? ld_f32(x + (t0 + r) * p.x_row) : 0.f;
                 d[r][0] = in && with_dh ? ld_f32(dh + (size_t)(t0 + r) * p.D) : 0.f;
             }
         }
@@ -526,7 +484,7 @@ __global__ void __launch_bounds__(NT, 2) scan_bwd_kernel(ScanParams p) {
             for (int r = 0; r < R; ++r) {
 #pragma unroll
                 for (int i = 0; i < V; ++i)
-                    if (t0 + r >= len) { a[r][i] = 1.f; rest[r][i] = 0.f; }
+                    if (t0 + r >= len) { a[r][i] = 1.f; rest[r][i] = 0.f; xv[r][i] = 0.f; d[r][i] = 0.f; }
             }
         }
 #pragma unroll
@@ -550,15 +508,20 @@ __global__ void __launch_bounds__(NT, 2) scan_bwd_kernel(ScanParams p) {
         warp_runs<V, L::LC, L::TL, false>(dA, M, exD, exM, l.lane_t);
         if (l.lane_t == L::TL - 1) {
 #pragma unroll
-            for (int i = 0; i < V; ++i) sm.up[k & 1][l.warp_t][l.c + i] = make_float2(A[i], H[i]);
+            for (int i = 0; i < V; ++i) sm.up[l.warp][l.c + i] = make_float2(A[i], H[i]);
         }
         if (l.lane_t == 0) {
 #pragma unroll
-            for (int i = 0; i < V; ++i) sm.down[k & 1][l.warp_t][l.c + i] = make_float2(dA[i], M[i]);
+            for (int i = 0; i < V; ++i) sm.down[l.warp][l.c + i] = make_float2(dA[i], M[i]);
         }
         __syncthreads();
+        if (k >= skip) fetch(k + STAGES);                 // the stage of turn k is in registers
+        if (l.warp == 0) warp_starts<false>(sm.down, sm.xch, sm.bars, sm.start, carry, lost, k, rank, ncl);
+        else if (l.warp == 1) warp_starts<true>(sm.up, nullptr, nullptr, sm.before, state, lost, k, 0, 1);
+        __syncthreads();
         float s[V], m[V], before[R][V];
-        run_start<V, true>(sm.up[k & 1], sm.ck[k % STAGES], exA, exH, l.warp_t, l.c, s);
+        run_start<V>(&sm.before[l.warp][l.c], exA, exH, s);
+        run_start<V>(&sm.start[l.warp][l.c], exD, exM, m);
 #pragma unroll
         for (int r = 0; r < R; ++r) {
 #pragma unroll
@@ -567,12 +530,9 @@ __global__ void __launch_bounds__(NT, 2) scan_bwd_kernel(ScanParams p) {
                 s[i] = fmaf(a[r][i], s[i], p.tied ? rest[r][i] * xv[r][i] : xv[r][i]);
             }
         }
-        tile_start<false>(sm.down[k & 1], sm.xch, sm.bars, sm.start, carry, lost, k, rank, ncl);
-        fetch(k + STAGES);                                // behind the barrier: the checkpoint's slot is read
-        run_start<V, false>(sm.down[k & 1], sm.start, exD, exM, l.warp_t, l.c, m);
         // the gradient of the gate: lam (h_{t-1} - [tied] x) a', a' = a or -a (1 - a)
-        XT* out_x = dx + (size_t)t0 * p.D + (size_t)(R - 1) * p.D;
-        GT* out_g = dg + (size_t)t0 * p.D + (size_t)(R - 1) * p.D;
+        XT* out_x = dx + (size_t)(t0 + R - 1) * p.D;
+        GT* out_g = dg + (size_t)(t0 + R - 1) * p.D;
         with_mode(p, [&](auto mode, auto tied) {
 #pragma unroll
             for (int r = R - 1; r >= 0; --r) {
