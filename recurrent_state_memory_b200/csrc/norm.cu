@@ -5,153 +5,134 @@
 #include "gdr.h"
 #include "host.cuh"
 #include "common.cuh"
+#include "norm.cuh"
 
 namespace gdr {
 namespace lnm {
 
-struct NormParams {
-    long long rows;
-    int D;
-    float eps;
-    const void* x;
-    const void* dy;
-    const void* weight;
-    const void* bias;
-    void* y;
-    void* dx;
-    float* mean;
-    float* rstd;
-    float* part_w;          // [parts, D] each block's share of dweight / dbias
-    float* part_b;
-    float* dweight;
-    float* dbias;
-    int parts;
-};
+// How a row of D elements is held: V elements a load, N loads a lane, `group` lanes of a warp or a
+// block of `block` threads; N = 0: the row is too long for a block's registers.
+struct Plan { int V, N, block, group; };
 
-constexpr int NT = 256;
-constexpr int PARTS = 296;
-
-__device__ __forceinline__ float block_sum(float v, float* sm) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) sm[threadIdx.x >> 5] = v;
-    __syncthreads();
-    float s = 0.f;
-#pragma unroll
-    for (int i = 0; i < NT / 32; ++i) s += sm[i];
-    return s;
-}
-
-// One block per row, three passes over it.
-template <typename XT, typename YT, typename WT>
-__global__ void __launch_bounds__(NT) norm_fwd_kernel(NormParams p) {
-    __shared__ float sm[NT / 32];
-    const float inv = 1.f / (float)p.D;
-    for (long long r = blockIdx.x; r < p.rows; r += gridDim.x) {
-        const XT* x = static_cast<const XT*>(p.x) + (size_t)r * p.D;
-        YT* y = static_cast<YT*>(p.y) + (size_t)r * p.D;
-        float s = 0.f;
-        for (int c = threadIdx.x; c < p.D; c += NT) s += ld_f32(x + c);
-        const float mean = block_sum(s, sm) * inv;
-        s = 0.f;
-        for (int c = threadIdx.x; c < p.D; c += NT) { const float v = ld_f32(x + c) - mean; s = fmaf(v, v, s); }
-        const float rstd = 1.f / sqrtf(block_sum(s, sm) * inv + p.eps);
-        for (int c = threadIdx.x; c < p.D; c += NT) {
-            float v = (ld_f32(x + c) - mean) * rstd;
-            if (p.weight) v *= ld_f32(static_cast<const WT*>(p.weight) + c);
-            if (p.bias) v += ld_f32(static_cast<const WT*>(p.bias) + c);
-            st_from_f32(y + c, v);
-        }
-        if (threadIdx.x == 0) {
-            if (p.mean) p.mean[r] = mean;
-            if (p.rstd) p.rstd[r] = rstd;
-        }
+// A warp while a lane holds at most 32 elements (backward: 8, since it also holds dy and two sums),
+// then a block: in the forward the smallest one whose threads hold the row in 32 elements each
+// (the more loads a thread has in flight the better), in the backward one whose threads hold it
+// in 8, or 16 for one-element loads.
+static Plan plan_of(int D, int V, bool bwd) {
+    Plan q{V, 0, 0, 32};
+    const int nv = (D + V - 1) / V;             // loads of a row
+    if (nv <= 32) {                             // one load a lane, as few lanes as hold the row
+        q.N = 1;
+        for (q.group = 1; q.group < nv; q.group *= 2) {}
+        return q;
     }
-}
-
-template <typename XT, typename YT, typename WT>
-__global__ void __launch_bounds__(NT) norm_dx_kernel(NormParams p) {
-    __shared__ float sm[NT / 32];
-    const float inv = 1.f / (float)p.D;
-    for (long long r = blockIdx.x; r < p.rows; r += gridDim.x) {
-        const XT* x = static_cast<const XT*>(p.x) + (size_t)r * p.D;
-        const YT* dy = static_cast<const YT*>(p.dy) + (size_t)r * p.D;
-        const float mean = p.mean[r], rstd = p.rstd[r];
-        float s1 = 0.f, s2 = 0.f;
-        for (int c = threadIdx.x; c < p.D; c += NT) {
-            const float w = p.weight ? ld_f32(static_cast<const WT*>(p.weight) + c) : 1.f;
-            const float wd = w * ld_f32(dy + c);
-            s1 += wd;
-            s2 = fmaf(wd, (ld_f32(x + c) - mean) * rstd, s2);
-        }
-        s1 = block_sum(s1, sm) * inv;
-        s2 = block_sum(s2, sm) * inv;
-        XT* dx = static_cast<XT*>(p.dx) + (size_t)r * p.D;
-        for (int c = threadIdx.x; c < p.D; c += NT) {
-            const float w = p.weight ? ld_f32(static_cast<const WT*>(p.weight) + c) : 1.f;
-            const float xh = (ld_f32(x + c) - mean) * rstd;
-            st_from_f32(dx + c, rstd * (w * ld_f32(dy + c) - s1 - xh * s2));
-        }
+    const int most = (bwd ? V == 1 ? 16 : 8 : 32) / V;
+    for (int n = 2; n <= (V == 1 ? 16 : most); n *= 2)
+        if (nv <= 32 * n) { q.N = n; return q; }
+    for (int block : {128, 256, 512, 1024}) {
+        if (block == 1024 && (!bwd || V == 1)) break;
+        for (int n = V == 1 ? 8 : bwd ? most : 1; n <= most; n *= 2)
+            if (nv <= block * n) { q.block = block; q.N = n; return q; }
     }
+    return q;
+}
+static int vector_of(const gdr_norm_desc* d) {  // elements of a load: 16 bytes, where every row starts on them
+    const int V = d->x_dtype == GDR_BF16 && d->y_dtype == GDR_BF16 ? 8 : 4;
+    return d->D % V == 0 ? V : 1;
 }
 
-// Rows part, part + parts, .. of one column per thread.
-template <typename XT, typename YT>
-__global__ void __launch_bounds__(NT) norm_part_kernel(NormParams p) {
-    const int c = blockIdx.x * NT + threadIdx.x;
-    if (c >= p.D) return;
-    float w = 0.f, b = 0.f;
-    for (long long r = blockIdx.y; r < p.rows; r += p.parts) {
-        const float dy = ld_f32(static_cast<const YT*>(p.dy) + (size_t)r * p.D + c);
-        w = fmaf(dy, (ld_f32(static_cast<const XT*>(p.x) + (size_t)r * p.D + c) - p.mean[r]) * p.rstd[r], w);
-        b += dy;
-    }
-    if (p.part_w) p.part_w[(size_t)blockIdx.y * p.D + c] = w;
-    if (p.part_b) p.part_b[(size_t)blockIdx.y * p.D + c] = b;
-}
-
-__global__ void __launch_bounds__(NT) norm_sum_kernel(NormParams p) {
-    const int c = blockIdx.x * NT + threadIdx.x;
-    if (c >= p.D) return;
-    float w = 0.f, b = 0.f;
-    for (int i = 0; i < p.parts; ++i) {
-        if (p.part_w) w += p.part_w[(size_t)i * p.D + c];
-        if (p.part_b) b += p.part_b[(size_t)i * p.D + c];
-    }
-    if (p.dweight) p.dweight[c] = w;
-    if (p.dbias) p.dbias[c] = b;
-}
-
-static unsigned row_grid(const NormParams& p) {
-    const long long cap = (long long)device_sm_count() * 8;
-    return (unsigned)(p.rows < cap ? p.rows : cap);
-}
-
-template <typename XT, typename YT, typename WT>
-static gdr_status launch(bool bwd, const NormParams& p, cudaStream_t st) {
-    if (!bwd) norm_fwd_kernel<XT, YT, WT><<<row_grid(p), NT, 0, st>>>(p);
-    else {
-        if (p.dx && p.rows > 0) norm_dx_kernel<XT, YT, WT><<<row_grid(p), NT, 0, st>>>(p);
-        if (p.dweight || p.dbias) {
-            const unsigned cols = (unsigned)((p.D + NT - 1) / NT);
-            norm_part_kernel<XT, YT><<<dim3(cols, p.parts), NT, 0, st>>>(p);
-            norm_sum_kernel<<<cols, NT, 0, st>>>(p);
-        }
+template <typename XT, typename YT, int V, int N, int BLOCK, bool BWD>
+static gdr_status launch_one(const NormParams& p, cudaStream_t st) {
+    constexpr int NTH = threads<BLOCK>();
+    const long long per = BLOCK ? 1 : WARP_NT / p.group;
+    if constexpr (!BWD) {
+        const long long blocks = (p.rows + per - 1) / per, cap = (long long)device_sm_count() * (2048 / NTH);
+        norm_fwd_kernel<XT, YT, V, N, BLOCK><<<(unsigned)(blocks < cap ? blocks : cap), NTH, 0, st>>>(p);
+    } else {
+        // the groups' sums in turn: at most 256 threads x 16 columns
+        const size_t smem = BLOCK || !(p.part_w || p.part_b) ? 0 : (size_t)per * p.D * sizeof(float);
+        norm_bwd_kernel<XT, YT, V, N, BLOCK><<<p.parts, NTH, smem, st>>>(p);
     }
     const cudaError_t e = cudaGetLastError();
     return e == cudaSuccess ? GDR_OK : cuda_fail(e, "launch(layer norm)");
 }
-template <typename XT, typename YT>
-static gdr_status launch_w(const gdr_norm_desc* d, bool bwd, const NormParams& p, cudaStream_t st) {
-    return d->w_dtype == GDR_BF16 ? launch<XT, YT, __nv_bfloat16>(bwd, p, st) : launch<XT, YT, float>(bwd, p, st);
+
+// The kernels that plan_of reaches.
+template <typename XT, typename YT, int V>
+static gdr_status launch_plan(bool bwd, const Plan& q, const NormParams& p, cudaStream_t st) {
+#define GDR_NORM(way, n, blk) \
+    if (bwd == way && q.N == n && q.block == blk) return launch_one<XT, YT, V, n, blk, way>(p, st)
+    GDR_NORM(false, 1, 0); GDR_NORM(true, 1, 0);
+    GDR_NORM(false, 2, 0); GDR_NORM(false, 4, 0);
+    if constexpr (V == 8) {
+        GDR_NORM(false, 2, 128); GDR_NORM(false, 4, 128); GDR_NORM(false, 4, 256); GDR_NORM(false, 4, 512);
+        GDR_NORM(true, 1, 128); GDR_NORM(true, 1, 256); GDR_NORM(true, 1, 512); GDR_NORM(true, 1, 1024);
+    } else if constexpr (V == 4) {
+        GDR_NORM(false, 8, 0);
+        GDR_NORM(false, 4, 128); GDR_NORM(false, 8, 128); GDR_NORM(false, 8, 256); GDR_NORM(false, 8, 512);
+        GDR_NORM(true, 2, 0);
+        GDR_NORM(true, 2, 128); GDR_NORM(true, 2, 256); GDR_NORM(true, 2, 512); GDR_NORM(true, 2, 1024);
+    } else {
+        GDR_NORM(false, 8, 0); GDR_NORM(false, 16, 0);
+        GDR_NORM(false, 8, 128); GDR_NORM(false, 16, 128); GDR_NORM(false, 32, 128); GDR_NORM(false, 32, 256);
+        GDR_NORM(false, 32, 512);
+        GDR_NORM(true, 2, 0); GDR_NORM(true, 4, 0); GDR_NORM(true, 8, 0); GDR_NORM(true, 16, 0);
+        GDR_NORM(true, 8, 128); GDR_NORM(true, 16, 128); GDR_NORM(true, 16, 256); GDR_NORM(true, 16, 512);
+    }
+#undef GDR_NORM
+    return fail(GDR_ERR_UNSUPPORTED, "layer norm: no kernel for this plan%s");
 }
-static gdr_status dispatch(const gdr_norm_desc* d, bool bwd, const NormParams& p, cudaStream_t st) {
+
+template <typename XT, typename YT>
+static gdr_status launch(const gdr_norm_desc* d, bool bwd, NormParams& p, cudaStream_t st) {
+    constexpr int V = sizeof(XT) == 2 && sizeof(YT) == 2 ? 8 : 4;
+    const Plan q = plan_of(p.D, vector_of(d), bwd);
+    p.group = q.group;
+    p.w_bf16 = d->w_dtype == GDR_BF16;
+    gdr_status s = GDR_OK;
+    if (p.rows > 0) {
+        if (q.N) s = q.V > 1 ? launch_plan<XT, YT, V>(bwd, q, p, st) : launch_plan<XT, YT, 1>(bwd, q, p, st);
+        else {
+            const unsigned grid = (unsigned)(p.rows < 2 * device_sm_count() ? p.rows : 2 * device_sm_count());
+            if (!bwd) norm_fwd_long_kernel<XT, YT><<<grid, LONG_NT, 0, st>>>(p);
+            else {
+                if (p.dx) norm_dx_long_kernel<XT, YT><<<grid, LONG_NT, 0, st>>>(p);
+                if (p.part_w || p.part_b)
+                    norm_part_long_kernel<XT, YT><<<dim3((unsigned)((p.D + 255) / 256), p.parts), 256, 0, st>>>(p);
+            }
+        }
+    }
+    if (s == GDR_OK && bwd && (p.dweight || p.dbias)) {
+        if (p.rows > 0) {
+            const unsigned cols = (unsigned)((p.D + 31) / 32);
+            norm_sum_kernel<<<cols * ((p.dweight ? 1 : 0) + (p.dbias ? 1 : 0)), SUM_NT, 0, st>>>(p);
+        } else {
+            cudaError_t e = cudaSuccess;
+            for (float* q0 : {p.dweight, p.dbias})
+                if (q0 && e == cudaSuccess) e = cudaMemsetAsync(q0, 0, (size_t)p.D * sizeof(float), st);
+            if (e != cudaSuccess) return cuda_fail(e, "memset(dweight, dbias)");
+        }
+    }
+    const cudaError_t e = cudaGetLastError();
+    return s != GDR_OK ? s : e == cudaSuccess ? GDR_OK : cuda_fail(e, "launch(layer norm)");
+}
+
+// Blocks of the backward, each with a partial row of its own: 1024 threads per SM, and at least
+// eight rows for each of a block's groups, so that the partial rows stay few against the rows.
+static int parts_of(const gdr_norm_desc* d) {
+    const Plan q = plan_of(d->D, vector_of(d), true);
+    const long long per = q.N && !q.block ? WARP_NT / q.group : 1;
+    const long long n = (d->rows + 8 * per - 1) / (8 * per);
+    const long long cap = (long long)device_sm_count() * (q.N ? 1024 / (q.block ? q.block : WARP_NT) : 2);
+    return (int)(n < 1 ? 1 : n < cap ? n : cap);
+}
+
+static gdr_status dispatch(const gdr_norm_desc* d, bool bwd, NormParams& p, cudaStream_t st) {
     const bool xb = d->x_dtype == GDR_BF16, yb = d->y_dtype == GDR_BF16;
-    if (xb && yb) return launch_w<__nv_bfloat16, __nv_bfloat16>(d, bwd, p, st);
-    if (xb) return launch_w<__nv_bfloat16, float>(d, bwd, p, st);
-    if (yb) return launch_w<float, __nv_bfloat16>(d, bwd, p, st);
-    return launch_w<float, float>(d, bwd, p, st);
+    if (xb && yb) return launch<__nv_bfloat16, __nv_bfloat16>(d, bwd, p, st);
+    if (xb) return launch<__nv_bfloat16, float>(d, bwd, p, st);
+    if (yb) return launch<float, __nv_bfloat16>(d, bwd, p, st);
+    return launch<float, float>(d, bwd, p, st);
 }
 
 static gdr_status check_desc(const gdr_norm_desc* d) {
@@ -164,8 +145,6 @@ static gdr_status check_desc(const gdr_norm_desc* d) {
     if (!(d->eps >= 0.f)) return fail(GDR_ERR_INVALID_ARG, "eps must be >= 0%s");
     return GDR_OK;
 }
-
-static int parts_of(const gdr_norm_desc* d) { return (int)(d->rows < PARTS ? (d->rows > 0 ? d->rows : 1) : PARTS); }
 
 }  // namespace lnm
 
