@@ -10,74 +10,75 @@
 namespace gdr {
 namespace lnm {
 
-// How a row of D elements is held: V elements a load, N loads a lane, `group` lanes of a warp or a
-// block of `block` threads; N = 0: the row is too long for a block's registers.
-struct Plan { int V, N, block, group; };
+// How a row of D elements is held: V elements a load, N loads a lane, G lanes (of a warp, or a block
+// of G threads); N = 0: the row is too long for a block's registers.
+struct Plan { int V, N, G; };
 
 // A warp while a lane holds at most 32 elements (backward: 8, since it also holds dy and two sums),
 // then a block: in the forward the smallest one whose threads hold the row in 32 elements each
 // (the more loads a thread has in flight the better), in the backward one whose threads hold it
 // in 8, or 16 for one-element loads.
 static Plan plan_of(int D, int V, bool bwd) {
-    Plan q{V, 0, 0, 32};
+    Plan q{V, 0, 32};
     const int nv = (D + V - 1) / V;             // loads of a row
     if (nv <= 32) {                             // one load a lane, as few lanes as hold the row
         q.N = 1;
-        for (q.group = 1; q.group < nv; q.group *= 2) {}
+        for (q.G = 1; q.G < nv; q.G *= 2) {}
         return q;
     }
     const int most = (bwd ? V == 1 ? 16 : 8 : 32) / V;
     for (int n = 2; n <= (V == 1 ? 16 : most); n *= 2)
         if (nv <= 32 * n) { q.N = n; return q; }
-    for (int block : {128, 256, 512, 1024}) {
-        if (block == 1024 && (!bwd || V == 1)) break;
+    for (int g : {128, 256, 512, 1024}) {
+        if (g == 1024 && (!bwd || V == 1)) break;
         for (int n = V == 1 ? 8 : bwd ? most : 1; n <= most; n *= 2)
-            if (nv <= block * n) { q.block = block; q.N = n; return q; }
+            if (nv <= g * n) { q.G = g; q.N = n; return q; }
     }
     return q;
 }
+static int rows_of_block(const Plan& q) { return q.N && q.G <= 32 ? WARP_NT / q.G : 1; }
 static int vector_of(const gdr_norm_desc* d) {  // elements of a load: 16 bytes, where every row starts on them
     const int V = d->x_dtype == GDR_BF16 && d->y_dtype == GDR_BF16 ? 8 : 4;
     return d->D % V == 0 ? V : 1;
 }
 
-template <typename XT, typename YT, int V, int N, int BLOCK, bool BWD>
+template <typename XT, typename YT, int V, int N, int G, bool BWD>
 static gdr_status launch_one(const NormParams& p, cudaStream_t st) {
-    constexpr int NTH = threads<BLOCK>();
-    const long long per = BLOCK ? 1 : WARP_NT / p.group;
+    constexpr int NTH = threads<G>(), per = NTH / G, U = rows_at_once<V, N, G>();
     if constexpr (!BWD) {
-        const long long blocks = (p.rows + per - 1) / per, cap = (long long)device_sm_count() * (2048 / NTH);
-        norm_fwd_kernel<XT, YT, V, N, BLOCK><<<(unsigned)(blocks < cap ? blocks : cap), NTH, 0, st>>>(p);
+        const long long blocks = (p.rows + per * U - 1) / (per * U), cap = (long long)device_sm_count() * (1024 / NTH);
+        norm_fwd_kernel<XT, YT, V, N, G><<<(unsigned)(blocks < cap ? blocks : cap), NTH, 0, st>>>(p);
     } else {
         // the groups' sums in turn: at most 256 threads x 16 columns
-        const size_t smem = BLOCK || !(p.part_w || p.part_b) ? 0 : (size_t)per * p.D * sizeof(float);
-        norm_bwd_kernel<XT, YT, V, N, BLOCK><<<p.parts, NTH, smem, st>>>(p);
+        const size_t smem = per == 1 || !(p.part_w || p.part_b) ? 0 : (size_t)per * p.D * sizeof(float);
+        norm_bwd_kernel<XT, YT, V, N, G><<<p.parts, NTH, smem, st>>>(p);
     }
     const cudaError_t e = cudaGetLastError();
     return e == cudaSuccess ? GDR_OK : cuda_fail(e, "launch(layer norm)");
 }
 
 // The kernels that plan_of reaches.
-template <typename XT, typename YT, int V>
-static gdr_status launch_plan(bool bwd, const Plan& q, const NormParams& p, cudaStream_t st) {
-#define GDR_NORM(way, n, blk) \
-    if (bwd == way && q.N == n && q.block == blk) return launch_one<XT, YT, V, n, blk, way>(p, st)
-    GDR_NORM(false, 1, 0); GDR_NORM(true, 1, 0);
-    GDR_NORM(false, 2, 0); GDR_NORM(false, 4, 0);
-    if constexpr (V == 8) {
-        GDR_NORM(false, 2, 128); GDR_NORM(false, 4, 128); GDR_NORM(false, 4, 256); GDR_NORM(false, 4, 512);
-        GDR_NORM(true, 1, 128); GDR_NORM(true, 1, 256); GDR_NORM(true, 1, 512); GDR_NORM(true, 1, 1024);
+template <typename XT, typename YT, int V, bool BWD>
+static gdr_status launch_plan(const Plan& q, const NormParams& p, cudaStream_t st) {
+#define GDR_NORM(n, g) if (q.N == n && q.G == g) return launch_one<XT, YT, V, n, g, BWD>(p, st)
+    GDR_NORM(1, 1); GDR_NORM(1, 2); GDR_NORM(1, 4); GDR_NORM(1, 8); GDR_NORM(1, 16); GDR_NORM(1, 32);
+    if constexpr (!BWD) {
+        GDR_NORM(2, 32); GDR_NORM(4, 32);
+        if constexpr (V == 8) {
+            GDR_NORM(2, 128); GDR_NORM(4, 128); GDR_NORM(4, 256); GDR_NORM(4, 512);
+        } else if constexpr (V == 4) {
+            GDR_NORM(8, 32); GDR_NORM(4, 128); GDR_NORM(8, 128); GDR_NORM(8, 256); GDR_NORM(8, 512);
+        } else {
+            GDR_NORM(8, 32); GDR_NORM(16, 32);
+            GDR_NORM(8, 128); GDR_NORM(16, 128); GDR_NORM(32, 128); GDR_NORM(32, 256); GDR_NORM(32, 512);
+        }
+    } else if constexpr (V == 8) {
+        GDR_NORM(1, 128); GDR_NORM(1, 256); GDR_NORM(1, 512); GDR_NORM(1, 1024);
     } else if constexpr (V == 4) {
-        GDR_NORM(false, 8, 0);
-        GDR_NORM(false, 4, 128); GDR_NORM(false, 8, 128); GDR_NORM(false, 8, 256); GDR_NORM(false, 8, 512);
-        GDR_NORM(true, 2, 0);
-        GDR_NORM(true, 2, 128); GDR_NORM(true, 2, 256); GDR_NORM(true, 2, 512); GDR_NORM(true, 2, 1024);
+        GDR_NORM(2, 32); GDR_NORM(2, 128); GDR_NORM(2, 256); GDR_NORM(2, 512); GDR_NORM(2, 1024);
     } else {
-        GDR_NORM(false, 8, 0); GDR_NORM(false, 16, 0);
-        GDR_NORM(false, 8, 128); GDR_NORM(false, 16, 128); GDR_NORM(false, 32, 128); GDR_NORM(false, 32, 256);
-        GDR_NORM(false, 32, 512);
-        GDR_NORM(true, 2, 0); GDR_NORM(true, 4, 0); GDR_NORM(true, 8, 0); GDR_NORM(true, 16, 0);
-        GDR_NORM(true, 8, 128); GDR_NORM(true, 16, 128); GDR_NORM(true, 16, 256); GDR_NORM(true, 16, 512);
+        GDR_NORM(2, 32); GDR_NORM(4, 32); GDR_NORM(8, 32); GDR_NORM(16, 32);
+        GDR_NORM(8, 128); GDR_NORM(16, 128); GDR_NORM(16, 256); GDR_NORM(16, 512);
     }
 #undef GDR_NORM
     return fail(GDR_ERR_UNSUPPORTED, "layer norm: no kernel for this plan%s");
@@ -87,11 +88,11 @@ template <typename XT, typename YT>
 static gdr_status launch(const gdr_norm_desc* d, bool bwd, NormParams& p, cudaStream_t st) {
     constexpr int V = sizeof(XT) == 2 && sizeof(YT) == 2 ? 8 : 4;
     const Plan q = plan_of(p.D, vector_of(d), bwd);
-    p.group = q.group;
     p.w_bf16 = d->w_dtype == GDR_BF16;
     gdr_status s = GDR_OK;
     if (p.rows > 0) {
-        if (q.N) s = q.V > 1 ? launch_plan<XT, YT, V>(bwd, q, p, st) : launch_plan<XT, YT, 1>(bwd, q, p, st);
+        if (q.N && bwd) s = q.V > 1 ? launch_plan<XT, YT, V, true>(q, p, st) : launch_plan<XT, YT, 1, true>(q, p, st);
+        else if (q.N) s = q.V > 1 ? launch_plan<XT, YT, V, false>(q, p, st) : launch_plan<XT, YT, 1, false>(q, p, st);
         else {
             const unsigned grid = (unsigned)(p.rows < 2 * device_sm_count() ? p.rows : 2 * device_sm_count());
             if (!bwd) norm_fwd_long_kernel<XT, YT><<<grid, LONG_NT, 0, st>>>(p);
@@ -105,7 +106,17 @@ static gdr_status launch(const gdr_norm_desc* d, bool bwd, NormParams& p, cudaSt
     if (s == GDR_OK && bwd && (p.dweight || p.dbias)) {
         if (p.rows > 0) {
             const unsigned cols = (unsigned)((p.D + 31) / 32);
-            norm_sum_kernel<<<cols * ((p.dweight ? 1 : 0) + (p.dbias ? 1 : 0)), SUM_NT, 0, st>>>(p);
+            cudaLaunchConfig_t cfg = {};
+            cfg.gridDim = dim3(cols * ((p.dweight ? 1 : 0) + (p.dbias ? 1 : 0)));
+            cfg.blockDim = dim3(SUM_NT);
+            cfg.stream = st;
+            cudaLaunchAttribute at[1];
+            at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+            at[0].val.programmaticStreamSerializationAllowed = 1;
+            cfg.attrs = at;
+            cfg.numAttrs = 1;
+            const cudaError_t e = cudaLaunchKernelEx(&cfg, norm_sum_kernel, p);
+            if (e != cudaSuccess) return cuda_fail(e, "launch(layer norm sums)");
         } else {
             cudaError_t e = cudaSuccess;
             for (float* q0 : {p.dweight, p.dbias})
@@ -117,13 +128,12 @@ static gdr_status launch(const gdr_norm_desc* d, bool bwd, NormParams& p, cudaSt
     return s != GDR_OK ? s : e == cudaSuccess ? GDR_OK : cuda_fail(e, "launch(layer norm)");
 }
 
-// Blocks of the backward, each with a partial row of its own: 1024 threads per SM, and at least
+// Blocks of the backward, each with a partial row of its own: 512 threads per SM, and at least
 // eight rows for each of a block's groups, so that the partial rows stay few against the rows.
 static int parts_of(const gdr_norm_desc* d) {
     const Plan q = plan_of(d->D, vector_of(d), true);
-    const long long per = q.N && !q.block ? WARP_NT / q.group : 1;
-    const long long n = (d->rows + 8 * per - 1) / (8 * per);
-    const long long cap = (long long)device_sm_count() * (q.N ? 1024 / (q.block ? q.block : WARP_NT) : 2);
+    const long long per = rows_of_block(q), n = (d->rows + 8 * per - 1) / (8 * per);
+    const long long cap = (long long)device_sm_count() * (q.N && q.G < 512 ? 512 / (q.G > 32 ? q.G : WARP_NT) : q.N ? 1 : 2);
     return (int)(n < 1 ? 1 : n < cap ? n : cap);
 }
 

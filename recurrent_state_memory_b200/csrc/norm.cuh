@@ -42,8 +42,68 @@ struct NormParams {
     float* dbias;
     int parts;
     int w_bf16;             // weight and bias are bf16 (else fp32)
-    int group;              // lanes of a row (warp kernels): 1, 2, .. 32
 };
+
+// Two fp32 values in one register pair: sm_100 adds, multiplies and fuses them in one instruction.
+struct Pair { unsigned long long v; };
+__device__ __forceinline__ Pair pair(float a, float b) { Pair p; asm("mov.b64 %0, {%1, %2};" : "=l"(p.v) : "f"(a), "f"(b)); return p; }
+__device__ __forceinline__ float lo(Pair p) { float a; asm("{\n\t.reg .f32 t;\n\tmov.b64 {%0, t}, %1;\n\t}" : "=f"(a) : "l"(p.v)); return a; }
+__device__ __forceinline__ float hi(Pair p) { float b; asm("{\n\t.reg .f32 t;\n\tmov.b64 {t, %0}, %1;\n\t}" : "=f"(b) : "l"(p.v)); return b; }
+__device__ __forceinline__ Pair operator+(Pair a, Pair b) { Pair d; asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d.v) : "l"(a.v), "l"(b.v)); return d; }
+__device__ __forceinline__ Pair operator*(Pair a, Pair b) { Pair d; asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d.v) : "l"(a.v), "l"(b.v)); return d; }
+__device__ __forceinline__ Pair fma(Pair a, Pair b, Pair c) { Pair d; asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d.v) : "l"(a.v), "l"(b.v), "l"(c.v)); return d; }
+
+// A lane's V elements: pairs, or one value.
+template <int V> struct Vals {
+    static constexpr int H = V / 2;
+    Pair v[H];
+    __device__ __forceinline__ void all(float x) {
+#pragma unroll
+        for (int i = 0; i < H; ++i) v[i] = pair(x, x);
+    }
+    __device__ __forceinline__ float total() const {
+        Pair s = v[0];
+#pragma unroll
+        for (int i = 1; i < H; ++i) s = s + v[i];
+        return lo(s) + hi(s);
+    }
+    __device__ __forceinline__ void set(int i, float x) { v[i / 2] = i & 1 ? pair(lo(v[i / 2]), x) : pair(x, hi(v[i / 2])); }
+    __device__ __forceinline__ float get(int i) const { return i & 1 ? hi(v[i / 2]) : lo(v[i / 2]); }
+};
+template <> struct Vals<1> {
+    float v;
+    __device__ __forceinline__ void all(float x) { v = x; }
+    __device__ __forceinline__ float total() const { return v; }
+    __device__ __forceinline__ void set(int, float x) { v = x; }
+    __device__ __forceinline__ float get(int) const { return v; }
+};
+template <int V> __device__ __forceinline__ Vals<V> operator+(const Vals<V>& a, const Vals<V>& b) {
+    Vals<V> d;
+    if constexpr (V == 1) d.v = a.v + b.v;
+    else {
+#pragma unroll
+        for (int i = 0; i < V / 2; ++i) d.v[i] = a.v[i] + b.v[i];
+    }
+    return d;
+}
+template <int V> __device__ __forceinline__ Vals<V> operator*(const Vals<V>& a, const Vals<V>& b) {
+    Vals<V> d;
+    if constexpr (V == 1) d.v = a.v * b.v;
+    else {
+#pragma unroll
+        for (int i = 0; i < V / 2; ++i) d.v[i] = a.v[i] * b.v[i];
+    }
+    return d;
+}
+template <int V> __device__ __forceinline__ Vals<V> fma(const Vals<V>& a, const Vals<V>& b, const Vals<V>& c) {
+    Vals<V> d;
+    if constexpr (V == 1) d.v = fmaf(a.v, b.v, c.v);
+    else {
+#pragma unroll
+        for (int i = 0; i < V / 2; ++i) d.v[i] = fma(a.v[i], b.v[i], c.v[i]);
+    }
+    return d;
+}
 
 // V consecutive elements as they lie in memory (one access of 16 bytes or less, or two), and as fp32.
 template <typename T, int V> struct Raw {
@@ -73,32 +133,39 @@ template <typename T, int V> struct Raw {
         if constexpr (sizeof(T) == 4) return __uint_as_float(w[i]);
         else return __uint_as_float(i & 1 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
     }
+    __device__ __forceinline__ Vals<V> vals() const {
+        Vals<V> x;
+        if constexpr (V == 1) x.v = get(0);
+        else {
+#pragma unroll
+            for (int i = 0; i < V / 2; ++i) x.v[i] = pair(get(2 * i), get(2 * i + 1));
+        }
+        return x;
+    }
 };
 // V weights or biases from column c on, of either type.
-template <int V> __device__ __forceinline__ void load_w(const void* p, int bf16, int c, float (&v)[V]) {
+template <int V> __device__ __forceinline__ Vals<V> load_w(const void* p, int bf16, int c) {
     if (bf16) {
         Raw<__nv_bfloat16, V> r;
         r.load(static_cast<const __nv_bfloat16*>(p) + c);
-#pragma unroll
-        for (int i = 0; i < V; ++i) v[i] = r.get(i);
-    } else {
-        Raw<float, V> r;
-        r.load(static_cast<const float*>(p) + c);
-#pragma unroll
-        for (int i = 0; i < V; ++i) v[i] = r.get(i);
+        return r.vals();
     }
+    Raw<float, V> r;
+    r.load(static_cast<const float*>(p) + c);
+    return r.vals();
 }
-template <typename T, int V> __device__ __forceinline__ void store_v(T* p, const float (&v)[V]) {
+template <typename T, int V> __device__ __forceinline__ void store_v(T* p, const Vals<V>& v) {
     if constexpr (V == 1) {
-        st_from_f32(p, v[0]);
+        st_from_f32(p, v.v);
     } else if constexpr (sizeof(T) == 4) {
 #pragma unroll
-        for (int i = 0; i < V; i += 4) *reinterpret_cast<float4*>(p + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+        for (int i = 0; i < V; i += 4)
+            *reinterpret_cast<float4*>(p + i) = make_float4(v.get(i), v.get(i + 1), v.get(i + 2), v.get(i + 3));
     } else {
         unsigned w[V / 2];
 #pragma unroll
         for (int i = 0; i < V / 2; ++i) {
-            const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+            const __nv_bfloat162 b = __floats2bfloat162_rn(v.get(2 * i), v.get(2 * i + 1));
             w[i] = *reinterpret_cast<const unsigned*>(&b);
         }
         if constexpr (V == 8) *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
@@ -106,261 +173,288 @@ template <typename T, int V> __device__ __forceinline__ void store_v(T* p, const
     }
 }
 
-// The sum over a row's group: lanes of a warp (n lanes), or the block (BLOCK threads; sm: two
-// sets of warp sums used in turn, so that one barrier a sum is enough).
-template <int BLOCK> struct Group {
-    float* sm;
-    int n, turn;
-    __device__ __forceinline__ float sum(float v) {
-        if constexpr (BLOCK == 0) {
-            for (int o = n >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-            return v;
+// Sums over a row's group of G lanes, n values at once: of a warp (G <= 32), or a block of G
+// threads (sm: two sets of warp sums used in turn, so that one barrier a sum is enough).
+template <int G, int MOST> struct Group {
+    static constexpr int WARPS = G > 32 ? G / 32 : 1;
+    float (*sm)[WARPS][MOST];           // [2]
+    int turn;
+    template <int n> __device__ __forceinline__ void sum(float (&v)[n]) {
+        static_assert(n <= MOST, "values");
+        if constexpr (G <= 32) {
+#pragma unroll
+            for (int o = G / 2; o > 0; o >>= 1)
+#pragma unroll
+                for (int i = 0; i < n; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
         } else {
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-            float* s = sm + turn * (BLOCK / 32);
+            // four values: each exchange halves what a lane still adds, so that 6 exchanges do
+            // the work of 20; lane l ends with value l & 3
+            const int lane = threadIdx.x & 31;
+            float (*s)[MOST] = sm[turn];
             turn ^= 1;
-            if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = v;
-            __syncthreads();
-            float t = 0.f;
+            if constexpr (n == 4) {
+                const bool b0 = lane & 1, b1 = lane & 2;
+                const float x0 = b0 ? v[0] : v[1], x1 = b0 ? v[2] : v[3];       // what the neighbour keeps
+                float y0 = b0 ? v[1] : v[0], y1 = b0 ? v[3] : v[2];
+                y0 += __shfl_xor_sync(0xffffffffu, x0, 1);
+                y1 += __shfl_xor_sync(0xffffffffu, x1, 1);
+                float z = b1 ? y1 : y0;
+                z += __shfl_xor_sync(0xffffffffu, b1 ? y0 : y1, 2);
 #pragma unroll
-            for (int i = 0; i < BLOCK / 32; ++i) t += s[i];
-            return t;
-        }
-    }
-    __device__ __forceinline__ void sum2(float& a, float& b) {
-        if constexpr (BLOCK == 0) {
-            for (int o = n >> 1; o > 0; o >>= 1) {
-                a += __shfl_xor_sync(0xffffffffu, a, o);
-                b += __shfl_xor_sync(0xffffffffu, b, o);
+                for (int o = 4; o < 32; o <<= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
+                if (lane < 4) s[threadIdx.x >> 5][lane] = z;
+            } else {
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+                    for (int i = 0; i < n; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+                if (lane == 0) {
+#pragma unroll
+                    for (int i = 0; i < n; ++i) s[threadIdx.x >> 5][i] = v[i];
+                }
             }
-        } else {
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) {
-                a += __shfl_xor_sync(0xffffffffu, a, o);
-                b += __shfl_xor_sync(0xffffffffu, b, o);
-            }
-            float2* s = reinterpret_cast<float2*>(sm) + turn * (BLOCK / 32);
-            turn ^= 1;
-            if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = make_float2(a, b);
             __syncthreads();
-            a = b = 0.f;
 #pragma unroll
-            for (int i = 0; i < BLOCK / 32; ++i) { a += s[i].x; b += s[i].y; }
+            for (int i = 0; i < n; ++i) v[i] = 0.f;
+#pragma unroll
+            for (int w = 0; w < WARPS; ++w)
+#pragma unroll
+                for (int i = 0; i < n; ++i) v[i] += s[w][i];
         }
     }
 };
 
 constexpr int WARP_NT = 256;            // threads of a block of the warp kernels
 
-// Threads of a block: BLOCK, or WARP_NT where a row is a warp's lanes.
-template <int BLOCK> constexpr int threads() { return BLOCK ? BLOCK : WARP_NT; }
+// Threads of a block whose rows belong to G lanes each.
+template <int G> constexpr int threads() { return G > 32 ? G : WARP_NT; }
 
-// Where this thread's group stands: its first row, the stride to its next, its lane, its lanes.
-template <int BLOCK> struct Place {
+// Where this thread stands: its lane in its row's group, its (first) row in the block's first
+// turn, and the rows of a turn of the grid.  A group's U rows of a turn are PER apart.
+template <int G, int U> struct Place {
+    static constexpr int PER = threads<G>() / G;      // groups of a block
+    int lane;
     long long row, step;
-    int lane, lanes;
-    __device__ __forceinline__ explicit Place(const NormParams& p) {
-        if constexpr (BLOCK == 0) {
-            const int per = WARP_NT / p.group;
-            lane = threadIdx.x & (p.group - 1);
-            lanes = p.group;
-            row = (long long)blockIdx.x * per + threadIdx.x / p.group;
-            step = (long long)gridDim.x * per;
-        } else {
-            lane = threadIdx.x;
-            lanes = BLOCK;
-            row = blockIdx.x;
-            step = gridDim.x;
-        }
-    }
+    __device__ __forceinline__ Place()
+        : lane(threadIdx.x % G), row((long long)blockIdx.x * (PER * U) + threadIdx.x / G),
+          step((long long)gridDim.x * (PER * U)) {}
 };
 
-// One row per group and turn, N loads of V elements per lane.
-template <typename XT, typename YT, int V, int N, int BLOCK>
-__global__ void __launch_bounds__(threads<BLOCK>()) norm_fwd_kernel(NormParams p) {
-    __shared__ float2 sm[2 * (BLOCK ? BLOCK / 32 : 1)];
-    const Place<BLOCK> at(p);
-    Group<BLOCK> grp{reinterpret_cast<float*>(sm), at.lanes, 0};
+// Rows that a group takes per turn: two while a row is few registers, so that more loads are in
+// flight and, in a block, two rows share a barrier.
+template <int V, int N, int G> constexpr int rows_at_once() { return V * N <= 8 && G < 1024 ? 2 : 1; }
+
+// N loads of V elements per lane and row.
+template <typename XT, typename YT, int V, int N, int G>
+__global__ void __launch_bounds__(threads<G>(), V * N <= 8 ? 1024 / threads<G>() : 1) norm_fwd_kernel(NormParams p) {
+    constexpr int U = rows_at_once<V, N, G>();
+    __shared__ __align__(16) float sm[2][G > 32 ? G / 32 : 1][U];
+    const Place<G, U> at;
+    Group<G, U> grp{sm, 0};
     const float inv = 1.f / (float)p.D;
-    const XT* x = static_cast<const XT*>(p.x);
-    YT* y = static_cast<YT*>(p.y);
+    const int c0 = at.lane * V;                       // this lane's columns: c0 + j * G * V ..
     constexpr bool KEEP = V * N <= 16;                // weights stay in registers
-    float w[KEEP ? N : 1][V], bi[KEEP ? N : 1][V];
-    auto weights = [&](int j, float (&wv)[V], float (&bv)[V]) {
-        const int c = (j * at.lanes + at.lane) * V;
-#pragma unroll
-        for (int i = 0; i < V; ++i) { wv[i] = 1.f; bv[i] = 0.f; }
+    Vals<V> w[KEEP ? N : 1], bi[KEEP ? N : 1];
+    auto weights = [&](int j, Vals<V>& wv, Vals<V>& bv) {
+        const int c = c0 + j * G * V;
+        wv.all(1.f);
+        bv.all(0.f);
         if (c < p.D) {
-            if (p.weight) load_w<V>(p.weight, p.w_bf16, c, wv);
-            if (p.bias) load_w<V>(p.bias, p.w_bf16, c, bv);
+            if (p.weight) wv = load_w<V>(p.weight, p.w_bf16, c);
+            if (p.bias) bv = load_w<V>(p.bias, p.w_bf16, c);
         }
     };
     if constexpr (KEEP) {
 #pragma unroll
         for (int j = 0; j < N; ++j) weights(j, w[j], bi[j]);
     }
-    Raw<XT, V> raw[N];
+    const size_t jump = (size_t)at.step * p.D, next = (size_t)at.PER * p.D;
+    const XT* x = static_cast<const XT*>(p.x) + (size_t)at.row * p.D + c0;      // the rows to fetch next
+    YT* y = static_cast<YT*>(p.y) + (size_t)at.row * p.D + c0;
+    Raw<XT, V> raw[U][N];
     auto fetch = [&](long long r) {
 #pragma unroll
-        for (int j = 0; j < N; ++j) {
-            const int c = (j * at.lanes + at.lane) * V;
-            if (r < p.rows && c < p.D) raw[j].load(x + (size_t)r * p.D + c);
-            else raw[j].zero();
-        }
-    };
-    // every lane of a warp makes the same number of turns (the sums are warp-wide)
-    const long long first = BLOCK ? at.row : at.row - (threadIdx.x & 31) / at.lanes;
-    fetch(at.row);
-    for (long long r0 = first; r0 < p.rows; r0 += at.step) {
-        const long long r = r0 + (at.row - first);
-        float v[N][V], s = 0.f;
-#pragma unroll
-        for (int j = 0; j < N; ++j)
-#pragma unroll
-            for (int i = 0; i < V; ++i) { v[j][i] = raw[j].get(i); s += v[j][i]; }
-        fetch(r + at.step);
-        const float mean = grp.sum(s) * inv;
-        s = 0.f;
-#pragma unroll
-        for (int j = 0; j < N; ++j) {
-            if ((j * at.lanes + at.lane) * V < p.D) {
-#pragma unroll
-                for (int i = 0; i < V; ++i) { v[j][i] -= mean; s = fmaf(v[j][i], v[j][i], s); }
-            }
-        }
-        const float rstd = 1.f / sqrtf(grp.sum(s) * inv + p.eps);
-        if (r < p.rows) {
+        for (int u = 0; u < U; ++u)
 #pragma unroll
             for (int j = 0; j < N; ++j) {
-                const int c = (j * at.lanes + at.lane) * V;
-                if (c >= p.D) continue;
-                float o[V];
-                if constexpr (KEEP) {
+                if (r + u * at.PER < p.rows && c0 + j * G * V < p.D) raw[u][j].load(x + u * next + j * G * V);
+                else raw[u][j].zero();
+            }
+        x += jump;
+    };
+    fetch(at.row);
+    // every lane of a warp makes the same number of turns (the sums are warp-wide)
+    const long long ahead = G > 32 ? 0 : (threadIdx.x & 31) / G;
+    for (long long r = at.row; r - ahead < p.rows; r += at.step) {
+        Vals<V> v[U][N], s;
+        float mean[U], rstd[U];
 #pragma unroll
-                    for (int i = 0; i < V; ++i) o[i] = fmaf(v[j][i] * rstd, w[j][i], bi[j][i]);
-                } else {
-                    float wv[V], bv[V];
-                    weights(j, wv, bv);
+        for (int u = 0; u < U; ++u) {
 #pragma unroll
-                    for (int i = 0; i < V; ++i) o[i] = fmaf(v[j][i] * rstd, wv[i], bv[i]);
-                }
-                if (GDR_INB(c + V <= p.D, 901)) store_v<YT, V>(y + (size_t)r * p.D + c, o);
+            for (int j = 0; j < N; ++j) {
+                v[u][j] = raw[u][j].vals();
+                s = j ? s + v[u][j] : v[u][j];
+            }
+            mean[u] = s.total();
+        }
+        fetch(r + at.step);
+        grp.sum(mean);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            mean[u] *= inv;
+            Vals<V> off;
+            off.all(-mean[u]);
+            s.all(0.f);
+#pragma unroll
+            for (int j = 0; j < N; ++j) {
+                v[u][j] = v[u][j] + off;
+                if (c0 + j * G * V < p.D) s = fma(v[u][j], v[u][j], s);
+            }
+            rstd[u] = s.total();
+        }
+        grp.sum(rstd);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (r + u * at.PER >= p.rows) continue;
+            rstd[u] = rsqrtf(rstd[u] * inv + p.eps);
+            Vals<V> rs;
+            rs.all(rstd[u]);
+#pragma unroll
+            for (int j = 0; j < N; ++j) {
+                if (c0 + j * G * V >= p.D) continue;
+                Vals<V> wv, bv;
+                if constexpr (!KEEP) weights(j, wv, bv);
+                const Vals<V> o = fma(v[u][j] * rs, KEEP ? w[KEEP ? j : 0] : wv, KEEP ? bi[KEEP ? j : 0] : bv);
+                if (GDR_INB(c0 + j * G * V + V <= p.D, 901)) store_v<YT, V>(y + u * next + j * G * V, o);
             }
             if (at.lane == 0) {
-                if (p.mean) p.mean[r] = mean;
-                if (p.rstd) p.rstd[r] = rstd;
+                if (p.mean) p.mean[r + u * at.PER] = mean[u];
+                if (p.rstd) p.rstd[r + u * at.PER] = rstd[u];
             }
         }
+        y += jump;
     }
 }
 
 // Backward: dx, and the block's share of dweight and dbias.
-template <typename XT, typename YT, int V, int N, int BLOCK>
-__global__ void __launch_bounds__(threads<BLOCK>()) norm_bwd_kernel(NormParams p) {
-    extern __shared__ float part[];                   // warp kernels: the groups' sums [NT / lanes][D], in turn
-    __shared__ float2 sm[2 * (BLOCK ? BLOCK / 32 : 1)];
-    const Place<BLOCK> at(p);
-    Group<BLOCK> grp{reinterpret_cast<float*>(sm), at.lanes, 0};
+template <typename XT, typename YT, int V, int N, int G>
+__global__ void __launch_bounds__(threads<G>(), V * N <= 8 && G <= 256 ? 512 / threads<G>() : 1) norm_bwd_kernel(NormParams p) {
+    constexpr int U = rows_at_once<V, N, G>();
+    extern __shared__ float part[];                   // G <= 32: the groups' sums [PER][D], in turn
+    __shared__ __align__(16) float sm[2][G > 32 ? G / 32 : 1][2 * U];
+    const Place<G, U> at;
+    Group<G, 2 * U> grp{sm, 0};
     const float inv = 1.f / (float)p.D;
-    const XT* x = static_cast<const XT*>(p.x);
-    const YT* dy = static_cast<const YT*>(p.dy);
-    XT* dx = static_cast<XT*>(p.dx);
+    const int c0 = at.lane * V;
     constexpr bool KEEP = V * N <= 8;
-    float w[KEEP ? N : 1][V];
-    auto weights = [&](int j, float (&wv)[V]) {
-        const int c = (j * at.lanes + at.lane) * V;
-#pragma unroll
-        for (int i = 0; i < V; ++i) wv[i] = 1.f;
-        if (c < p.D && p.weight) load_w<V>(p.weight, p.w_bf16, c, wv);
+    Vals<V> w[KEEP ? N : 1];
+    auto weights = [&](int j, Vals<V>& wv) {
+        wv.all(1.f);
+        if (c0 + j * G * V < p.D && p.weight) wv = load_w<V>(p.weight, p.w_bf16, c0 + j * G * V);
     };
     if constexpr (KEEP) {
 #pragma unroll
         for (int j = 0; j < N; ++j) weights(j, w[j]);
     }
-    float sw[N][V], sb[N][V];
+    Vals<V> sw[N], sb[N];
 #pragma unroll
-    for (int j = 0; j < N; ++j)
-#pragma unroll
-        for (int i = 0; i < V; ++i) sw[j][i] = sb[j][i] = 0.f;
-    Raw<XT, V> rx[N];
-    Raw<YT, V> rd[N];
-    float mean = 0.f, rstd = 0.f;
+    for (int j = 0; j < N; ++j) { sw[j].all(0.f); sb[j].all(0.f); }
+    const size_t jump = (size_t)at.step * p.D, next = (size_t)at.PER * p.D, start = (size_t)at.row * p.D + c0;
+    const XT* x = static_cast<const XT*>(p.x) + start;
+    const YT* dy = static_cast<const YT*>(p.dy) + start;
+    XT* dx = static_cast<XT*>(p.dx) + start;
+    Raw<XT, V> rx[U][N];
+    Raw<YT, V> rd[U][N];
+    float mean[U], rstd[U];
     auto fetch = [&](long long r) {
-        const bool in = r < p.rows;
-        mean = in ? p.mean[r] : 0.f;
-        rstd = in ? p.rstd[r] : 0.f;
 #pragma unroll
-        for (int j = 0; j < N; ++j) {
-            const int c = (j * at.lanes + at.lane) * V;
-            if (in && c < p.D) {
-                rx[j].load(x + (size_t)r * p.D + c);
-                rd[j].load(dy + (size_t)r * p.D + c);
-            } else { rx[j].zero(); rd[j].zero(); }
-        }
-    };
-    const long long first = BLOCK ? at.row : at.row - (threadIdx.x & 31) / at.lanes;
-    fetch(at.row);
-    for (long long r0 = first; r0 < p.rows; r0 += at.step) {
-        const long long r = r0 + (at.row - first);
-        float xh[N][V], d[N][V], c1 = 0.f, c2 = 0.f;
-        const float here = rstd;
-#pragma unroll
-        for (int j = 0; j < N; ++j) {
-            float wv[V];
-            if constexpr (!KEEP) weights(j, wv);
-#pragma unroll
-            for (int i = 0; i < V; ++i) {             // columns behind D: dy is zero
-                xh[j][i] = (rx[j].get(i) - mean) * rstd;
-                d[j][i] = rd[j].get(i);
-                sw[j][i] = fmaf(d[j][i], xh[j][i], sw[j][i]);
-                sb[j][i] += d[j][i];
-                d[j][i] *= KEEP ? w[KEEP ? j : 0][i] : wv[i];
-                c1 += d[j][i];
-                c2 = fmaf(d[j][i], xh[j][i], c2);
-            }
-        }
-        fetch(r + at.step);
-        if (!dx) continue;
-        grp.sum2(c1, c2);
-        c1 *= inv;
-        c2 *= inv;
-        if (r < p.rows) {
+        for (int u = 0; u < U; ++u) {
+            const bool in = r + u * at.PER < p.rows;
+            mean[u] = in ? p.mean[r + u * at.PER] : 0.f;
+            rstd[u] = in ? p.rstd[r + u * at.PER] : 0.f;
 #pragma unroll
             for (int j = 0; j < N; ++j) {
-                const int c = (j * at.lanes + at.lane) * V;
-                float o[V];
-#pragma unroll
-                for (int i = 0; i < V; ++i) o[i] = here * (d[j][i] - fmaf(xh[j][i], c2, c1));
-                if (c < p.D && GDR_INB(c + V <= p.D, 911)) store_v<XT, V>(dx + (size_t)r * p.D + c, o);
+                if (in && c0 + j * G * V < p.D) {
+                    rx[u][j].load(x + u * next + j * G * V);
+                    rd[u][j].load(dy + u * next + j * G * V);
+                } else { rx[u][j].zero(); rd[u][j].zero(); }
             }
         }
+        x += jump;
+        dy += jump;
+    };
+    fetch(at.row);
+    const long long ahead = G > 32 ? 0 : (threadIdx.x & 31) / G;
+    for (long long r = at.row; r - ahead < p.rows; r += at.step) {
+        Vals<V> xh[U][N], d[U][N];
+        float here[U], c[2 * U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            Vals<V> s1, s2, rs, off;
+            here[u] = rstd[u];
+            rs.all(rstd[u]);
+            off.all(-mean[u]);
+#pragma unroll
+            for (int j = 0; j < N; ++j) {             // columns behind D: dy is zero
+                Vals<V> wv;
+                if constexpr (!KEEP) weights(j, wv);
+                xh[u][j] = (rx[u][j].vals() + off) * rs;
+                d[u][j] = rd[u][j].vals();
+                sw[j] = fma(d[u][j], xh[u][j], sw[j]);
+                sb[j] = sb[j] + d[u][j];
+                d[u][j] = d[u][j] * (KEEP ? w[KEEP ? j : 0] : wv);
+                s1 = j ? s1 + d[u][j] : d[u][j];
+                s2 = j ? fma(d[u][j], xh[u][j], s2) : d[u][j] * xh[u][j];
+            }
+            c[2 * u] = s1.total();
+            c[2 * u + 1] = s2.total();
+        }
+        fetch(r + at.step);
+        if (p.dx) {
+            grp.sum(c);
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                if (r + u * at.PER >= p.rows) continue;
+                Vals<V> m1, m2, rs;
+                rs.all(here[u]);
+                m1.all(-c[2 * u] * inv);
+                m2.all(-c[2 * u + 1] * inv);
+#pragma unroll
+                for (int j = 0; j < N; ++j) {
+                    const Vals<V> o = (d[u][j] + fma(xh[u][j], m2, m1)) * rs;
+                    if (c0 + j * G * V < p.D && GDR_INB(c0 + j * G * V + V <= p.D, 911))
+                        store_v<XT, V>(dx + u * next + j * G * V, o);
+                }
+            }
+            dx += jump;
+        }
     }
+    asm volatile("griddepcontrol.launch_dependents;");  // the sum's blocks may come; they wait for these stores
     const size_t base = (size_t)blockIdx.x * p.D;
-    if constexpr (BLOCK != 0) {
+    if constexpr (G > 32) {
 #pragma unroll
         for (int j = 0; j < N; ++j) {
-            const int c = (j * at.lanes + at.lane) * V;
+            const int c = c0 + j * G * V;
             if (c >= p.D) continue;
             if (p.part_w) store_v<float, V>(p.part_w + base + c, sw[j]);
             if (p.part_b) store_v<float, V>(p.part_b + base + c, sb[j]);
         }
     } else {
         // the block's groups, added column by column in the groups' order
-        const int per = WARP_NT / at.lanes, g = threadIdx.x / at.lanes;
+        const int g = threadIdx.x / G;
         for (int which = 0; which < 2; ++which) {
             float* to = which ? p.part_b : p.part_w;
             if (!to) continue;
             __syncthreads();
 #pragma unroll
             for (int j = 0; j < N; ++j) {
-                const int c = (j * at.lanes + at.lane) * V;
+                const int c = c0 + j * G * V;
                 if (c < p.D) store_v<float, V>(part + (size_t)g * p.D + c, which ? sb[j] : sw[j]);
             }
             __syncthreads();
             for (int c = threadIdx.x; c < p.D; c += WARP_NT) {
                 float s = 0.f;
-                for (int i = 0; i < per; ++i) s += part[(size_t)i * p.D + c];
+                for (int i = 0; i < at.PER; ++i) s += part[(size_t)i * p.D + c];
                 to[base + c] = s;
             }
         }
@@ -371,23 +465,24 @@ __global__ void __launch_bounds__(threads<BLOCK>()) norm_bwd_kernel(NormParams p
 constexpr int LONG_NT = 1024;
 template <typename XT, typename YT>
 __global__ void __launch_bounds__(LONG_NT) norm_fwd_long_kernel(NormParams p) {
-    __shared__ float2 sm[2 * LONG_NT / 32];
-    Group<LONG_NT> grp{reinterpret_cast<float*>(sm), LONG_NT, 0};
+    __shared__ __align__(16) float sm[2][LONG_NT / 32][2];
+    Group<LONG_NT, 2> grp{sm, 0};
     const float inv = 1.f / (float)p.D;
     for (long long r = blockIdx.x; r < p.rows; r += gridDim.x) {
         const XT* x = static_cast<const XT*>(p.x) + (size_t)r * p.D;
         YT* y = static_cast<YT*>(p.y) + (size_t)r * p.D;
-        float s = 0.f;
-        for (int c = threadIdx.x; c < p.D; c += LONG_NT) s += ld_f32(x + c);
-        const float mean = grp.sum(s) * inv;
-        s = 0.f;
-        for (int c = threadIdx.x; c < p.D; c += LONG_NT) { const float v = ld_f32(x + c) - mean; s = fmaf(v, v, s); }
-        const float rstd = 1.f / sqrtf(grp.sum(s) * inv + p.eps);
+        float s[1] = {0.f};
+        for (int c = threadIdx.x; c < p.D; c += LONG_NT) s[0] += ld_f32(x + c);
+        grp.sum(s);
+        const float mean = s[0] * inv;
+        s[0] = 0.f;
+        for (int c = threadIdx.x; c < p.D; c += LONG_NT) { const float v = ld_f32(x + c) - mean; s[0] = fmaf(v, v, s[0]); }
+        grp.sum(s);
+        const float rstd = rsqrtf(s[0] * inv + p.eps);
         for (int c = threadIdx.x; c < p.D; c += LONG_NT) {
-            float w[1] = {1.f}, b[1] = {0.f};
-            if (p.weight) load_w<1>(p.weight, p.w_bf16, c, w);
-            if (p.bias) load_w<1>(p.bias, p.w_bf16, c, b);
-            st_from_f32(y + c, fmaf((ld_f32(x + c) - mean) * rstd, w[0], b[0]));
+            const float w = p.weight ? load_w<1>(p.weight, p.w_bf16, c).v : 1.f;
+            const float b = p.bias ? load_w<1>(p.bias, p.w_bf16, c).v : 0.f;
+            st_from_f32(y + c, fmaf((ld_f32(x + c) - mean) * rstd, w, b));
         }
         if (threadIdx.x == 0) {
             if (p.mean) p.mean[r] = mean;
@@ -397,30 +492,27 @@ __global__ void __launch_bounds__(LONG_NT) norm_fwd_long_kernel(NormParams p) {
 }
 template <typename XT, typename YT>
 __global__ void __launch_bounds__(LONG_NT) norm_dx_long_kernel(NormParams p) {
-    __shared__ float2 sm[2 * LONG_NT / 32];
-    Group<LONG_NT> grp{reinterpret_cast<float*>(sm), LONG_NT, 0};
+    __shared__ __align__(16) float sm[2][LONG_NT / 32][2];
+    Group<LONG_NT, 2> grp{sm, 0};
     const float inv = 1.f / (float)p.D;
     for (long long r = blockIdx.x; r < p.rows; r += gridDim.x) {
         const XT* x = static_cast<const XT*>(p.x) + (size_t)r * p.D;
         const YT* dy = static_cast<const YT*>(p.dy) + (size_t)r * p.D;
         const float mean = p.mean[r], rstd = p.rstd[r];
-        float s1 = 0.f, s2 = 0.f;
+        float s[2] = {0.f, 0.f};
         for (int c = threadIdx.x; c < p.D; c += LONG_NT) {
-            float w[1] = {1.f};
-            if (p.weight) load_w<1>(p.weight, p.w_bf16, c, w);
-            const float wd = w[0] * ld_f32(dy + c);
-            s1 += wd;
-            s2 = fmaf(wd, (ld_f32(x + c) - mean) * rstd, s2);
+            const float w = p.weight ? load_w<1>(p.weight, p.w_bf16, c).v : 1.f;
+            const float wd = w * ld_f32(dy + c);
+            s[0] += wd;
+            s[1] = fmaf(wd, (ld_f32(x + c) - mean) * rstd, s[1]);
         }
-        grp.sum2(s1, s2);
-        s1 *= inv;
-        s2 *= inv;
+        grp.sum(s);
+        const float s1 = s[0] * inv, s2 = s[1] * inv;
         XT* dx = static_cast<XT*>(p.dx) + (size_t)r * p.D;
         for (int c = threadIdx.x; c < p.D; c += LONG_NT) {
-            float w[1] = {1.f};
-            if (p.weight) load_w<1>(p.weight, p.w_bf16, c, w);
+            const float w = p.weight ? load_w<1>(p.weight, p.w_bf16, c).v : 1.f;
             const float xh = (ld_f32(x + c) - mean) * rstd;
-            st_from_f32(dx + c, rstd * (w[0] * ld_f32(dy + c) - s1 - xh * s2));
+            st_from_f32(dx + c, rstd * (w * ld_f32(dy + c) - s1 - xh * s2));
         }
     }
 }
@@ -447,9 +539,12 @@ __global__ void __launch_bounds__(SUM_NT) norm_sum_kernel(NormParams p) {
     const int cols = (p.D + 31) / 32, which = blockIdx.x / cols, c = (blockIdx.x % cols) * 32 + lane;
     const bool weights = p.part_w && which == 0;
     const float* from = weights ? p.part_w : p.part_b;
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // launched ahead of the partial rows' end
     float s = 0.f;
-    if (c < p.D)
+    if (c < p.D) {
+#pragma unroll 4
         for (int i = warp; i < p.parts; i += 32) s += from[(size_t)i * p.D + c];
+    }
     sm[warp][lane] = s;
     __syncthreads();
     s = sm[lane][warp];                               // lane: partial; warp: column
