@@ -5,99 +5,58 @@
 #include "gdr.h"
 #include "host.cuh"
 #include "common.cuh"
+#include "beam.cuh"
 
 namespace gdr {
 namespace bms {
 
-constexpr int NT = 256;
-
-struct BeamParams {
-    int G, K, V, M;
-    long long row;
-    int eos;
-    const void* logits;
-    const float* scores;
-    const unsigned char* finished;
-    float* out_scores;
-    int* out_parent;
-    int* out_token;
-    double* lse;            // [G*K]
-};
-
-// log sum exp of one beam's logits per block, in 64 bits.
-template <typename XT>
-__global__ void __launch_bounds__(NT) beam_lse_kernel(BeamParams p) {
-    __shared__ double sm[NT];
-    const XT* x = static_cast<const XT*>(p.logits) + (size_t)blockIdx.x * p.row;
-    float top = -INFINITY;
-    for (int v = threadIdx.x; v < p.V; v += NT) top = fmaxf(top, ld_f32(x + v));
-    sm[threadIdx.x] = top;
-    __syncthreads();
-    for (int o = NT / 2; o > 0; o >>= 1) {
-        if (threadIdx.x < o) sm[threadIdx.x] = fmax(sm[threadIdx.x], sm[threadIdx.x + o]);
-        __syncthreads();
-    }
-    const double big = sm[0];
-    __syncthreads();
-    double s = 0.0;
-    for (int v = threadIdx.x; v < p.V; v += NT) s += exp((double)ld_f32(x + v) - big);
-    sm[threadIdx.x] = s;
-    __syncthreads();
-    for (int o = NT / 2; o > 0; o >>= 1) {
-        if (threadIdx.x < o) sm[threadIdx.x] += sm[threadIdx.x + o];
-        __syncthreads();
-    }
-    if (threadIdx.x == 0) p.lse[blockIdx.x] = big + log(sm[0]);
+// Pieces of a row: 8192 elements (32 per thread) when the rows fill the GPU with them, 2048 (8 per
+// thread) otherwise, so that a few beams still spread over the SMs.
+static void plan_pieces(const gdr_beam_desc* d, int* piece, int* pieces) {
+    const long long rows = (long long)d->G * d->K, big = (d->V + 8191) / 8192;
+    *piece = rows * big >= 2LL * device_sm_count() ? 8192 : 2048;
+    *pieces = (d->V + *piece - 1) / *piece;
 }
 
-struct Cand { double s; int at; };
-__device__ __forceinline__ bool before(const Cand& a, const Cand& b) { return a.s > b.s || (a.s == b.s && a.at < b.at); }
-
-template <typename XT>
-__device__ __forceinline__ double cand_score(const BeamParams& p, int g, int k, int v) {
-    const size_t row = (size_t)g * p.K + k;
-    const double sc = p.scores[row];
-    double s;
-    if (p.finished && p.finished[row]) s = v == p.eos ? sc : -INFINITY;
-    else s = sc + ((double)ld_f32(static_cast<const XT*>(p.logits) + row * p.row + v) - p.lse[row]);
-    return s != s || s == INFINITY ? -INFINITY : s;
-}
-
-// M rounds over a group's candidates: each takes the best one behind the last.
-template <typename XT>
-__global__ void __launch_bounds__(NT) beam_pick_kernel(BeamParams p) {
-    __shared__ Cand sm[NT];
-    const int g = blockIdx.x, n = p.K * p.V;
-    Cand last = {INFINITY, -1};
-    for (int m = 0; m < p.M; ++m) {
-        Cand best = {-INFINITY, INT32_MAX};
-        for (int i = threadIdx.x; i < n; i += NT) {
-            const Cand c = {cand_score<XT>(p, g, i / p.V, i % p.V), i};
-            if (before(last, c) && before(c, best)) best = c;
-        }
-        sm[threadIdx.x] = best;
-        __syncthreads();
-        for (int o = NT / 2; o > 0; o >>= 1) {
-            if (threadIdx.x < o && before(sm[threadIdx.x + o], sm[threadIdx.x])) sm[threadIdx.x] = sm[threadIdx.x + o];
-            __syncthreads();
-        }
-        last = sm[0];
-        __syncthreads();
-        if (threadIdx.x == 0) {
-            const size_t at = (size_t)g * p.M + m;
-            p.out_scores[at] = (float)last.s;
-            p.out_parent[at] = last.at / p.V;
-            p.out_token[at] = last.at % p.V;
-        }
+// The workspace: the pieces' sums, their best logits and tokens.
+static size_t workspace_of(const gdr_beam_desc* d, BeamParams* p, void* base) {
+    int piece, pieces;
+    plan_pieces(d, &piece, &pieces);
+    const size_t n = (size_t)d->G * d->K * pieces;
+    if (p) {
+        p->piece = piece; p->pieces = pieces;
+        p->sums = static_cast<float2*>(base);
+        p->best = reinterpret_cast<float*>(p->sums + n);
+        p->token = reinterpret_cast<int*>(p->best + n * d->M);
     }
+    return n * (sizeof(float2) + (size_t)d->M * (sizeof(float) + sizeof(int)));
 }
 
 template <typename XT>
 static gdr_status launch_select(const BeamParams& p, cudaStream_t st) {
-    beam_lse_kernel<XT><<<p.G * p.K, NT, 0, st>>>(p);
-    beam_pick_kernel<XT><<<p.G, NT, 0, st>>>(p);
-    const cudaError_t e = cudaGetLastError();
-    return e == cudaSuccess ? GDR_OK : cuda_fail(e, "launch(beam selection)");
+    const dim3 grid(p.pieces, p.G * p.K);
+    // 16-byte loads where every row starts on them
+    const bool vec = reinterpret_cast<uintptr_t>(p.logits) % 16 == 0 && p.row * sizeof(XT) % 16 == 0;
+    if (p.piece == 8192) {
+        if (vec) beam_row_kernel<XT, 32, true><<<grid, NT, 0, st>>>(p);
+        else beam_row_kernel<XT, 32, false><<<grid, NT, 0, st>>>(p);
+    } else {
+        if (vec) beam_row_kernel<XT, 8, true><<<grid, NT, 0, st>>>(p);
+        else beam_row_kernel<XT, 8, false><<<grid, NT, 0, st>>>(p);
+    }
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return cuda_fail(e, "launch(beam rows)");
+    cudaLaunchConfig_t cfg = {};        // launched ahead of the rows' end, waits for it
+    cfg.gridDim = dim3(p.G);
+    cfg.blockDim = dim3(NT);
+    cfg.stream = st;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, beam_group_kernel<XT>, p);
+    return e == cudaSuccess ? GDR_OK : cuda_fail(e, "launch(beam groups)");
 }
 
 static gdr_status check_desc(const gdr_beam_desc* d) {
@@ -106,47 +65,12 @@ static gdr_status check_desc(const gdr_beam_desc* d) {
     if (d->K < 1 || d->K > 64 || d->M < 1 || d->M > 64) return fail(GDR_ERR_UNSUPPORTED, "K and M must be 1 .. 64%s");
     if (d->V < 1) return fail(GDR_ERR_INVALID_ARG, "V must be >= 1%s");
     const long long n = (long long)d->K * d->V;
-    if (n > 0x7fffffffLL || (long long)d->G * d->K > 0x7fffffffLL)
-        return fail(GDR_ERR_UNSUPPORTED, "K * V and G * K must be below 2^31%s");
+    if (n > 0x7fffffffLL) return fail(GDR_ERR_UNSUPPORTED, "K * V must be below 2^31%s");
+    if ((long long)d->G * d->K > 65535) return fail(GDR_ERR_UNSUPPORTED, "G * K must be at most 65535%s");
     if (d->M > n) return fail(GDR_ERR_INVALID_ARG, "M must be at most K * V%s");
     if (d->row != 0 && d->row < d->V) return fail(GDR_ERR_INVALID_ARG, "row must be 0 or at least V%s");
     if (!dtype_ok(d->x_dtype)) return fail(GDR_ERR_INVALID_ARG, "bad dtype%s");
     return GDR_OK;
-}
-
-// ---------------------------------------------------------------- reorder ----
-
-struct ReorderParams {
-    int G, K;
-    size_t n;               // elements (of the kernel's width) of one state
-    char* S;
-    const int* parent;
-};
-
-// One thread owns one position of the K states of a group: it reads what every moving beam takes
-// over, and only then writes, so that the exchange needs no second buffer and no other thread.
-template <typename VT, int KMAX>
-__global__ void __launch_bounds__(NT) reorder_kernel(ReorderParams p) {
-    const int g = blockIdx.y % p.G;
-    const int* parent = p.parent + (size_t)g * p.K;
-    VT* S = reinterpret_cast<VT*>(p.S) + (size_t)blockIdx.y * p.K * p.n;
-    if (blockIdx.x == 0 && blockIdx.y < p.G && threadIdx.x < p.K) {
-        const int q = parent[threadIdx.x];
-        if (q < 0 || q >= p.K) atomicOr(&g_device_status, STATUS_INDEX);
-    }
-    for (size_t i = (size_t)blockIdx.x * NT + threadIdx.x; i < p.n; i += (size_t)gridDim.x * NT) {
-        VT v[KMAX];
-        bool moves[KMAX];
-#pragma unroll
-        for (int j = 0; j < KMAX; ++j) {
-            const int q = j < p.K ? parent[j] : j;
-            moves[j] = q != j && q >= 0 && q < p.K;
-            if (moves[j]) v[j] = S[(size_t)q * p.n + i];
-        }
-#pragma unroll
-        for (int j = 0; j < KMAX; ++j)
-            if (moves[j]) S[(size_t)j * p.n + i] = v[j];
-    }
 }
 
 template <typename VT>
@@ -174,7 +98,7 @@ extern "C" {
 
 size_t gdr_beam_select_workspace_bytes(const gdr_beam_desc* d) {
     if (bms::check_desc(d) != GDR_OK) return 0;
-    return (size_t)d->G * d->K * sizeof(double);
+    return bms::workspace_of(d, nullptr, nullptr);
 }
 
 gdr_status gdr_beam_select(const gdr_beam_desc* d, const void* logits, const float* scores,
@@ -198,7 +122,7 @@ gdr_status gdr_beam_select(const gdr_beam_desc* d, const void* logits, const flo
     p.G = d->G; p.K = d->K; p.V = d->V; p.M = d->M; p.row = d->row ? d->row : d->V; p.eos = d->eos;
     p.logits = logits; p.scores = scores; p.finished = finished;
     p.out_scores = out_scores; p.out_parent = out_parent; p.out_token = out_token;
-    p.lse = static_cast<double*>(workspace);
+    bms::workspace_of(d, &p, workspace);
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     return d->x_dtype == GDR_BF16 ? bms::launch_select<__nv_bfloat16>(p, st) : bms::launch_select<float>(p, st);
 }
