@@ -48,7 +48,7 @@ static gdr_status launch_select(const BeamParams& p, cudaStream_t st) {
     if (e != cudaSuccess) return cuda_fail(e, "launch(beam rows)");
     cudaLaunchConfig_t cfg = {};        // launched ahead of the rows' end, waits for it
     cfg.gridDim = dim3(p.G);
-    cfg.blockDim = dim3(NT);
+    cfg.blockDim = dim3(GNT);
     cfg.stream = st;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

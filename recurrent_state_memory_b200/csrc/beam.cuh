@@ -5,10 +5,10 @@
 //
 //   1. beam_row_kernel: a block per (beam, piece of the vocabulary) reads its piece once into
 //      registers and leaves the piece's maximum, its sum of exp(x - maximum) and its M best
-//      (logit, token) pairs, unordered.  Every warp takes the q-th largest of its lanes' own maxima,
-//      q = M / warps rounded up; at least M elements reach the smallest of these marks, and for
-//      logits in no particular order only a few more do, so one sweep over the registers collects
-//      them all and a count of the larger ones ranks them.
+//      (logit, token) pairs.  Every warp puts down the few largest of its lanes' own maxima; the M-th
+//      largest of these marks is reached by at least M elements, and for logits in no particular
+//      order by few more, so one sweep over the registers collects them all and a count of the
+//      larger ones ranks them.
 //   2. beam_group_kernel: a block per group merges its beams' pieces the same way.  Its sums hold
 //      fp32 exponentials; where two neighbours of the list from different beams are closer than
 //      those allow (TOL), the beams' sums are formed again from the logits in 64 bits and the
@@ -52,51 +52,55 @@ __device__ __forceinline__ unsigned key_of(float x) {
 }
 __device__ __forceinline__ float value_of(unsigned k) { return __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k); }
 
-// The q-th largest of the lanes' keys (equal ones count one by one); 0 when fewer are above zero.
-__device__ __forceinline__ unsigned warp_mark(unsigned key, int q) {
-    unsigned m = 0;
+// The q largest of the lanes' keys (equal ones count one by one), by lane 0 into out[0 .. q).
+__device__ __forceinline__ void warp_best(unsigned key, int q, unsigned* out) {
+    const int lane = threadIdx.x & 31;
     for (int i = 0; i < q; ++i) {
-        m = __reduce_max_sync(0xffffffffu, key);
+        const unsigned m = __reduce_max_sync(0xffffffffu, key);
         const unsigned who = __ballot_sync(0xffffffffu, key == m);
-        if ((int)(threadIdx.x & 31) == __ffs(who) - 1) key = 0;
+        if (lane == __ffs(who) - 1) key = 0;
+        if (lane == 0) out[i] = m;
     }
-    return m;
+}
+// The want-th largest of n keys in shared memory (0 when they are fewer), by every warp for itself.
+__device__ __forceinline__ unsigned nth_best(const unsigned* keys, int n, int want) {
+    const int lane = threadIdx.x & 31;
+    unsigned mark = 0;
+    if (n <= 32 && want <= 12) {                // few rounds of the largest are shorter than 32 comparisons
+        unsigned k = lane < n ? keys[lane] : 0u;
+        for (int i = 0; i < want; ++i) {
+            mark = __reduce_max_sync(0xffffffffu, k);
+            const unsigned who = __ballot_sync(0xffffffffu, k == mark);
+            if (lane == __ffs(who) - 1) k = 0;
+        }
+        return mark;
+    }
+    for (int i0 = 0; i0 < n; i0 += 32) {
+        const int i = i0 + lane;
+        const unsigned k = i < n ? keys[i] : 0u;
+        int rank = 0;
+#pragma unroll 8
+        for (int j = 0; j < n; ++j) rank += keys[j] > k || (keys[j] == k && j < i);
+        const unsigned who = __ballot_sync(0xffffffffu, i < n && rank == want - 1);
+        if (who) mark = __shfl_sync(0xffffffffu, k, __ffs(who) - 1);
+    }
+    return mark;
 }
 
-struct BlockSmem {
-    unsigned mark[WARPS];
-    float red[WARPS];
-    int count;
-    unsigned long long pick[WARPS];
-};
-
-__device__ __forceinline__ float block_max(float v, float* red) {
+// Sum over the 8 lanes that share a candidate.
+__device__ __forceinline__ int sum8(int v) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
-    __syncthreads();
-    v = red[0];
-#pragma unroll
-    for (int i = 1; i < WARPS; ++i) v = fmaxf(v, red[i]);
-    __syncthreads();
-    return v;
-}
-__device__ __forceinline__ float block_sum(float v, float* red) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
-    __syncthreads();
-    v = 0.f;
-#pragma unroll
-    for (int i = 0; i < WARPS; ++i) v += red[i];
-    __syncthreads();
+    for (int o = 4; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     return v;
 }
 
 // E elements per thread: 16-byte loads (VEC) or one by one.
 template <typename XT, int E, bool VEC>
-__global__ void __launch_bounds__(NT) beam_row_kernel(BeamParams p) {
-    __shared__ BlockSmem sm;
+__global__ void __launch_bounds__(NT, E > 8 ? 4 : 6) beam_row_kernel(BeamParams p) {
+    __shared__ unsigned marks[WARPS * 8];
+    __shared__ float2 sums[WARPS];
+    __shared__ int count;
+    __shared__ unsigned long long pick[WARPS];
     __shared__ unsigned long long list[LIST];       // key, then the token's complement: larger is better
     const int row = blockIdx.y, piece = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int v0 = piece * p.piece, n = min(p.piece, p.V - v0);      // this block's tokens
@@ -125,18 +129,16 @@ __global__ void __launch_bounds__(NT) beam_row_kernel(BeamParams p) {
             v[j] = o < n ? ld_f32(x + o) : -INFINITY;
         }
     }
+    if (threadIdx.x == 0) count = 0;
     float top = -INFINITY;
 #pragma unroll
     for (int i = 0; i < E; ++i) top = fmaxf(top, v[i]);              // passes NaN over
-    const unsigned mine = at(0) < n ? key_of(top) : 0u;
-    // the marks of the warps all of whose lanes hold elements (a short piece fills the first ones)
-    const int full = min((n + W - 1) / W, NT) / 32, q = full ? (p.M + full - 1) / full : 33;
-    const unsigned mark_w = q <= 32 && warp < full ? warp_mark(mine, q) : 0u;
-    if (lane == 0) sm.mark[warp] = mark_w;
-    if (threadIdx.x == 0) sm.count = 0;
-    const float big = block_max(top, sm.red);
-    // exp(x - big); all masked (big = -inf): nothing but NaN counts.  +inf gives NaN: the beam drops out.
-    const float base = big == -INFINITY ? 0.f : big;
+    const int q = p.M <= 16 ? 4 : 8;                                 // 32 or 64 marks: at least M
+    const unsigned key = at(0) < n ? key_of(top) : 0u, top_key = __reduce_max_sync(0xffffffffu, key);
+    warp_best(key, q, marks + warp * q);
+    // exp(x - maximum); all masked (maximum -inf): nothing but NaN counts.  +inf gives NaN: the beam
+    // drops out.
+    const float big = top_key ? value_of(top_key) : -INFINITY, base = big == -INFINITY ? 0.f : big;
     float s = 0.f;
 #pragma unroll
     for (int i = 0; i < E; ++i) {
@@ -144,61 +146,82 @@ __global__ void __launch_bounds__(NT) beam_row_kernel(BeamParams p) {
         asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"((v[i] - base) * 1.44269502f));
         s += e;
     }
-    s = block_sum(s, sm.red);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if (lane == 0) sums[warp] = make_float2(big, s);
+    __syncthreads();
     const size_t out = (size_t)row * p.pieces + piece;
-    if (threadIdx.x == 0) p.sums[out] = make_float2(big, s);
-
-    unsigned mark = sm.mark[0];
+    const unsigned mark = nth_best(marks, WARPS * q, p.M);
+    // this thread's elements that reach the mark; a mark of -inf or less lets everything through
+    unsigned hits = 0;
+    if (mark > key_of(-INFINITY)) {
+        const float least = value_of(mark);
 #pragma unroll
-    for (int w = 1; w < WARPS; ++w) mark = w < full ? min(mark, sm.mark[w]) : mark;
-    const float least = value_of(max(mark, 1u));                     // a zero mark lets everything through
-#pragma unroll
-    for (int i = 0; i < E; ++i) {
-        if (v[i] >= least || mark <= key_of(-INFINITY)) {
-            if (at(i) < n && key_of(v[i]) >= mark) {
-                const int slot = atomicAdd(&sm.count, 1);
-                if (slot < LIST) list[slot] = (unsigned long long)key_of(v[i]) << 32 | (unsigned)~at(i);
-            }
-        }
+        for (int i = 0; i < E; ++i) hits |= v[i] >= least ? 1u << i : 0u;
+    } else {
+        hits = (unsigned)((1ull << E) - 1);
+    }
+    auto element = [&](int i) { return (unsigned long long)key_of(ld_f32(x + at(i))) << 32 | (unsigned)~at(i); };
+    while (hits) {                                                   // few: read them again
+        const int i = __ffs(hits) - 1;
+        hits &= hits - 1;
+        if (at(i) >= n) continue;
+        const unsigned long long c = element(i);
+        if ((unsigned)(c >> 32) < mark) continue;
+        const int slot = atomicAdd(&count, 1);
+        if (slot < LIST) list[slot] = c;
     }
     __syncthreads();
-    const int have = sm.count;
+    const int have = count;
     float* best = p.best + out * p.M;
     int* token = p.token + out * p.M;
+    if (threadIdx.x == 0) {
+        float m = sums[0].x;
+#pragma unroll
+        for (int w = 1; w < WARPS; ++w) m = fmaxf(m, sums[w].x);
+        float t = 0.f;
+#pragma unroll
+        for (int w = 0; w < WARPS; ++w) {
+            // a masked warp adds nothing, unless it holds a NaN
+            if (sums[w].x > -INFINITY || sums[w].y != sums[w].y) t += sums[w].y * expf(sums[w].x - m);
+        }
+        p.sums[out] = make_float2(m, t);
+    }
     if (have <= LIST) {
-        // the rank of a candidate is the number of larger ones: all differ
-        for (int i = threadIdx.x; i < max(have, p.M); i += NT) {
-            if (i >= have) {
-                best[i] = -INFINITY;
-                token[i] = -1;
-                continue;
-            }
-            const unsigned long long c = list[i];
+        // the rank of a candidate is the number of larger ones (all differ), counted by 8 lanes
+        for (int i0 = 0; i0 < have; i0 += NT / 8) {
+            const int i = i0 + (int)threadIdx.x / 8;
+            const unsigned long long c = i < have ? list[i] : 0;
             int rank = 0;
-            for (int j = 0; j < have; ++j) rank += list[j] > c;
-            if (rank < p.M && GDR_INB(rank >= 0, 1001)) {
+            for (int j = threadIdx.x & 7; j < have; j += 8) rank += list[j] > c;
+            rank = sum8(rank);
+            if (i < have && (threadIdx.x & 7) == 0 && rank < p.M) {
                 best[rank] = value_of((unsigned)(c >> 32));
                 token[rank] = v0 + (int)~(unsigned)c;
             }
+        }
+        for (int i = have + threadIdx.x; i < p.M; i += NT) {
+            best[i] = -INFINITY;
+            token[i] = -1;
         }
     } else {
         // too many equal ones for the list: the largest, M times
         unsigned long long last = ~0ull;
         for (int m = 0; m < p.M; ++m) {
             unsigned long long c = 0;
-#pragma unroll
+#pragma unroll 1
             for (int i = 0; i < E; ++i) {
                 if (at(i) >= n) continue;
-                const unsigned long long k = (unsigned long long)key_of(v[i]) << 32 | (unsigned)~at(i);
+                const unsigned long long k = element(i);
                 if (k < last && k > c) c = k;
             }
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) { const unsigned long long k = __shfl_xor_sync(0xffffffffu, c, o); c = k > c ? k : c; }
-            if (lane == 0) sm.pick[warp] = c;
+            if (lane == 0) pick[warp] = c;
             __syncthreads();
             c = 0;
 #pragma unroll
-            for (int w = 0; w < WARPS; ++w) c = sm.pick[w] > c ? sm.pick[w] : c;
+            for (int w = 0; w < WARPS; ++w) c = pick[w] > c ? pick[w] : c;
             __syncthreads();
             last = c;
             if (threadIdx.x == 0) {
@@ -217,71 +240,96 @@ __device__ __forceinline__ unsigned key_of_score(double s) { return key_of(__dou
 
 // How far two scores may be from their 64-bit values together, u = 2^-24: an exponent d = x - maximum
 // and its product with the rounded log2(e) are off by 2.25 u |d|, |d| weighted by e^d is at most
-// log V <= 22: 50 u; the exponential 3 u; 32 sums in a thread and 16 across the block 48 u.  101 u =
-// 6.1e-6 of the sum, twice that for two beams.
+// log V <= 22: 50 u; the exponential 3 u; 32 sums in a thread, 5 in its warp, 8 across the block and
+// the warps' factors (4 u) 49 u.  102 u = 6.1e-6 of the sum, twice that for two beams.
 constexpr double TOL = 1.25e-5;
 
+constexpr int GNT = 1024;               // threads of a group's block
+constexpr int GWARPS = GNT / 32;
+constexpr int HELD = 2;                 // candidates of a thread that stay in registers
+
+// The 64-bit sum over one beam's logits.
 template <typename XT>
 __device__ double exact_lse(const BeamParams& p, int row, double big, double* red) {
     const XT* x = static_cast<const XT*>(p.logits) + (size_t)row * p.row;
     double s = 0.0;
-    for (int v = threadIdx.x; v < p.V; v += NT) s += exp((double)ld_f32(x + v) - big);
+    for (int v = threadIdx.x; v < p.V; v += GNT) s += exp((double)ld_f32(x + v) - big);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
     if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = s;
     __syncthreads();
     s = 0.0;
-#pragma unroll
-    for (int i = 0; i < WARPS; ++i) s += red[i];
+    for (int i = 0; i < GWARPS; ++i) s += red[i];
     __syncthreads();
     return big + log(s);
 }
 
 template <typename XT>
-__global__ void __launch_bounds__(NT) beam_group_kernel(BeamParams p) {
-    __shared__ BlockSmem sm;
+__global__ void __launch_bounds__(GNT) beam_group_kernel(BeamParams p) {
+    __shared__ unsigned marks[2 * (MOST + 1 + GWARPS)];
+    __shared__ int count;
     __shared__ Cand list[LIST];
     __shared__ Cand first[MOST + 1];                // the best in order, and the one behind
-    __shared__ double lse[MOST], top[MOST], red[WARPS];
+    __shared__ double lse[MOST], top[MOST], red[GWARPS];
     __shared__ float score[MOST];
     __shared__ unsigned char kind[MOST], redo[MOST];
     enum { LIVE, ENDED, OUT };                      // a beam that goes on, that has one candidate, that has none
     const int g = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int per = p.pieces * p.M, n = p.K * per;
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    for (int k = threadIdx.x; k < p.K; k += NT) {
+
+    // this thread's candidates: beam, position in its lists, logit and token.  A warp's lanes lie
+    // evenly over all beams and pieces, so that every warp has some of the best.
+    const int span = (n + 31) / 32;
+    auto index = [&](int u) { const int j = warp + u * GWARPS; return j < span ? lane * span + j : n; };
+    int hk[HELD], hj[HELD], ht[HELD];
+    float hx[HELD];
+#pragma unroll
+    for (int u = 0; u < HELD; ++u) {
+        const int i = index(u);
+        hk[u] = i / per;
+        hj[u] = i - hk[u] * per;
+        if (i < n) {
+            const size_t at = (size_t)g * n + i;
+            ht[u] = p.token[at];
+            hx[u] = p.best[at];
+        }
+    }
+    for (int k = warp; k < p.K; k += GWARPS) {      // a warp per beam, lanes along its pieces
         const size_t row = (size_t)g * p.K + k;
+        const float sc = p.scores[row];
+        const bool ended = p.finished && p.finished[row];
         float big = -INFINITY;
-        for (int i = 0; i < p.pieces; ++i) big = fmaxf(big, p.sums[row * p.pieces + i].x);
+        for (int i = lane; i < p.pieces; i += 32) big = fmaxf(big, p.sums[row * p.pieces + i].x);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
         double s = 0.0;
-        for (int i = 0; i < p.pieces; ++i) {
+        for (int i = lane; i < p.pieces; i += 32) {
             const float2 e = p.sums[row * p.pieces + i];
             // an all-masked piece adds nothing, unless it holds a NaN
-            s += e.x == -INFINITY ? (e.y != e.y ? (double)e.y : 0.0) : (double)e.y * exp((double)e.x - (double)big);
+            if (e.x > -INFINITY) s += (double)e.y * exp((double)e.x - (double)big);
+            else if (e.y != e.y) s = e.y;
         }
-        const float sc = p.scores[row];
-        const bool no_score = !(sc < INFINITY) || sc == -INFINITY;
-        const bool ended = p.finished && p.finished[row];
-        score[k] = sc;
-        top[k] = big;
-        lse[k] = (double)big + log(s);
-        kind[k] = no_score ? OUT : ended ? ENDED : !(big > -INFINITY && big < INFINITY && s == s) ? OUT : LIVE;
-        redo[k] = 0;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        if (lane == 0) {
+            const bool no_score = !(sc < INFINITY) || sc == -INFINITY;
+            score[k] = sc;
+            top[k] = big;
+            lse[k] = (double)big + log(s);
+            kind[k] = no_score ? OUT : ended ? ENDED : !(big > -INFINITY && big < INFINITY && s == s) ? OUT : LIVE;
+            redo[k] = 0;
+        }
     }
     __syncthreads();
 
-    const int per = p.pieces * p.M, n = p.K * per;
-    auto cand = [&](int i, Cand& c) -> bool {
-        const int k = i / per, j = i % per;
+    auto score_of = [&](int k, int j, int t, float x, Cand& c) -> bool {
         if (kind[k] == LIVE) {
-            const size_t at = ((size_t)g * p.K + k) * per + j;
-            const int t = p.token[at];
-            if (t < 0) return false;
-            c.s = (double)score[k] + ((double)p.best[at] - lse[k]);
+            c.s = (double)score[k] + ((double)x - lse[k]);
             c.at = k * p.V + t;
-            return true;
+            return t >= 0;
         }
         // without logits of its own: the lowest tokens at -inf, behind `eos` of a finished beam
-        if (j >= p.M || j >= p.V) return false;
         if (kind[k] == ENDED) {
             c.s = j == 0 ? (double)score[k] : -INFINITY;
             c.at = k * p.V + (j == 0 ? p.eos : j - 1 < p.eos ? j - 1 : j);
@@ -289,50 +337,59 @@ __global__ void __launch_bounds__(NT) beam_group_kernel(BeamParams p) {
             c.s = -INFINITY;
             c.at = k * p.V + j;
         }
-        return true;
+        return j < p.M && j < p.V;
+    };
+    // f(candidate) for this thread's candidates
+    auto each = [&](auto f) {
+#pragma unroll
+        for (int u = 0; u < HELD; ++u) {
+            Cand c;
+            if (index(u) < n && score_of(hk[u], hj[u], ht[u], hx[u], c)) f(c);
+        }
+        for (int u = HELD; warp + u * GWARPS < span; ++u) {
+            const int i = index(u);
+            if (i >= n) continue;
+            const size_t at = (size_t)g * n + i;
+            Cand c;
+            if (score_of(i / per, i % per, p.token[at], p.best[at], c)) f(c);
+        }
     };
     // one more than asked for: the candidate behind the last may be too near to it
     const long long all = (long long)p.K * p.V;
     const int want = (int)(all < p.M + 1 ? all : p.M + 1);
     for (int turn = 0; turn < 2; ++turn) {
         unsigned mine = 0;
-        for (int i = threadIdx.x; i < n; i += NT) {
-            Cand c;
-            if (cand(i, c)) mine = max(mine, key_of_score(c.s));
-        }
-        const unsigned mark_w = warp_mark(mine, (want + WARPS - 1) / WARPS);
-        if (lane == 0) sm.mark[warp] = mark_w;
-        if (threadIdx.x == 0) sm.count = 0;
+        each([&](const Cand& c) { mine = max(mine, key_of_score(c.s)); });
+        // marks of the warps that hold candidates: at least want (twice that where a warp gives several)
+        const int aw = min(GWARPS, span), q = aw >= want ? 1 : min(32, 2 * ((want + aw - 1) / aw));
+        if (warp < aw) warp_best(mine, q, marks + warp * q);
+        if (threadIdx.x == 0) count = 0;
         if (threadIdx.x <= p.M) first[threadIdx.x] = Cand{-INFINITY, -1};
         __syncthreads();
-        unsigned mark = sm.mark[0];
-#pragma unroll
-        for (int w = 1; w < WARPS; ++w) mark = min(mark, sm.mark[w]);
-        for (int i = threadIdx.x; i < n; i += NT) {
-            Cand c;
-            if (cand(i, c) && key_of_score(c.s) >= mark) {
-                const int slot = atomicAdd(&sm.count, 1);
-                if (slot < LIST) list[slot] = c;
-            }
-        }
+        const unsigned mark = nth_best(marks, aw * q, want);
+        each([&](const Cand& c) {
+            if (key_of_score(c.s) < mark) return;
+            const int slot = atomicAdd(&count, 1);
+            if (slot < LIST) list[slot] = c;
+        });
         __syncthreads();
-        const int have = sm.count;
+        const int have = count;
         if (have <= LIST) {
-            for (int i = threadIdx.x; i < have; i += NT) {
-                const Cand c = list[i];
+            for (int i0 = 0; i0 < have; i0 += GNT / 8) {
+                const int i = i0 + (int)threadIdx.x / 8;
+                const Cand c = i < have ? list[i] : Cand{0.0, 0};
                 int rank = 0;
-                for (int j = 0; j < have; ++j) rank += before(list[j], c);
-                if (rank < want) first[rank] = c;
+                for (int j = threadIdx.x & 7; j < have; j += 8) rank += before(list[j], c);
+                rank = sum8(rank);
+                if (i < have && (threadIdx.x & 7) == 0 && rank < want) first[rank] = c;
             }
             __syncthreads();
         } else {
+            // too many equal ones for the list: the best, want times
             Cand last = {INFINITY, -1};
             for (int m = 0; m < want; ++m) {
                 Cand b = {-INFINITY, INT32_MAX};
-                for (int i = threadIdx.x; i < n; i += NT) {
-                    Cand c;
-                    if (cand(i, c) && before(last, c) && before(c, b)) b = c;
-                }
+                each([&](const Cand& c) { if (before(last, c) && before(c, b)) b = c; });
 #pragma unroll
                 for (int o = 16; o > 0; o >>= 1) {
                     const Cand c = {__shfl_xor_sync(0xffffffffu, b.s, o), __shfl_xor_sync(0xffffffffu, b.at, o)};
@@ -341,8 +398,7 @@ __global__ void __launch_bounds__(NT) beam_group_kernel(BeamParams p) {
                 if (lane == 0) list[warp] = b;
                 __syncthreads();
                 b = list[0];
-#pragma unroll
-                for (int w = 1; w < WARPS; ++w) if (before(list[w], b)) b = list[w];
+                for (int w = 1; w < GWARPS; ++w) if (before(list[w], b)) b = list[w];
                 if (threadIdx.x == 0) first[m] = b;
                 last = b;
                 __syncthreads();
@@ -369,7 +425,7 @@ __global__ void __launch_bounds__(NT) beam_group_kernel(BeamParams p) {
         }
         __syncthreads();
     }
-    for (int m = threadIdx.x; m < p.M; m += NT) {
+    for (int m = threadIdx.x; m < p.M; m += GNT) {
         const size_t at = (size_t)g * p.M + m;
         const Cand c = first[m];
         if (!GDR_INB(c.at >= 0 && (long long)c.at < all, 1011)) continue;
