@@ -5,8 +5,8 @@
 //
 //   1. beam_row_kernel: a block per (beam, piece of the vocabulary) reads its piece once into
 //      registers and leaves the piece's maximum, its sum of exp(x - maximum) and its M best
-//      (logit, token) pairs.  Every warp puts down the few largest of its lanes' own maxima; the M-th
-//      largest of these marks is reached by at least M elements, and for logits in no particular
+//      (logit, token) pairs.  The M-th largest of the maxima of groups of
+//      lanes is reached by at least M elements, and for logits in no particular
 //      order by few more, so one sweep over the registers collects them all and a count of the
 //      larger ones ranks them.
 //   2. beam_group_kernel: a block per group merges its beams' pieces the same way.  Its sums hold
@@ -52,39 +52,31 @@ __device__ __forceinline__ unsigned key_of(float x) {
 }
 __device__ __forceinline__ float value_of(unsigned k) { return __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k); }
 
-// The q largest of the lanes' keys (equal ones count one by one), by lane 0 into out[0 .. q).
-__device__ __forceinline__ void warp_best(unsigned key, int q, unsigned* out) {
-    const int lane = threadIdx.x & 31;
-    for (int i = 0; i < q; ++i) {
-        const unsigned m = __reduce_max_sync(0xffffffffu, key);
-        const unsigned who = __ballot_sync(0xffffffffu, key == m);
-        if (lane == __ffs(who) - 1) key = 0;
-        if (lane == 0) out[i] = m;
-    }
+// A mark that at least `want` of a block's keys reach, and few more of keys in no particular order:
+// the want-th largest of the maxima of groups of lanes.  group_lanes: the largest groups of which
+// the `active` first threads make at least 2 * want (so at most 4 * want, unless a group is one
+// lane).  0 when there are not that many; it then lets everything through.
+constexpr int MARKS = 4 * (MOST + 1);
+__device__ __forceinline__ int group_lanes(int active, int want) {
+    int l = 32;
+    while (l > 1 && active < 2 * want * l) l >>= 1;
+    return l;
 }
-// The want-th largest of n keys in shared memory (0 when they are fewer), by every warp for itself.
-__device__ __forceinline__ unsigned nth_best(const unsigned* keys, int n, int want) {
+__device__ __forceinline__ void put_marks(unsigned key, int lanes, int active, unsigned* marks) {
+    for (int o = 1; o < lanes; o <<= 1) key = max(key, __shfl_xor_sync(0xffffffffu, key, o));
+    if ((threadIdx.x & (lanes - 1)) == 0 && (int)threadIdx.x < active) marks[threadIdx.x / lanes] = key;
+}
+// Behind a barrier; *mark was set to 0 before it.  Each warp compares 32 of the n marks with all.
+template <int WARPS_> __device__ __forceinline__ void find_mark(const unsigned* marks, int n, int want, unsigned* mark) {
     const int lane = threadIdx.x & 31;
-    unsigned mark = 0;
-    if (n <= 32 && want <= 12) {                // few rounds of the largest are shorter than 32 comparisons
-        unsigned k = lane < n ? keys[lane] : 0u;
-        for (int i = 0; i < want; ++i) {
-            mark = __reduce_max_sync(0xffffffffu, k);
-            const unsigned who = __ballot_sync(0xffffffffu, k == mark);
-            if (lane == __ffs(who) - 1) k = 0;
-        }
-        return mark;
-    }
-    for (int i0 = 0; i0 < n; i0 += 32) {
+    for (int i0 = (threadIdx.x >> 5) * 32; i0 < n; i0 += WARPS_ * 32) {
         const int i = i0 + lane;
-        const unsigned k = i < n ? keys[i] : 0u;
+        const unsigned k = i < n ? marks[i] : 0u;
         int rank = 0;
 #pragma unroll 8
-        for (int j = 0; j < n; ++j) rank += keys[j] > k || (keys[j] == k && j < i);
-        const unsigned who = __ballot_sync(0xffffffffu, i < n && rank == want - 1);
-        if (who) mark = __shfl_sync(0xffffffffu, k, __ffs(who) - 1);
+        for (int j = 0; j < n; ++j) rank += marks[j] > k || (marks[j] == k && j < i);
+        if (i < n && rank == want - 1) *mark = k;
     }
-    return mark;
 }
 
 // Sum over the 8 lanes that share a candidate.
@@ -97,12 +89,13 @@ __device__ __forceinline__ int sum8(int v) {
 // E elements per thread: 16-byte loads (VEC) or one by one.
 template <typename XT, int E, bool VEC>
 __global__ void __launch_bounds__(NT, E > 8 ? 4 : 6) beam_row_kernel(BeamParams p) {
-    __shared__ unsigned marks[WARPS * 8];
+    __shared__ unsigned marks[MARKS], the_mark;
     __shared__ float2 sums[WARPS];
     __shared__ int count;
     __shared__ unsigned long long pick[WARPS];
     __shared__ unsigned long long list[LIST];       // key, then the token's complement: larger is better
     const int row = blockIdx.y, piece = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    asm volatile("griddepcontrol.launch_dependents;");               // the groups' blocks may come; they wait
     const int v0 = piece * p.piece, n = min(p.piece, p.V - v0);      // this block's tokens
     const XT* x = static_cast<const XT*>(p.logits) + (size_t)row * p.row + v0;
     constexpr int W = VEC ? 16 / (int)sizeof(XT) : 1;                // elements of a load
@@ -129,13 +122,13 @@ __global__ void __launch_bounds__(NT, E > 8 ? 4 : 6) beam_row_kernel(BeamParams 
             v[j] = o < n ? ld_f32(x + o) : -INFINITY;
         }
     }
-    if (threadIdx.x == 0) count = 0;
+    if (threadIdx.x == 0) { count = 0; the_mark = 0; }
     float top = -INFINITY;
 #pragma unroll
     for (int i = 0; i < E; ++i) top = fmaxf(top, v[i]);              // passes NaN over
-    const int q = p.M <= 16 ? 4 : 8;                                 // 32 or 64 marks: at least M
+    const int active = min((n + W - 1) / W, NT), lanes = group_lanes(active, p.M);
     const unsigned key = at(0) < n ? key_of(top) : 0u, top_key = __reduce_max_sync(0xffffffffu, key);
-    warp_best(key, q, marks + warp * q);
+    put_marks(key, lanes, active, marks);
     // exp(x - maximum); all masked (maximum -inf): nothing but NaN counts.  +inf gives NaN: the beam
     // drops out.
     const float big = top_key ? value_of(top_key) : -INFINITY, base = big == -INFINITY ? 0.f : big;
@@ -150,8 +143,10 @@ __global__ void __launch_bounds__(NT, E > 8 ? 4 : 6) beam_row_kernel(BeamParams 
     for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
     if (lane == 0) sums[warp] = make_float2(big, s);
     __syncthreads();
+    find_mark<WARPS>(marks, (active + lanes - 1) / lanes, p.M, &the_mark);
+    __syncthreads();
     const size_t out = (size_t)row * p.pieces + piece;
-    const unsigned mark = nth_best(marks, WARPS * q, p.M);
+    const unsigned mark = the_mark;
     // this thread's elements that reach the mark; a mark of -inf or less lets everything through
     unsigned hits = 0;
     if (mark > key_of(-INFINITY)) {
@@ -240,9 +235,11 @@ __device__ __forceinline__ unsigned key_of_score(double s) { return key_of(__dou
 
 // How far two scores may be from their 64-bit values together, u = 2^-24: an exponent d = x - maximum
 // and its product with the rounded log2(e) are off by 2.25 u |d|, |d| weighted by e^d is at most
-// log V <= 22: 50 u; the exponential 3 u; 32 sums in a thread, 5 in its warp, 8 across the block and
-// the warps' factors (4 u) 49 u.  102 u = 6.1e-6 of the sum, twice that for two beams.
-constexpr double TOL = 1.25e-5;
+// log V <= 22: 50 u; the exponential 3 u; 32 sums in a thread, 5 in its warp, 8 across the block and the
+// factors of warps and pieces (4 u each; the pieces are added in 64 bits) 53 u: together 106 u of the
+// sum, as much in its logarithm, whose rounding adds 17 u (it is at most 22).  123 u = 7.4e-6, twice
+// that for two beams.
+constexpr double TOL = 1.5e-5;
 
 constexpr int GNT = 1024;               // threads of a group's block
 constexpr int GWARPS = GNT / 32;
@@ -266,7 +263,7 @@ __device__ double exact_lse(const BeamParams& p, int row, double big, double* re
 
 template <typename XT>
 __global__ void __launch_bounds__(GNT) beam_group_kernel(BeamParams p) {
-    __shared__ unsigned marks[2 * (MOST + 1 + GWARPS)];
+    __shared__ unsigned marks[MARKS], the_mark;
     __shared__ int count;
     __shared__ Cand list[LIST];
     __shared__ Cand first[MOST + 1];                // the best in order, and the one behind
@@ -276,6 +273,9 @@ __global__ void __launch_bounds__(GNT) beam_group_kernel(BeamParams p) {
     enum { LIVE, ENDED, OUT };                      // a beam that goes on, that has one candidate, that has none
     const int g = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int per = p.pieces * p.M, n = p.K * per;
+    float sc = 0.f;                                 // of beam `warp`: older than the rows' launch
+    bool ended = false;
+    if (warp < p.K) { sc = p.scores[(size_t)g * p.K + warp]; ended = p.finished && p.finished[(size_t)g * p.K + warp]; }
     asm volatile("griddepcontrol.wait;" ::: "memory");
 
     // this thread's candidates: beam, position in its lists, logit and token.  A warp's lanes lie
@@ -297,26 +297,28 @@ __global__ void __launch_bounds__(GNT) beam_group_kernel(BeamParams p) {
     }
     for (int k = warp; k < p.K; k += GWARPS) {      // a warp per beam, lanes along its pieces
         const size_t row = (size_t)g * p.K + k;
-        const float sc = p.scores[row];
-        const bool ended = p.finished && p.finished[row];
-        float big = -INFINITY;
-        for (int i = lane; i < p.pieces; i += 32) big = fmaxf(big, p.sums[row * p.pieces + i].x);
+        const float2* sums = p.sums + row * p.pieces;
+        if (k != warp) { sc = p.scores[row]; ended = p.finished && p.finished[row]; }
+        const float2 mine = lane < p.pieces ? sums[lane] : make_float2(-INFINITY, 0.f);
+        float big = mine.x;
+        for (int i = lane + 32; i < p.pieces; i += 32) big = fmaxf(big, sums[i].x);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
         double s = 0.0;
-        for (int i = lane; i < p.pieces; i += 32) {
-            const float2 e = p.sums[row * p.pieces + i];
+        auto add = [&](float2 e) {
             // an all-masked piece adds nothing, unless it holds a NaN
-            if (e.x > -INFINITY) s += (double)e.y * exp((double)e.x - (double)big);
+            if (e.x > -INFINITY) s += (double)(e.y * expf(e.x - big));
             else if (e.y != e.y) s = e.y;
-        }
+        };
+        add(mine);
+        for (int i = lane + 32; i < p.pieces; i += 32) add(sums[i]);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
         if (lane == 0) {
             const bool no_score = !(sc < INFINITY) || sc == -INFINITY;
             score[k] = sc;
             top[k] = big;
-            lse[k] = (double)big + log(s);
+            lse[k] = (double)big + (double)logf((float)s);
             kind[k] = no_score ? OUT : ended ? ENDED : !(big > -INFINITY && big < INFINITY && s == s) ? OUT : LIVE;
             redo[k] = 0;
         }
@@ -360,13 +362,14 @@ __global__ void __launch_bounds__(GNT) beam_group_kernel(BeamParams p) {
     for (int turn = 0; turn < 2; ++turn) {
         unsigned mine = 0;
         each([&](const Cand& c) { mine = max(mine, key_of_score(c.s)); });
-        // marks of the warps that hold candidates: at least want (twice that where a warp gives several)
-        const int aw = min(GWARPS, span), q = aw >= want ? 1 : min(32, 2 * ((want + aw - 1) / aw));
-        if (warp < aw) warp_best(mine, q, marks + warp * q);
-        if (threadIdx.x == 0) count = 0;
+        const int active = 32 * min(GWARPS, span), lanes = group_lanes(active, want);
+        put_marks(mine, lanes, active, marks);
+        if (threadIdx.x == 0) { count = 0; the_mark = 0; }
         if (threadIdx.x <= p.M) first[threadIdx.x] = Cand{-INFINITY, -1};
         __syncthreads();
-        const unsigned mark = nth_best(marks, aw * q, want);
+        find_mark<GWARPS>(marks, active / lanes, want, &the_mark);
+        __syncthreads();
+        const unsigned mark = the_mark;
         each([&](const Cand& c) {
             if (key_of_score(c.s) < mark) return;
             const int slot = atomicAdd(&count, 1);
