@@ -229,6 +229,7 @@ def use_library(path: str) -> None:
     global LIB_PATH, _lib
     LIB_PATH = path
     _lib = None
+    _descs.clear()
 
 
 def debug_bounds_site() -> int:
@@ -492,6 +493,25 @@ def decode_step(q, k, v, g, beta, S, theta=None, *, gate_mode=GATE_NEG_SOFTPLUS,
 
 
 # ------------------------------------------------ scan, layer norm, beam search ----
+#
+# These calls are short (a serving token's kernel takes a few microseconds), so the binding spends
+# little on the host: outputs by empty_like / new_empty, descriptors kept by their sizes, the raw
+# stream handle.
+
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
+_descs = {}
+
+
+def _desc(make, *key):
+    """The descriptor make(*key), and what make wants to keep beside it, made once per sizes and types."""
+    k = (make, key)
+    d = _descs.get(k)
+    if d is None:
+        if len(_descs) >= 4096:         # sizes that change from call to call
+            _descs.clear()
+        d = _descs[k] = make(*key)
+    return d
 
 
 def _on_device(t: torch.Tensor, name: str):
@@ -500,10 +520,12 @@ def _on_device(t: torch.Tensor, name: str):
     return t.device
 
 
-def _check_shape(t, name, shape, dtype, dev):
+def _want(t, name, shape, dtype, dev):
+    """t has this shape, type and device and is contiguous (dtype None: any the library takes)."""
+    if t.shape == shape and t.device == dev and t.is_contiguous() and (t.dtype is dtype or dtype is None):
+        return
     _need(t, name, dtype, dev)
-    if tuple(t.shape) != shape:
-        raise ValueError(f"{name} must have the shape {shape}, got {tuple(t.shape)}")
+    raise ValueError(f"{name} must have the shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
 def _row_stride(t: torch.Tensor, name: str) -> int:
@@ -523,12 +545,19 @@ def _row_stride(t: torch.Tensor, name: str) -> int:
 
 def _call(fn, where, dev, stream, *args):
     """One library call on `stream` (default: dev's current stream) with dev current."""
-    if dev.index == torch.cuda.current_device():
-        st = fn(*args, _stream_handle(stream, dev))
+    i = dev.index
+    s = _raw_stream(i) if stream is None else stream.cuda_stream
+    if _current_device() == i:
+        st = fn(*args, s)
     else:
-        with torch.cuda.device(dev):
-            st = fn(*args, _stream_handle(stream, dev))
-    _check(st, where)
+        with torch.cuda.device(i):
+            st = fn(*args, s)
+    if st:
+        _check(st, where)
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
 
 
 def _scan_args(x, g, dims, lengths=None):
@@ -538,7 +567,7 @@ def _scan_args(x, g, dims, lengths=None):
     if g.device != dev:
         raise ValueError(f"g is on {g.device}, expected {dev}")
     if lengths is not None:
-        _check_shape(lengths, "lengths", (x.shape[0],), torch.int32, dev)
+        _want(lengths, "lengths", (x.shape[0],), torch.int32, dev)
     return dev
 
 
@@ -561,13 +590,17 @@ def scan_fwd(x, g, h0=None, *, gate_mode=GATE_NEG_SOFTPLUS, tied=False, lengths=
     B, T, D = x.shape
     out_dtype = out_dtype or x.dtype
     if h0 is not None:
-        _check_shape(h0, "h0", (B, D), torch.float32, dev)
-    desc = scan_desc(B, T, D, x.dtype, g.dtype, out_dtype, gate_mode, tied, _row_stride(x, "x"), _row_stride(g, "g"))
-    h = torch.empty((B, T, D), dtype=out_dtype, device=dev)
-    h_T = torch.empty((B, D), dtype=torch.float32, device=dev) if want_state else None
-    ckpt = torch.empty((B, -(-T // SCAN_CKPT), D), dtype=torch.float32, device=dev) if want_ckpt else None
-    _call(lib().gdr_scan_fwd, "gdr_scan_fwd", dev, stream, desc, _ptr(x), _ptr(g), _ptr(h0), _ptr(lengths), _ptr(h),
-          _ptr(h_T), _ptr(ckpt))
+        _want(h0, "h0", (B, D), torch.float32, dev)
+    desc = _desc(scan_desc, B, T, D, x.dtype, g.dtype, out_dtype, gate_mode, tied, _row_stride(x, "x"),
+                 _row_stride(g, "g"))
+    h = x.new_empty((B, T, D), dtype=out_dtype)
+    h_T = ckpt = None
+    if want_state:
+        h_T = x.new_empty((B, D), dtype=torch.float32) if h0 is None else torch.empty_like(h0)
+    if want_ckpt:
+        ckpt = x.new_empty((B, -(-T // SCAN_CKPT), D), dtype=torch.float32)
+    _call(lib().gdr_scan_fwd, "gdr_scan_fwd", dev, stream, desc, x.data_ptr(), g.data_ptr(), _at(h0), _at(lengths),
+          h.data_ptr(), _at(h_T), _at(ckpt))
     return (h, h_T, ckpt) if want_ckpt else (h, h_T)
 
 
@@ -578,18 +611,21 @@ def scan_bwd(x, g, ckpt, dh=None, dh_T=None, *, gate_mode=GATE_NEG_SOFTPLUS, tie
     "x" (x's dtype), "g" (g's dtype), "h0" (fp32; None unless want_dh0)."""
     dev = _scan_args(x, g, 3, lengths)
     B, T, D = x.shape
-    _check_shape(ckpt, "ckpt", (B, -(-T // SCAN_CKPT), D), torch.float32, dev)
+    _want(ckpt, "ckpt", (B, -(-T // SCAN_CKPT), D), torch.float32, dev)
     if dh is not None:
-        _check_shape(dh, "dh", (B, T, D), None, dev)
+        _want(dh, "dh", (B, T, D), None, dev)
     if dh_T is not None:
-        _check_shape(dh_T, "dh_T", (B, D), torch.float32, dev)
-    desc = scan_desc(B, T, D, x.dtype, g.dtype, x.dtype if dh is None else dh.dtype, gate_mode, tied,
-                     _row_stride(x, "x"), _row_stride(g, "g"))
-    out = {"x": torch.empty((B, T, D), dtype=x.dtype, device=dev), "g": torch.empty((B, T, D), dtype=g.dtype, device=dev),
-           "h0": torch.empty((B, D), dtype=torch.float32, device=dev) if want_dh0 else None}
-    _call(lib().gdr_scan_bwd, "gdr_scan_bwd", dev, stream, desc, _ptr(x), _ptr(g), _ptr(ckpt), _ptr(lengths), _ptr(dh),
-          _ptr(dh_T), _ptr(out["x"]), _ptr(out["g"]), _ptr(out["h0"]))
-    return out
+        _want(dh_T, "dh_T", (B, D), torch.float32, dev)
+    x_row, g_row = _row_stride(x, "x"), _row_stride(g, "g")
+    desc = _desc(scan_desc, B, T, D, x.dtype, g.dtype, x.dtype if dh is None else dh.dtype, gate_mode, tied, x_row, g_row)
+    dx = x.new_empty((B, T, D)) if x_row else torch.empty_like(x)
+    dg = g.new_empty((B, T, D)) if g_row else torch.empty_like(g)
+    dh0 = None
+    if want_dh0:
+        dh0 = x.new_empty((B, D), dtype=torch.float32) if dh_T is None else torch.empty_like(dh_T)
+    _call(lib().gdr_scan_bwd, "gdr_scan_bwd", dev, stream, desc, x.data_ptr(), g.data_ptr(), ckpt.data_ptr(),
+          _at(lengths), _at(dh), _at(dh_T), dx.data_ptr(), dg.data_ptr(), _at(dh0))
+    return {"x": dx, "g": dg, "h0": dh0}
 
 
 def scan_step(x, g, h, *, gate_mode=GATE_NEG_SOFTPLUS, tied=False, out_dtype=None, o=None, stream=None):
@@ -598,13 +634,15 @@ def scan_step(x, g, h, *, gate_mode=GATE_NEG_SOFTPLUS, tied=False, out_dtype=Non
     dev = _scan_args(x, g, 2)
     N, D = x.shape
     out_dtype = out_dtype or x.dtype
-    _check_shape(h, "h", (N, D), torch.float32, dev)
+    _want(h, "h", (N, D), torch.float32, dev)
     if o is None:
-        o = torch.empty((N, D), dtype=out_dtype, device=dev)
+        o = x.new_empty((N, D), dtype=out_dtype)
     else:
-        _check_shape(o, "o", (N, D), out_dtype, dev)
-    desc = scan_desc(N, 1, D, x.dtype, g.dtype, out_dtype, gate_mode, tied, _row_stride(x, "x"), _row_stride(g, "g"))
-    _call(lib().gdr_scan_step, "gdr_scan_step", dev, stream, desc, _ptr(x), _ptr(g), _ptr(h), _ptr(o))
+        _want(o, "o", (N, D), out_dtype, dev)
+    desc = _desc(scan_desc, N, 1, D, x.dtype, g.dtype, out_dtype, gate_mode, tied, _row_stride(x, "x"),
+                 _row_stride(g, "g"))
+    _call(lib().gdr_scan_step, "gdr_scan_step", dev, stream, desc, x.data_ptr(), g.data_ptr(), h.data_ptr(),
+          o.data_ptr())
     return o
 
 
@@ -613,10 +651,11 @@ def norm_desc(rows, D, x_dtype, y_dtype, w_dtype=torch.float32, eps=1e-5) -> Nor
 
 
 def _norm_weights(weight, bias, D, dev):
-    w_dtype = next((t.dtype for t in (weight, bias) if t is not None), torch.float32)
-    for t, n in ((weight, "weight"), (bias, "bias")):
-        if t is not None:
-            _check_shape(t, n, (D,), w_dtype, dev)
+    w_dtype = torch.float32 if weight is None and bias is None else (bias if weight is None else weight).dtype
+    if weight is not None:
+        _want(weight, "weight", (D,), w_dtype, dev)
+    if bias is not None:
+        _want(bias, "bias", (D,), w_dtype, dev)
     return w_dtype
 
 
@@ -628,16 +667,23 @@ def layernorm_fwd(x, weight=None, bias=None, *, eps=1e-5, out_dtype=None, want_s
     if x.dim() < 1:
         raise ValueError("x must have at least one dimension")
     _need(x, "x")
-    D = x.shape[-1]
-    out_dtype = out_dtype or x.dtype
+    shape = x.shape
+    D = shape[-1]
     w_dtype = _norm_weights(weight, bias, D, dev)
-    desc = norm_desc(x.numel() // max(D, 1), D, x.dtype, out_dtype, w_dtype, eps)
-    y = torch.empty(x.shape, dtype=out_dtype, device=dev)
-    mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=dev) if want_stats else None
-    rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=dev) if want_stats else None
-    _call(lib().gdr_layernorm_fwd, "gdr_layernorm_fwd", dev, stream, desc, _ptr(x), _ptr(weight), _ptr(bias), _ptr(y),
-          _ptr(mean), _ptr(rstd))
+    y = torch.empty_like(x, dtype=out_dtype) if out_dtype is not None and out_dtype is not x.dtype else torch.empty_like(x)
+    desc = _desc(norm_desc, x.numel() // D if D else 0, D, x.dtype, y.dtype, w_dtype, eps)
+    mean = rstd = None
+    if want_stats:
+        mean = x.new_empty(shape[:-1], dtype=torch.float32)
+        rstd = torch.empty_like(mean)
+    _call(lib().gdr_layernorm_fwd, "gdr_layernorm_fwd", dev, stream, desc, x.data_ptr(), _at(weight), _at(bias),
+          y.data_ptr(), _at(mean), _at(rstd))
     return y, mean, rstd
+
+
+def _norm_bwd_plan(rows, D, x_dtype, y_dtype, w_dtype, with_w, with_b):
+    desc = norm_desc(rows, D, x_dtype, y_dtype, w_dtype, 0.0)
+    return desc, int(lib().gdr_layernorm_bwd_workspace_bytes(desc, with_w, with_b))
 
 
 def layernorm_bwd(x, dy, mean, rstd, weight=None, *, with_bias=True, want_dx=True, workspace=None, stream=None):
@@ -646,21 +692,24 @@ def layernorm_bwd(x, dy, mean, rstd, weight=None, *, with_bias=True, want_dx=Tru
     unless with_bias)."""
     dev = _on_device(x, "x")
     _need(x, "x")
-    D = x.shape[-1]
-    _check_shape(dy, "dy", tuple(x.shape), None, dev)
-    for t, n in ((mean, "mean"), (rstd, "rstd")):
-        _check_shape(t, n, tuple(x.shape[:-1]), torch.float32, dev)
+    shape = x.shape
+    D = shape[-1]
+    _want(dy, "dy", shape, None, dev)
+    _want(mean, "mean", shape[:-1], torch.float32, dev)
+    _want(rstd, "rstd", shape[:-1], torch.float32, dev)
     w_dtype = _norm_weights(weight, None, D, dev)
-    desc = norm_desc(x.numel() // max(D, 1), D, x.dtype, dy.dtype, w_dtype, 0.0)
-    dx = torch.empty(x.shape, dtype=x.dtype, device=dev) if want_dx else None
-    dw = torch.empty(D, dtype=torch.float32, device=dev) if weight is not None else None
-    db = torch.empty(D, dtype=torch.float32, device=dev) if with_bias else None
-    need = int(lib().gdr_layernorm_bwd_workspace_bytes(desc, int(dw is not None), int(with_bias)))
-    if need and workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    _call(lib().gdr_layernorm_bwd, "gdr_layernorm_bwd", dev, stream, desc, _ptr(x), _ptr(dy), _ptr(weight), _ptr(mean),
-          _ptr(rstd), _ptr(dx), _ptr(dw), _ptr(db), _ptr(workspace), ws_bytes)
+    desc, need = _desc(_norm_bwd_plan, x.numel() // D if D else 0, D, x.dtype, dy.dtype, w_dtype,
+                       int(weight is not None), int(bool(with_bias)))
+    dx = torch.empty_like(x) if want_dx else None
+    dw = mean.new_empty((D,)) if weight is not None else None
+    db = mean.new_empty((D,)) if with_bias else None
+    ws_bytes = need
+    if workspace is not None:
+        ws_bytes = workspace.numel() * workspace.element_size()
+    elif need:
+        workspace = mean.new_empty((need // 4,))
+    _call(lib().gdr_layernorm_bwd, "gdr_layernorm_bwd", dev, stream, desc, x.data_ptr(), dy.data_ptr(), _at(weight),
+          mean.data_ptr(), rstd.data_ptr(), _at(dx), _at(dw), _at(db), _at(workspace), ws_bytes)
     return {"x": dx, "weight": dw, "bias": db}
 
 
@@ -669,7 +718,12 @@ def beam_desc(G, K, V, M, x_dtype, row=0, eos=0) -> BeamDesc:
 
 
 def beam_workspace_bytes(desc: BeamDesc) -> int:
-    return int(lib().gdr_beam_select_workspace_bytes(desc))
+    return int(lib().gdr_beam_select_workspace_bytes(ctypes.byref(desc)))
+
+
+def _beam_plan(*key):
+    desc = beam_desc(*key)
+    return desc, beam_workspace_bytes(desc)
 
 
 def beam_select(logits, scores, n_out=None, *, finished=None, eos=0, workspace=None, stream=None):
@@ -682,19 +736,20 @@ def beam_select(logits, scores, n_out=None, *, finished=None, eos=0, workspace=N
         raise ValueError("logits must be [G, K, V]")
     G, K, V = logits.shape
     M = K if n_out is None else int(n_out)
-    _check_shape(scores, "scores", (G, K), torch.float32, dev)
+    _want(scores, "scores", (G, K), torch.float32, dev)
     if finished is not None:
-        _check_shape(finished, "finished", (G, K), torch.bool, dev)
-    desc = beam_desc(G, K, V, M, logits.dtype, _row_stride(logits, "logits"), eos)
-    out = torch.empty((G, M), dtype=torch.float32, device=dev)
-    parent = torch.empty((G, M), dtype=torch.int32, device=dev)
-    token = torch.empty((G, M), dtype=torch.int32, device=dev)
-    need = beam_workspace_bytes(desc)
-    if need and workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    _call(lib().gdr_beam_select, "gdr_beam_select", dev, stream, desc, _ptr(logits), _ptr(scores), _ptr(finished),
-          _ptr(out), _ptr(parent), _ptr(token), _ptr(workspace), ws_bytes)
+        _want(finished, "finished", (G, K), torch.bool, dev)
+    desc, need = _desc(_beam_plan, G, K, V, M, logits.dtype, _row_stride(logits, "logits"), int(eos))
+    out = scores.new_empty((G, max(M, 0)))
+    parent = scores.new_empty((G, max(M, 0)), dtype=torch.int32)
+    token = torch.empty_like(parent)
+    ws_bytes = need
+    if workspace is not None:
+        ws_bytes = workspace.numel() * workspace.element_size()
+    elif need:
+        workspace = scores.new_empty((need // 4,))
+    _call(lib().gdr_beam_select, "gdr_beam_select", dev, stream, desc, logits.data_ptr(), scores.data_ptr(),
+          _at(finished), out.data_ptr(), parent.data_ptr(), token.data_ptr(), _at(workspace), ws_bytes)
     return out, parent, token
 
 
@@ -706,15 +761,16 @@ def state_reorder(S, parent, *, layers=False, stream=None):
     dev = _on_device(S, "S")
     _need(S, "S")
     _need(parent, "parent", torch.int32, dev)
-    if parent.dim() != 2 or S.dim() < 1 + int(bool(layers)):
+    at = 1 if layers else 0
+    if parent.dim() != 2 or S.dim() < 1 + at:
         raise ValueError("parent must be [G, K] and S [G * K, ...] (layers: [L, G * K, ...])")
     G, K = parent.shape
     L = S.shape[0] if layers else 1
-    if S.shape[int(bool(layers))] != G * K:
-        raise ValueError(f"S must hold G * K = {G * K} states, got {S.shape[int(bool(layers))]}")
+    if S.shape[at] != G * K:
+        raise ValueError(f"S must hold G * K = {G * K} states, got {S.shape[at]}")
     n = L * G * K
-    desc = ReorderDesc(L, G, K, S.numel() * S.element_size() // n if n else 0)
-    _call(lib().gdr_state_reorder, "gdr_state_reorder", dev, stream, desc, _ptr(S), _ptr(parent))
+    desc = _desc(ReorderDesc, L, G, K, S.numel() * S.element_size() // n if n else 0)
+    _call(lib().gdr_state_reorder, "gdr_state_reorder", dev, stream, desc, S.data_ptr(), parent.data_ptr())
     return S
 
 
