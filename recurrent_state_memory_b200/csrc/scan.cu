@@ -63,20 +63,55 @@ static gdr_status encode_rows(CUtensorMap* m, const void* base, const ScanParams
     return GDR_ERR_CUDA;
 }
 
+// The same tensor for rows that start anywhere (Phases in scan.cuh): P rows as one long row.
+template <typename T>
+static gdr_status encode_phases(CUtensorMap* m, const void* base, const ScanParams& p, long long row, int tok) {
+    EncodeTiledFn fn = nullptr;
+    const gdr_status s = encode_fn(&fn);
+    if (s != GDR_OK) return s;
+    constexpr int P = 16 / (int)sizeof(T);
+    const uintptr_t at = reinterpret_cast<uintptr_t>(base), lead = at % 16 / sizeof(T);
+    const cuuint64_t bytes = (cuuint64_t)P * row * sizeof(T), rows = (cuuint64_t)p.covered / P;
+    const cuuint64_t dims[4] = {(cuuint64_t)(lead + (P - 1) * row + p.D), 1u, rows, 1u};
+    const cuuint64_t strides[3] = {bytes, bytes, bytes * rows};
+    const cuuint32_t box[4] = {CH + P, 1u, (cuuint32_t)(tok / P), 1u}, estr[4] = {1u, 1u, 1u, 1u};
+    const CUresult r = fn(m, sizeof(T) == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4,
+                          reinterpret_cast<void*>(at - at % 16), dims, strides, box, estr,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+                          CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r == CUDA_SUCCESS) return GDR_OK;
+    snprintf(t_detail, sizeof(t_detail), "cuTensorMapEncodeTiled failed (%d)", (int)r);
+    return GDR_ERR_CUDA;
+}
+
+template <typename T, int V>
+static gdr_status encode(CUtensorMap* m, const void* base, const ScanParams& p, long long row, int tok) {
+    return V > 1 ? encode_rows<T>(m, base, p, row, tok) : encode_phases<T>(m, base, p, row, tok);
+}
+
 template <typename XT, typename GT, typename OT, int V>
-static gdr_status launch_v(Pass pass, const ScanParams& p, cudaStream_t st) {
+static gdr_status launch_v(Pass pass, ScanParams& p, cudaStream_t st) {
     if (pass == STEP) {
         const size_t blocks = ((size_t)p.B * (p.D / V) + NT - 1) / NT, cap = (size_t)device_sm_count() * 8;
         scan_step_kernel<XT, GT, OT, V><<<(unsigned)(blocks < cap ? blocks : cap), NT, 0, st>>>(p);
         const cudaError_t e = cudaGetLastError();
         return e == cudaSuccess ? GDR_OK : cuda_fail(e, "launch(scan step)");
     }
-    const int tok = pass == FWD ? Tile<V, FWD_ELEMS>::TOK : Tile<V, BWD_ELEMS>::TOK;
+    const int tok = pass == FWD ? Tile<V, fwd_elems<V>()>::TOK : Tile<V, BWD_ELEMS>::TOK;
     ScanMaps maps = {};
-    if (V > 1) {
-        gdr_status s = encode_rows<XT>(&maps.x, p.x, p, p.x_row, tok);
-        if (s == GDR_OK) s = encode_rows<GT>(&maps.g, p.g, p, p.g_row, tok);
-        if (s == GDR_OK && pass == BWD && p.dh) s = encode_rows<OT>(&maps.dh, p.dh, p, p.D, tok);
+    // V = 1: whole groups of 8 rows, where the copies' coordinates and sizes fit their types
+    const long long rows = (long long)p.B * p.T, wide = p.x_row > p.g_row ? p.x_row : p.g_row;
+    auto inside = [&](const void* q, long long row, size_t el) {    // a long row does not reach into the next one
+        const long long lead = (long long)(reinterpret_cast<uintptr_t>(q) % 16 / el);
+        return lead == 0 || lead + p.D <= row;
+    };
+    const bool fits = rows / 8 < (1LL << 31) - 1 && wide < (1LL << 27) && rows * wide < (1LL << 37) &&
+                      inside(p.x, p.x_row, sizeof(XT)) && inside(p.g, p.g_row, sizeof(GT));
+    p.covered = fits ? rows / 8 * 8 : 0;
+    if (V > 1 || p.covered > 0) {
+        gdr_status s = encode<XT, V>(&maps.x, p.x, p, p.x_row, tok);
+        if (s == GDR_OK) s = encode<GT, V>(&maps.g, p.g, p, p.g_row, tok);
+        if (s == GDR_OK && pass == BWD && p.dh) s = encode<OT, V>(&maps.dh, p.dh, p, p.D, tok);
         if (s != GDR_OK) return s;
     }
     if (pass == FWD)
@@ -87,7 +122,7 @@ static gdr_status launch_v(Pass pass, const ScanParams& p, cudaStream_t st) {
 // Four channels per thread (and tiles by TMA) where every row of every tensor starts on 16 bytes,
 // one channel per thread otherwise.  The step only needs four elements' alignment.
 template <typename XT, typename GT, typename OT>
-static gdr_status launch(Pass pass, const ScanParams& p, cudaStream_t st) {
+static gdr_status launch(Pass pass, ScanParams& p, cudaStream_t st) {
     auto fits = [&](const void* q, long long row, size_t el) {
         const size_t by = pass == STEP ? 4 * el : 16;
         return reinterpret_cast<uintptr_t>(q) % by == 0 && row * el % by == 0 &&
@@ -99,10 +134,10 @@ static gdr_status launch(Pass pass, const ScanParams& p, cudaStream_t st) {
 }
 
 template <typename XT, typename GT>
-static gdr_status launch_o(const gdr_scan_desc* d, Pass pass, const ScanParams& p, cudaStream_t st) {
+static gdr_status launch_o(const gdr_scan_desc* d, Pass pass, ScanParams& p, cudaStream_t st) {
     return d->out_dtype == GDR_BF16 ? launch<XT, GT, __nv_bfloat16>(pass, p, st) : launch<XT, GT, float>(pass, p, st);
 }
-static gdr_status dispatch(const gdr_scan_desc* d, Pass pass, const ScanParams& p, cudaStream_t st) {
+static gdr_status dispatch(const gdr_scan_desc* d, Pass pass, ScanParams& p, cudaStream_t st) {
     const bool xb = d->x_dtype == GDR_BF16, gb = d->g_dtype == GDR_BF16;
     if (xb && gb) return launch_o<__nv_bfloat16, __nv_bfloat16>(d, pass, p, st);
     if (xb) return launch_o<__nv_bfloat16, float>(d, pass, p, st);

@@ -47,6 +47,7 @@ struct ScanParams {
     void* dx;
     void* dg;
     float* dh0;
+    long long covered;                  // V = 1: rows (of B * T) that the tensor maps reach
 };
 
 constexpr int CKPT = GDR_SCAN_CKPT;
@@ -132,8 +133,8 @@ __device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity) {
     return true;
 }
 
-// How a block's threads lie over its tile.  V = 4: 8 lanes x 4 channels and 4 runs per warp, tiles
-// by TMA; V = 1 (rows that TMA does not take): 32 lanes x 1 channel, loads into registers.
+// How a block's threads lie over its tile.  V = 4: 8 lanes x 4 channels and 4 runs per warp; V = 1
+// (rows that start on no 16 bytes): 32 lanes x 1 channel.
 template <int V, int ELEMS> struct Tile {
     static constexpr int LC = 32 / V;           // lanes along the channels
     static constexpr int TL = 32 / LC;          // runs in a warp
@@ -144,6 +145,47 @@ template <int V, int ELEMS> struct Tile {
                                         c(((threadIdx.x & 31) % LC) * V) {}
     __device__ __forceinline__ int first_token() const { return (warp * TL + lane_t) * R; }
 };
+
+// Tiles whose rows start anywhere.  A tensor copy starts on 16 bytes, a row of odd length does not;
+// but every P-th row has the same offset from 16 bytes, P = 16 / sizeof(T).  So the map takes P rows
+// as one long row, and a tile comes in P copies, one for the tokens of each offset, each a few
+// elements wider than the channels and started at the 16 bytes before them: slot q holds the
+// tile's tokens q, q + P, .. .  The last B * T mod 8 rows, which no whole long row holds, are
+// read from global memory.
+template <typename T, int TOK> struct Phases {
+    static constexpr int P = 16 / (int)sizeof(T), W = CH + P, ROWS = TOK / P;
+    alignas(128) T v[P][ROWS][W];
+    static __device__ __forceinline__ int lead(const void* base) { return (int)(reinterpret_cast<uintptr_t>(base) % 16 / sizeof(T)); }
+    // Elements from the map's start to the first channel of the tile's token q (its row n0 + q).
+    static __device__ __forceinline__ long long start(const void* base, long long row, int c0, long long n0, int q) {
+        return lead(base) + (long long)((n0 + q) % P) * row + c0;
+    }
+    __device__ __forceinline__ void copy(int q, const void* base, long long row, int c0, long long n0,
+                                         const CUtensorMap* map, uint64_t* bar) {
+        const long long e = start(base, row, c0, n0, q);
+        tc::tma_load_4d(smem_addr(v[q]), map, (int)(e - e % P), 0, (int)((n0 + q) / P), 0, bar);
+    }
+};
+// R tokens of one lane's channel: tile tokens i0 .. (a multiple of P), row n0 of the tensor first.
+// skew[q]: where slot q's rows hold the lane's channel.
+template <typename T, int TOK, int R>
+__device__ __forceinline__ void read_run(const Phases<T, TOK>& ph, const int (&skew)[Phases<T, TOK>::P], int i0, float (&v)[R][1]) {
+    constexpr int P = Phases<T, TOK>::P;
+#pragma unroll
+    for (int r = 0; r < R; ++r) v[r][0] = ld_f32(&ph.v[r % P][(i0 + r) / P][skew[r % P]]);
+}
+template <typename T, int TOK>
+__device__ __forceinline__ void skews(const Phases<T, TOK>& ph, const void* base, long long row, int c0, long long n0,
+                                      int (&skew)[Phases<T, TOK>::P]) {
+#pragma unroll
+    for (int q = 0; q < Phases<T, TOK>::P; ++q)
+        skew[q] = (int)(Phases<T, TOK>::start(base, row, c0, n0, q) % Phases<T, TOK>::P) + (int)(threadIdx.x & 31);
+}
+template <typename T, int R>
+__device__ __forceinline__ void read_run_global(const T* src, long long row, int have, float (&v)[R][1]) {
+#pragma unroll
+    for (int r = 0; r < R; ++r) v[r][0] = r < have ? ld_f32(src + r * row) : 0.f;
+}
 
 // Compose a warp's runs: in (A, H) of this thread's run; out the composition of the runs before
 // it (ex_*) and, in the warp's last run's lanes, of all of them (A, H).  UP = false: from the end.
@@ -228,16 +270,20 @@ __device__ __forceinline__ void run_start(const float* start, const float (&exA)
     for (int i = 0; i < V; ++i) s[i] = fmaf(exA[i], start[i], exH[i]);
 }
 
-// The tensor maps of a call ({D, 1, T, B}, boxes of CH channels x TOK tokens).
+// A tile in shared memory.
+template <typename T, int TOK> struct Rows { alignas(128) T v[TOK][CH]; };
+template <typename T, int V, int TOK> using TileOf = std::conditional_t<(V > 1), Rows<T, TOK>, Phases<T, TOK>>;
+
+// The tensor maps of a call.
 struct ScanMaps { CUtensorMap x, g, dh; };
 
-constexpr int FWD_ELEMS = 32;           // elements of a thread: 2 registers each (decay, input)
-constexpr int BWD_ELEMS = 16;           // 5 registers each
+template <int V> constexpr int fwd_elems() { return V > 1 ? 32 : 16; }  // of a thread: 2 registers each
+constexpr int BWD_ELEMS = 16;                                           // 5 registers each
 
 template <typename XT, typename GT, int V> struct FwdSmem {
-    static constexpr int TOK = Tile<V, FWD_ELEMS>::TOK, N = V > 1 ? STAGES : 1;
-    alignas(128) GT g[N][V > 1 ? TOK : 1][CH];
-    alignas(128) XT x[N][V > 1 ? TOK : 1][CH];
+    static constexpr int TOK = Tile<V, fwd_elems<V>()>::TOK;
+    TileOf<GT, V, TOK> g[STAGES];
+    TileOf<XT, V, TOK> x[STAGES];
     float2 agg[WT][CH];
     float start[WT][CH];
     uint64_t bars[2 + STAGES];          // the exchange's, the stages'
@@ -245,8 +291,8 @@ template <typename XT, typename GT, int V> struct FwdSmem {
 };
 
 template <typename XT, typename GT, typename OT, int V>
-__global__ void __launch_bounds__(NT, 2) scan_fwd_kernel(ScanParams p, const __grid_constant__ ScanMaps maps) {
-    using L = Tile<V, FWD_ELEMS>;
+__global__ void __launch_bounds__(NT, V > 1 ? 2 : 3) scan_fwd_kernel(ScanParams p, const __grid_constant__ ScanMaps maps) {
+    using L = Tile<V, fwd_elems<V>()>;
     using S = FwdSmem<XT, GT, V>;
     constexpr int R = L::R;
     extern __shared__ __align__(128) unsigned char raw[];
@@ -265,37 +311,54 @@ __global__ void __launch_bounds__(NT, 2) scan_fwd_kernel(ScanParams p, const __g
 
     barriers_begin(sm.bars, 2 + STAGES, ncl);
     auto fetch = [&](int k) {                             // turn k's tile, unless it lies behind the sequence
-        const int t = k * turn + tile;
-        if (V == 1 || threadIdx.x != 0 || k >= turns || t >= len) return;
-        uint64_t* bar = &sm.bars[2 + k % STAGES];
-        expect_bytes(bar, sizeof(sm.g[0]) + sizeof(sm.x[0]));
-        tc::tma_load_4d(smem_addr(sm.g[k % STAGES]), &maps.g, c0, 0, t, b, bar);
-        tc::tma_load_4d(smem_addr(sm.x[k % STAGES]), &maps.x, c0, 0, t, b, bar);
+        const int t = k * turn + tile, st = k % STAGES;
+        if (l.warp != 0 || k >= turns || t >= len) return;
+        uint64_t* bar = &sm.bars[2 + st];
+        const int lane = threadIdx.x & 31;
+        if constexpr (V > 1) {
+            if (lane != 0) return;
+            expect_bytes(bar, sizeof(sm.g[0]) + sizeof(sm.x[0]));
+            tc::tma_load_4d(smem_addr(sm.g[st].v), &maps.g, c0, 0, t, b, bar);
+            tc::tma_load_4d(smem_addr(sm.x[st].v), &maps.x, c0, 0, t, b, bar);
+        } else if (p.covered > 0) {
+            if (lane == 0) expect_bytes(bar, sizeof(sm.g[0]) + sizeof(sm.x[0]));
+            __syncwarp();
+            const long long n0 = (long long)b * p.T + t;
+            if (lane < sm.g[0].P) sm.g[st].copy(lane, p.g, p.g_row, c0, n0, &maps.g, bar);
+            else if (lane >= 16 && lane - 16 < sm.x[0].P) sm.x[st].copy(lane - 16, p.x, p.x_row, c0, n0, &maps.x, bar);
+        }
     };
 #pragma unroll
     for (int k = 0; k < STAGES; ++k) fetch(k);
 
+    int skew_g[V > 1 ? 1 : TileOf<GT, 1, L::TOK>::P], skew_x[V > 1 ? 1 : TileOf<XT, 1, L::TOK>::P];
+    if constexpr (V == 1) {
+        const long long n0 = (long long)b * p.T;          // tiles start a multiple of P tokens later
+        skews(sm.g[0], p.g, p.g_row, c0, n0, skew_g);
+        skews(sm.x[0], p.x, p.x_row, c0, n0, skew_x);
+    }
     float carry = 0.f;                                    // of warp 0: the state at the turn's start
     if (threadIdx.x < CH && c0 + (int)threadIdx.x < p.D && p.h0) carry = p.h0[(size_t)b * p.D + c0 + threadIdx.x];
 
     for (int k = 0; k < turns; ++k) {
         const int t0 = k * turn + first;
         float a[R][V], bb[R][V], A[V], H[V], exA[V], exH[V];
-        if constexpr (V > 1) {
-            if (k * turn + tile < len) {
-                if (!lost) lost = !wait_phase(&sm.bars[2 + k % STAGES], (uint32_t)(k / STAGES) & 1u);
+        if (k * turn + tile < len) {
+            const int st = k % STAGES;
+            if ((V > 1 || p.covered > 0) && !lost) lost = !wait_phase(&sm.bars[2 + st], (uint32_t)(k / STAGES) & 1u);
+            if constexpr (V > 1) {
 #pragma unroll
                 for (int r = 0; r < R; ++r) {
-                    Pack<GT, V>::get(*reinterpret_cast<const typename Pack<GT, V>::Raw*>(&sm.g[k % STAGES][l.first_token() + r][l.c]), a[r]);
-                    Pack<XT, V>::get(*reinterpret_cast<const typename Pack<XT, V>::Raw*>(&sm.x[k % STAGES][l.first_token() + r][l.c]), bb[r]);
+                    const int t = l.first_token() + r;
+                    Pack<GT, V>::get(*reinterpret_cast<const typename Pack<GT, V>::Raw*>(&sm.g[st].v[t][l.c]), a[r]);
+                    Pack<XT, V>::get(*reinterpret_cast<const typename Pack<XT, V>::Raw*>(&sm.x[st].v[t][l.c]), bb[r]);
                 }
-            }
-        } else {
-#pragma unroll
-            for (int r = 0; r < R; ++r) {
-                const bool in = on && t0 + r < len;
-                a[r][0] = in ? ld_f32(g + (t0 + r) * p.g_row) : 0.f;
-                bb[r][0] = in ? ld_f32(x + (t0 + r) * p.x_row) : 0.f;
+            } else if ((long long)b * p.T + t0 + R <= p.covered) {
+                read_run(sm.g[st], skew_g, l.first_token(), a);
+                read_run(sm.x[st], skew_x, l.first_token(), bb);
+            } else {
+                read_run_global(g + t0 * p.g_row, p.g_row, on ? len - t0 : 0, a);
+                read_run_global(x + t0 * p.x_row, p.x_row, on ? len - t0 : 0, bb);
             }
         }
         with_mode(p, [&](auto mode, auto tied) {
@@ -375,10 +438,10 @@ __global__ void __launch_bounds__(NT, 2) scan_fwd_kernel(ScanParams p, const __g
 }
 
 template <typename XT, typename GT, typename OT, int V> struct BwdSmem {
-    static constexpr int TOK = Tile<V, BWD_ELEMS>::TOK, N = V > 1 ? STAGES : 1;
-    alignas(128) GT g[N][V > 1 ? TOK : 1][CH];
-    alignas(128) XT x[N][V > 1 ? TOK : 1][CH];
-    alignas(128) OT dh[N][V > 1 ? TOK : 1][CH];
+    static constexpr int TOK = Tile<V, BWD_ELEMS>::TOK;
+    TileOf<GT, V, TOK> g[STAGES];
+    TileOf<XT, V, TOK> x[STAGES];
+    TileOf<OT, V, TOK> dh[STAGES];
     float2 up[WT][CH];
     float2 down[WT][CH];
     float before[WT][CH];
@@ -418,17 +481,36 @@ __global__ void __launch_bounds__(NT, 2) scan_bwd_kernel(ScanParams p, const __g
     const int live = (len - tile + turn - 1) / turn;      // turns of this block with tokens (len > tile), else <= 0
     const int skip = turns - max(live, 0);
     auto fetch = [&](int k) {
-        if (V == 1 || threadIdx.x != 0 || k < skip || k >= turns) return;
-        const int t = (turns - 1 - k) * turn + tile, st = (k - skip) % STAGES;
+        if (l.warp != 0 || k < skip || k >= turns) return;
+        const int t = (turns - 1 - k) * turn + tile, st = (k - skip) % STAGES, lane = threadIdx.x & 31;
         uint64_t* bar = &sm.bars[2 + st];
-        expect_bytes(bar, sizeof(sm.g[0]) + sizeof(sm.x[0]) + (with_dh ? sizeof(sm.dh[0]) : 0));
-        tc::tma_load_4d(smem_addr(sm.g[st]), &maps.g, c0, 0, t, b, bar);
-        tc::tma_load_4d(smem_addr(sm.x[st]), &maps.x, c0, 0, t, b, bar);
-        if (with_dh) tc::tma_load_4d(smem_addr(sm.dh[st]), &maps.dh, c0, 0, t, b, bar);
+        const uint32_t bytes = sizeof(sm.g[0]) + sizeof(sm.x[0]) + (with_dh ? sizeof(sm.dh[0]) : 0);
+        if constexpr (V > 1) {
+            if (lane != 0) return;
+            expect_bytes(bar, bytes);
+            tc::tma_load_4d(smem_addr(sm.g[st].v), &maps.g, c0, 0, t, b, bar);
+            tc::tma_load_4d(smem_addr(sm.x[st].v), &maps.x, c0, 0, t, b, bar);
+            if (with_dh) tc::tma_load_4d(smem_addr(sm.dh[st].v), &maps.dh, c0, 0, t, b, bar);
+        } else if (p.covered > 0) {
+            if (lane == 0) expect_bytes(bar, bytes);
+            __syncwarp();
+            const long long n0 = (long long)b * p.T + t;
+            if (lane < sm.g[0].P) sm.g[st].copy(lane, p.g, p.g_row, c0, n0, &maps.g, bar);
+            else if (lane >= 8 && lane - 8 < sm.x[0].P) sm.x[st].copy(lane - 8, p.x, p.x_row, c0, n0, &maps.x, bar);
+            else if (with_dh && lane >= 16 && lane - 16 < sm.dh[0].P) sm.dh[st].copy(lane - 16, p.dh, p.D, c0, n0, &maps.dh, bar);
+        }
     };
 #pragma unroll
     for (int k = 0; k < STAGES; ++k) fetch(skip + k);
 
+    int skew_g[V > 1 ? 1 : TileOf<GT, 1, L::TOK>::P], skew_x[V > 1 ? 1 : TileOf<XT, 1, L::TOK>::P],
+        skew_d[V > 1 ? 1 : TileOf<OT, 1, L::TOK>::P];
+    if constexpr (V == 1) {
+        const long long n0 = (long long)b * p.T;
+        skews(sm.g[0], p.g, p.g_row, c0, n0, skew_g);
+        skews(sm.x[0], p.x, p.x_row, c0, n0, skew_x);
+        skews(sm.dh[0], p.dh, p.D, c0, n0, skew_d);
+    }
     float carry = 0.f;                                    // of warp 0: a_{t+1} lam_{t+1} behind the turn
     if (threadIdx.x < CH && c0 + (int)threadIdx.x < p.D && p.dh_T) carry = p.dh_T[(size_t)b * p.D + c0 + threadIdx.x];
 
@@ -441,29 +523,30 @@ __global__ void __launch_bounds__(NT, 2) scan_bwd_kernel(ScanParams p, const __g
             if (j < nck && ch < p.D) state = p.ckpt[((size_t)b * nck + j) * p.D + ch];
         }
         float a[R][V], rest[R][V], xv[R][V], d[R][V];
-        if constexpr (V > 1) {
-            if (k >= skip) {
-                const int st = (k - skip) % STAGES;
-                if (!lost) lost = !wait_phase(&sm.bars[2 + st], (uint32_t)((k - skip) / STAGES) & 1u);
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+            for (int i = 0; i < V; ++i) d[r][i] = 0.f;
+        if (k >= skip) {
+            const int st = (k - skip) % STAGES;
+            if ((V > 1 || p.covered > 0) && !lost) lost = !wait_phase(&sm.bars[2 + st], (uint32_t)((k - skip) / STAGES) & 1u);
+            if constexpr (V > 1) {
 #pragma unroll
                 for (int r = 0; r < R; ++r) {
                     const int t = l.first_token() + r;
-                    Pack<GT, V>::get(*reinterpret_cast<const typename Pack<GT, V>::Raw*>(&sm.g[st][t][l.c]), a[r]);
-                    Pack<XT, V>::get(*reinterpret_cast<const typename Pack<XT, V>::Raw*>(&sm.x[st][t][l.c]), xv[r]);
-                    if (with_dh) Pack<OT, V>::get(*reinterpret_cast<const typename Pack<OT, V>::Raw*>(&sm.dh[st][t][l.c]), d[r]);
-                    else {
-#pragma unroll
-                        for (int i = 0; i < V; ++i) d[r][i] = 0.f;
-                    }
+                    Pack<GT, V>::get(*reinterpret_cast<const typename Pack<GT, V>::Raw*>(&sm.g[st].v[t][l.c]), a[r]);
+                    Pack<XT, V>::get(*reinterpret_cast<const typename Pack<XT, V>::Raw*>(&sm.x[st].v[t][l.c]), xv[r]);
+                    if (with_dh) Pack<OT, V>::get(*reinterpret_cast<const typename Pack<OT, V>::Raw*>(&sm.dh[st].v[t][l.c]), d[r]);
                 }
-            }
-        } else {
-#pragma unroll
-            for (int r = 0; r < R; ++r) {
-                const bool in = on && t0 + r < len;
-                a[r][0] = in ? ld_f32(g + (t0 + r) * p.g_row) : 0.f;
-                xv[r][0] = in ? ld_f32(x + (t0 + r) * p.x_row) : 0.f;
-                d[r][0] = in && with_dh ? ld_f32(dh + (size_t)(t0 + r) * p.D) : 0.f;
+            } else if ((long long)b * p.T + t0 + R <= p.covered) {
+                read_run(sm.g[st], skew_g, l.first_token(), a);
+                read_run(sm.x[st], skew_x, l.first_token(), xv);
+                if (with_dh) read_run(sm.dh[st], skew_d, l.first_token(), d);
+            } else {
+                const int have = on ? len - t0 : 0;
+                read_run_global(g + t0 * p.g_row, p.g_row, have, a);
+                read_run_global(x + t0 * p.x_row, p.x_row, have, xv);
+                if (with_dh) read_run_global(dh + (size_t)t0 * p.D, p.D, have, d);
             }
         }
         float A[V], H[V], M[V], dA[V], exA[V], exH[V], exD[V], exM[V];
