@@ -1,10 +1,12 @@
-"""Build libgdr.so (the CUDA library) in-tree for sm_100a with nvcc.
+"""Build libgdr.so (the CUDA library) in-tree for sm_100a with nvcc, and _binding.so (the host side of
+some of its Python calls) with g++.
 
     python -m recurrent_state_memory_b200.build [--force]
 """
 import os
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -15,12 +17,15 @@ LIB = os.path.join(PKG, "libgdr.so")
 LIB_DEBUG = os.path.join(PKG, "libgdr_debug.so")    # every kernel's computed indices checked
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 
+BINDING = os.path.join(PKG, "_binding.so")
+CXX = os.environ.get("CXX", "g++")
+
 SOURCES = ["gdr.cu", "scan.cu", "norm.cu", "beam.cu"]
 OBJ = os.path.join(PKG, "_build")                   # object files, one folder per build kind
 
 
 def _deps():
-    files = [os.path.join(CSRC, f) for f in os.listdir(CSRC)]
+    files = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if not f.endswith(".cpp")]
     files.append(os.path.join(INCLUDE, "gdr.h"))
     files.append(os.path.abspath(__file__))
     return files
@@ -35,11 +40,35 @@ def _fresh(out, dep):
     return all(os.path.exists(f) and os.path.getmtime(f) <= made for f in files + [os.path.abspath(__file__)])
 
 
+def build_binding(force: bool = False) -> str:
+    """Build _binding.so (csrc/binding.cpp) against the installed torch."""
+    src = os.path.join(CSRC, "binding.cpp")
+    made_from = [src, os.path.join(INCLUDE, "gdr.h"), os.path.abspath(__file__)]
+    if not force and os.path.exists(BINDING) and os.path.getmtime(BINDING) >= max(map(os.path.getmtime, made_from)):
+        return BINDING
+    import torch
+    from torch.utils import cpp_extension
+    paths = cpp_extension.include_paths() + [sysconfig.get_paths()["include"], os.path.join(os.path.dirname(
+        os.path.dirname(NVCC)), "include")]
+    libs = os.path.join(os.path.dirname(torch.__file__), "lib")
+    tmp = BINDING + ".tmp"
+    cmd = [CXX, "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-I", INCLUDE]
+    for p in paths:
+        cmd += ["-isystem", p]
+    cmd += [f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", src, "-o", tmp, "-L", libs,
+            "-ltorch", "-ltorch_cpu", "-ltorch_python", "-lc10", "-lc10_cuda", "-ldl"]
+    subprocess.run(cmd, check=True)
+    os.replace(tmp, BINDING)
+    return BINDING
+
+
 def build(force: bool = False, verbose: bool = False, debug: bool = False) -> str:
-    """Build libgdr.so, or with debug=True libgdr_debug.so (-DGDR_BOUNDS_CHECK: every kernel
+    """Build libgdr.so (and _binding.so), or with debug=True libgdr_debug.so (-DGDR_BOUNDS_CHECK: every kernel
     tests the indices of the global-memory accesses it computes and reports a failure through
     the status word instead of making the access)."""
     lib = LIB_DEBUG if debug else LIB
+    if not debug:
+        build_binding(force)
     if not force and os.path.exists(lib):
         newest = max(os.path.getmtime(f) for f in _deps())
         if os.path.getmtime(lib) >= newest:

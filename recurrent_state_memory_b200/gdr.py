@@ -18,6 +18,7 @@ import torch
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libgdr.so")
+BINDING_PATH = os.path.join(_HERE, "_binding.so")
 HEADER_PATH = os.path.join(os.path.dirname(_HERE), "include", "gdr.h")
 
 (GDR_OK, GDR_ERR_INVALID_ARG, GDR_ERR_UNSUPPORTED, GDR_ERR_CUDA, GDR_ERR_TIMEOUT, GDR_ERR_WORKSPACE,
@@ -229,7 +230,6 @@ def use_library(path: str) -> None:
     global LIB_PATH, _lib
     LIB_PATH = path
     _lib = None
-    _descs.clear()
 
 
 def debug_bounds_site() -> int:
@@ -494,81 +494,25 @@ def decode_step(q, k, v, g, beta, S, theta=None, *, gate_mode=GATE_NEG_SOFTPLUS,
 
 # ------------------------------------------------ scan, layer norm, beam search ----
 #
-# These calls are short (a serving token's kernel takes a few microseconds), so the binding spends
-# little on the host: outputs by empty_like / new_empty, descriptors kept by their sizes, the raw
-# stream handle.
+# Checks, outputs and the C call of these are in csrc/binding.cpp: at serving sizes their kernels take
+# a few microseconds, less than the same steps in Python.  Tensors are CUDA tensors on one device,
+# the call is asynchronous on `stream` (default: that device's current stream).
 
-_raw_stream = torch._C._cuda_getCurrentRawStream
-_current_device = torch._C._cuda_getDevice
-_descs = {}
+_binding = None
 
 
-def _desc(make, *key):
-    """The descriptor make(*key), and what make wants to keep beside it, made once per sizes and types."""
-    k = (make, key)
-    d = _descs.get(k)
-    if d is None:
-        if len(_descs) >= 4096:         # sizes that change from call to call
-            _descs.clear()
-        d = _descs[k] = make(*key)
-    return d
-
-
-def _on_device(t: torch.Tensor, name: str):
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    return t.device
-
-
-def _want(t, name, shape, dtype, dev):
-    """t has this shape, type and device and is contiguous (dtype None: any the library takes)."""
-    if t.shape == shape and t.device == dev and t.is_contiguous() and (t.dtype is dtype or dtype is None):
-        return
-    _need(t, name, dtype, dev)
-    raise ValueError(f"{name} must have the shape {tuple(shape)}, got {tuple(t.shape)}")
-
-
-def _row_stride(t: torch.Tensor, name: str) -> int:
-    """Elements between the rows of t (dense: 0), whose rows are dense and evenly spaced (a slice
-    along the last dimension of a wider contiguous tensor is)."""
-    if t.is_contiguous():
-        return 0
-    st, sh = t.stride(), t.shape
-    row = st[-2]
-    ok = st[-1] == 1 and row >= sh[-1]
-    for d in range(t.dim() - 3, -1, -1):
-        ok = ok and (sh[d] == 1 or st[d] == st[d + 1] * sh[d + 1])
-    if not ok:
-        raise ValueError(f"{name} must be contiguous, or a slice of a contiguous tensor along its last dimension")
-    return row
-
-
-def _call(fn, where, dev, stream, *args):
-    """One library call on `stream` (default: dev's current stream) with dev current."""
-    i = dev.index
-    s = _raw_stream(i) if stream is None else stream.cuda_stream
-    if _current_device() == i:
-        st = fn(*args, s)
-    else:
-        with torch.cuda.device(i):
-            st = fn(*args, s)
-    if st:
-        _check(st, where)
-
-
-def _at(t):
-    return None if t is None else t.data_ptr()
-
-
-def _scan_args(x, g, dims, lengths=None):
-    dev = _on_device(x, "x")
-    if x.dim() != dims or g.shape != x.shape:
-        raise ValueError("x and g must have the same shape, " + ("[B, T, D]" if dims == 3 else "[N, D]"))
-    if g.device != dev:
-        raise ValueError(f"g is on {g.device}, expected {dev}")
-    if lengths is not None:
-        _want(lengths, "lengths", (x.shape[0],), torch.int32, dev)
-    return dev
+def _ops():
+    """The native binding, calling the library that lib() has loaded."""
+    global _binding
+    if _lib is None or _binding is None:
+        lib()
+        if not os.path.exists(BINDING_PATH):
+            raise RuntimeError(f"{BINDING_PATH} is missing: build it with "
+                               "`python -m recurrent_state_memory_b200.build`")
+        from . import _binding as module
+        module.load(LIB_PATH)
+        _binding = module
+    return _binding
 
 
 def scan_desc(B, T, D, x_dtype, g_dtype, out_dtype, gate_mode=GATE_NEG_SOFTPLUS, tied=False, x_row=0,
@@ -585,23 +529,8 @@ def scan_fwd(x, g, h0=None, *, gate_mode=GATE_NEG_SOFTPLUS, tied=False, lengths=
     they are), a from the gate g by gate_mode, w = 1 or, tied, 1 - a; h0 [B,D] fp32 or None (zero);
     lengths [B] int32 or None: tokens of each sequence (h is zero behind them).  Returns
     (h [B,T,D], h_T [B,D] fp32), or (h, h_T, ckpt) with want_ckpt: the states that ``scan_bwd``
-    starts from.  h_T is None unless want_state.  Asynchronous on `stream` (default: current)."""
-    dev = _scan_args(x, g, 3, lengths)
-    B, T, D = x.shape
-    out_dtype = out_dtype or x.dtype
-    if h0 is not None:
-        _want(h0, "h0", (B, D), torch.float32, dev)
-    desc = _desc(scan_desc, B, T, D, x.dtype, g.dtype, out_dtype, gate_mode, tied, _row_stride(x, "x"),
-                 _row_stride(g, "g"))
-    h = x.new_empty((B, T, D), dtype=out_dtype)
-    h_T = ckpt = None
-    if want_state:
-        h_T = x.new_empty((B, D), dtype=torch.float32) if h0 is None else torch.empty_like(h0)
-    if want_ckpt:
-        ckpt = x.new_empty((B, -(-T // SCAN_CKPT), D), dtype=torch.float32)
-    _call(lib().gdr_scan_fwd, "gdr_scan_fwd", dev, stream, desc, x.data_ptr(), g.data_ptr(), _at(h0), _at(lengths),
-          h.data_ptr(), _at(h_T), _at(ckpt))
-    return (h, h_T, ckpt) if want_ckpt else (h, h_T)
+    starts from.  h_T is None unless want_state."""
+    return _ops().scan_fwd(x, g, h0, gate_mode, tied, lengths, out_dtype, want_state, want_ckpt, stream)
 
 
 def scan_bwd(x, g, ckpt, dh=None, dh_T=None, *, gate_mode=GATE_NEG_SOFTPLUS, tied=False, lengths=None,
@@ -609,108 +538,31 @@ def scan_bwd(x, g, ckpt, dh=None, dh_T=None, *, gate_mode=GATE_NEG_SOFTPLUS, tie
     """Backward of ``scan_fwd``: the gradients of x, g and h0 given ckpt (from the forward of the same
     inputs), dh [B,T,D] (like h) and dh_T [B,D] fp32; either may be None (zero).  Returns a dict
     "x" (x's dtype), "g" (g's dtype), "h0" (fp32; None unless want_dh0)."""
-    dev = _scan_args(x, g, 3, lengths)
-    B, T, D = x.shape
-    _want(ckpt, "ckpt", (B, -(-T // SCAN_CKPT), D), torch.float32, dev)
-    if dh is not None:
-        _want(dh, "dh", (B, T, D), None, dev)
-    if dh_T is not None:
-        _want(dh_T, "dh_T", (B, D), torch.float32, dev)
-    x_row, g_row = _row_stride(x, "x"), _row_stride(g, "g")
-    desc = _desc(scan_desc, B, T, D, x.dtype, g.dtype, x.dtype if dh is None else dh.dtype, gate_mode, tied, x_row, g_row)
-    dx = x.new_empty((B, T, D)) if x_row else torch.empty_like(x)
-    dg = g.new_empty((B, T, D)) if g_row else torch.empty_like(g)
-    dh0 = None
-    if want_dh0:
-        dh0 = x.new_empty((B, D), dtype=torch.float32) if dh_T is None else torch.empty_like(dh_T)
-    _call(lib().gdr_scan_bwd, "gdr_scan_bwd", dev, stream, desc, x.data_ptr(), g.data_ptr(), ckpt.data_ptr(),
-          _at(lengths), _at(dh), _at(dh_T), dx.data_ptr(), dg.data_ptr(), _at(dh0))
-    return {"x": dx, "g": dg, "h0": dh0}
+    return _ops().scan_bwd(x, g, ckpt, dh, dh_T, gate_mode, tied, lengths, want_dh0, stream)
 
 
 def scan_step(x, g, h, *, gate_mode=GATE_NEG_SOFTPLUS, tied=False, out_dtype=None, o=None, stream=None):
     """One token of ``scan_fwd`` for N sequences: x, g [N,D]; h [N,D] fp32 is updated in place.
     Returns o [N,D], the new state in out_dtype (default: x's)."""
-    dev = _scan_args(x, g, 2)
-    N, D = x.shape
-    out_dtype = out_dtype or x.dtype
-    _want(h, "h", (N, D), torch.float32, dev)
-    if o is None:
-        o = x.new_empty((N, D), dtype=out_dtype)
-    else:
-        _want(o, "o", (N, D), out_dtype, dev)
-    desc = _desc(scan_desc, N, 1, D, x.dtype, g.dtype, out_dtype, gate_mode, tied, _row_stride(x, "x"),
-                 _row_stride(g, "g"))
-    _call(lib().gdr_scan_step, "gdr_scan_step", dev, stream, desc, x.data_ptr(), g.data_ptr(), h.data_ptr(),
-          o.data_ptr())
-    return o
+    return _ops().scan_step(x, g, h, gate_mode, tied, out_dtype, o, stream)
 
 
 def norm_desc(rows, D, x_dtype, y_dtype, w_dtype=torch.float32, eps=1e-5) -> NormDesc:
     return NormDesc(rows, D, _dtype_code(x_dtype), _dtype_code(y_dtype), _dtype_code(w_dtype), float(eps))
 
 
-def _norm_weights(weight, bias, D, dev):
-    w_dtype = torch.float32 if weight is None and bias is None else (bias if weight is None else weight).dtype
-    if weight is not None:
-        _want(weight, "weight", (D,), w_dtype, dev)
-    if bias is not None:
-        _want(bias, "bias", (D,), w_dtype, dev)
-    return w_dtype
-
-
 def layernorm_fwd(x, weight=None, bias=None, *, eps=1e-5, out_dtype=None, want_stats=True, stream=None):
     """Layer norm over the last dimension (``gdr_layernorm_fwd``): x [..., D] bf16 or fp32, weight and
     bias [D] (one dtype) or None.  Returns (y [..., D] out_dtype, mean [...], rstd [...] fp32); the
     statistics are None unless want_stats."""
-    dev = _on_device(x, "x")
-    if x.dim() < 1:
-        raise ValueError("x must have at least one dimension")
-    _need(x, "x")
-    shape = x.shape
-    D = shape[-1]
-    w_dtype = _norm_weights(weight, bias, D, dev)
-    y = torch.empty_like(x, dtype=out_dtype) if out_dtype is not None and out_dtype is not x.dtype else torch.empty_like(x)
-    desc = _desc(norm_desc, x.numel() // D if D else 0, D, x.dtype, y.dtype, w_dtype, eps)
-    mean = rstd = None
-    if want_stats:
-        mean = x.new_empty(shape[:-1], dtype=torch.float32)
-        rstd = torch.empty_like(mean)
-    _call(lib().gdr_layernorm_fwd, "gdr_layernorm_fwd", dev, stream, desc, x.data_ptr(), _at(weight), _at(bias),
-          y.data_ptr(), _at(mean), _at(rstd))
-    return y, mean, rstd
-
-
-def _norm_bwd_plan(rows, D, x_dtype, y_dtype, w_dtype, with_w, with_b):
-    desc = norm_desc(rows, D, x_dtype, y_dtype, w_dtype, 0.0)
-    return desc, int(lib().gdr_layernorm_bwd_workspace_bytes(desc, with_w, with_b))
+    return _ops().layernorm_fwd(x, weight, bias, eps, out_dtype, want_stats, stream)
 
 
 def layernorm_bwd(x, dy, mean, rstd, weight=None, *, with_bias=True, want_dx=True, workspace=None, stream=None):
     """Backward of ``layernorm_fwd`` given dy (like y) and the forward's mean and rstd.  Returns a dict
     "x" (x's dtype; None unless want_dx), "weight" (fp32; None without weight) and "bias" (fp32; None
     unless with_bias)."""
-    dev = _on_device(x, "x")
-    _need(x, "x")
-    shape = x.shape
-    D = shape[-1]
-    _want(dy, "dy", shape, None, dev)
-    _want(mean, "mean", shape[:-1], torch.float32, dev)
-    _want(rstd, "rstd", shape[:-1], torch.float32, dev)
-    w_dtype = _norm_weights(weight, None, D, dev)
-    desc, need = _desc(_norm_bwd_plan, x.numel() // D if D else 0, D, x.dtype, dy.dtype, w_dtype,
-                       int(weight is not None), int(bool(with_bias)))
-    dx = torch.empty_like(x) if want_dx else None
-    dw = mean.new_empty((D,)) if weight is not None else None
-    db = mean.new_empty((D,)) if with_bias else None
-    ws_bytes = need
-    if workspace is not None:
-        ws_bytes = workspace.numel() * workspace.element_size()
-    elif need:
-        workspace = mean.new_empty((need // 4,))
-    _call(lib().gdr_layernorm_bwd, "gdr_layernorm_bwd", dev, stream, desc, x.data_ptr(), dy.data_ptr(), _at(weight),
-          mean.data_ptr(), rstd.data_ptr(), _at(dx), _at(dw), _at(db), _at(workspace), ws_bytes)
-    return {"x": dx, "weight": dw, "bias": db}
+    return _ops().layernorm_bwd(x, dy, mean, rstd, weight, with_bias, want_dx, workspace, stream)
 
 
 def beam_desc(G, K, V, M, x_dtype, row=0, eos=0) -> BeamDesc:
@@ -721,36 +573,12 @@ def beam_workspace_bytes(desc: BeamDesc) -> int:
     return int(lib().gdr_beam_select_workspace_bytes(ctypes.byref(desc)))
 
 
-def _beam_plan(*key):
-    desc = beam_desc(*key)
-    return desc, beam_workspace_bytes(desc)
-
-
 def beam_select(logits, scores, n_out=None, *, finished=None, eos=0, workspace=None, stream=None):
     """The n_out (default K) best of every group's K * V continuations (``gdr_beam_select``): logits
     [G,K,V] bf16 or fp32 (rows may be slices of wider ones), scores [G,K] fp32 summed log
     probabilities, finished [G,K] bool or None.  Returns (scores fp32, parent int32, token int32),
     each [G, n_out], best first; parent is the beam within its group, as ``state_reorder`` takes it."""
-    dev = _on_device(logits, "logits")
-    if logits.dim() != 3:
-        raise ValueError("logits must be [G, K, V]")
-    G, K, V = logits.shape
-    M = K if n_out is None else int(n_out)
-    _want(scores, "scores", (G, K), torch.float32, dev)
-    if finished is not None:
-        _want(finished, "finished", (G, K), torch.bool, dev)
-    desc, need = _desc(_beam_plan, G, K, V, M, logits.dtype, _row_stride(logits, "logits"), int(eos))
-    out = scores.new_empty((G, max(M, 0)))
-    parent = scores.new_empty((G, max(M, 0)), dtype=torch.int32)
-    token = torch.empty_like(parent)
-    ws_bytes = need
-    if workspace is not None:
-        ws_bytes = workspace.numel() * workspace.element_size()
-    elif need:
-        workspace = scores.new_empty((need // 4,))
-    _call(lib().gdr_beam_select, "gdr_beam_select", dev, stream, desc, logits.data_ptr(), scores.data_ptr(),
-          _at(finished), out.data_ptr(), parent.data_ptr(), token.data_ptr(), _at(workspace), ws_bytes)
-    return out, parent, token
+    return _ops().beam_select(logits, scores, n_out, finished, eos, workspace, stream)
 
 
 def state_reorder(S, parent, *, layers=False, stream=None):
@@ -758,20 +586,7 @@ def state_reorder(S, parent, *, layers=False, stream=None):
     [G * K, ...] (decode_step's states, scan_step's, Raven's slots), or [L, G * K, ...] with layers;
     parent [G,K] int32.  Returns S.  A parent outside 0 .. K - 1 keeps its beam's state and shows as
     GDR_ERR_INDEX in query_device_status."""
-    dev = _on_device(S, "S")
-    _need(S, "S")
-    _need(parent, "parent", torch.int32, dev)
-    at = 1 if layers else 0
-    if parent.dim() != 2 or S.dim() < 1 + at:
-        raise ValueError("parent must be [G, K] and S [G * K, ...] (layers: [L, G * K, ...])")
-    G, K = parent.shape
-    L = S.shape[0] if layers else 1
-    if S.shape[at] != G * K:
-        raise ValueError(f"S must hold G * K = {G * K} states, got {S.shape[at]}")
-    n = L * G * K
-    desc = _desc(ReorderDesc, L, G, K, S.numel() * S.element_size() // n if n else 0)
-    _call(lib().gdr_state_reorder, "gdr_state_reorder", dev, stream, desc, S.data_ptr(), parent.data_ptr())
-    return S
+    return _ops().state_reorder(S, parent, layers, stream)
 
 
 def query_device_status(stream=None) -> int:

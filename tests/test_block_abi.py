@@ -140,10 +140,10 @@ def test_binding_refuses_what_is_not_on_the_gpu(G):
 
 
 def test_binding_takes_row_slices_only(G):
-    wide = torch.zeros(2, 5, 12)
-    assert G._row_stride(wide, "x") == 0
-    assert G._row_stride(wide[..., 4:8], "x") == 12
-    assert G._row_stride(wide[:1, :, :8], "x") == 12
+    wide, row_stride = torch.zeros(2, 5, 12), G._ops().row_stride
+    assert row_stride(wide, "x") == 0
+    assert row_stride(wide[..., 4:8], "x") == 12
+    assert row_stride(wide[:1, :, :8], "x") == 12
     for bad in (wide[:, ::2], wide[:, :4, :8], wide[..., ::2], wide.transpose(1, 2), wide[0].expand(2, 5, 12)):
         with pytest.raises(ValueError, match="contiguous"):
-            G._row_stride(bad, "x")
+            row_stride(bad, "x")
