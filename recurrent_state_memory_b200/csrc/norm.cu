@@ -14,10 +14,10 @@ namespace lnm {
 // of G threads); N = 0: the row is too long for a block's registers.
 struct Plan { int V, N, G; };
 
-// A warp while a lane holds at most 16 elements (backward: 8, since it also holds dy and two sums),
-// then the smallest block whose threads hold the row in as many; one-element loads 32 and 16.
+// A warp while a lane holds at most 16 elements (one by one, and in the backward, which also holds
+// dy, the weights and two sums: 8), then the smallest block whose threads hold the row in as many.
 // (Forward of 33.5 M bf16 elements: rows of 1024 in 32 elements a lane of a warp 32.3 us, in 8 of 128
-// threads 28.6; rows of 4096 in 32 of 128 threads 34.0.)
+// threads 28.6; rows of 4096 in 32 of 128 threads 34.0, in 16 of 256 32.0.)
 static Plan plan_of(int D, int V, bool bwd) {
     Plan q{V, 0, 32};
     const int nv = (D + V - 1) / V;             // loads of a row
@@ -26,14 +26,13 @@ static Plan plan_of(int D, int V, bool bwd) {
         for (q.G = 1; q.G < nv; q.G *= 2) {}
         return q;
     }
-    const int most = V == 1 ? (bwd ? 16 : 32) : (bwd ? 8 : 16) / V;
-    for (int n = 2; n <= (V == 1 ? 16 : most); n *= 2)
+    const int most = (bwd || V == 1 ? 8 : 16) / V;
+    for (int n = 2; n <= most; n *= 2)
         if (nv <= 32 * n) { q.N = n; return q; }
-    for (int g : {128, 256, 512, 1024}) {
-        if (g == 1024 && V == 1) break;
-        for (int n = V == 1 ? 8 : bwd ? most : 1; n <= most; n *= 2)
+    for (int g : {128, 256, 512, 1024})
+        for (int n = V == 1 ? 4 : bwd ? most : 1; n <= most; n *= 2)
             if (nv <= g * n) { q.G = g; q.N = n; return q; }
-    }
+    if (!bwd && V == 1 && nv <= 16 * 1024) { q.G = 1024; q.N = 16; }
     return q;
 }
 static int rows_of_block(const Plan& q) { return q.N && q.G <= 32 ? WARP_NT / q.G : 1; }
@@ -69,16 +68,16 @@ static gdr_status launch_plan(const Plan& q, const NormParams& p, cudaStream_t s
         } else if constexpr (V == 4) {
             GDR_NORM(4, 32); GDR_NORM(2, 128); GDR_NORM(4, 128); GDR_NORM(4, 256); GDR_NORM(4, 512); GDR_NORM(4, 1024);
         } else {
-            GDR_NORM(4, 32); GDR_NORM(8, 32); GDR_NORM(16, 32);
-            GDR_NORM(8, 128); GDR_NORM(16, 128); GDR_NORM(32, 128); GDR_NORM(32, 256); GDR_NORM(32, 512);
+            GDR_NORM(4, 32); GDR_NORM(8, 32);
+            GDR_NORM(4, 128); GDR_NORM(8, 128); GDR_NORM(8, 256); GDR_NORM(8, 512); GDR_NORM(8, 1024); GDR_NORM(16, 1024);
         }
     } else if constexpr (V == 8) {
         GDR_NORM(1, 128); GDR_NORM(1, 256); GDR_NORM(1, 512); GDR_NORM(1, 1024);
     } else if constexpr (V == 4) {
         GDR_NORM(2, 32); GDR_NORM(2, 128); GDR_NORM(2, 256); GDR_NORM(2, 512); GDR_NORM(2, 1024);
     } else {
-        GDR_NORM(2, 32); GDR_NORM(4, 32); GDR_NORM(8, 32); GDR_NORM(16, 32);
-        GDR_NORM(8, 128); GDR_NORM(16, 128); GDR_NORM(16, 256); GDR_NORM(16, 512);
+        GDR_NORM(2, 32); GDR_NORM(4, 32); GDR_NORM(8, 32);
+        GDR_NORM(4, 128); GDR_NORM(8, 128); GDR_NORM(8, 256); GDR_NORM(8, 512); GDR_NORM(8, 1024);
     }
 #undef GDR_NORM
     return fail(GDR_ERR_UNSUPPORTED, "layer norm: no kernel for this plan%s");

@@ -143,16 +143,16 @@ template <typename T, int V> struct Raw {
         return x;
     }
 };
-// V weights or biases from column c on, of either type.
-template <int V> __device__ __forceinline__ Vals<V> load_w(const void* p, int bf16, int c) {
-    if (bf16) {
-        Raw<__nv_bfloat16, V> r;
-        r.load(static_cast<const __nv_bfloat16*>(p) + c);
-        return r.vals();
-    }
-    Raw<float, V> r;
-    r.load(static_cast<const float*>(p) + c);
+// V weights or biases from column c on.
+template <typename WT, int V> __device__ __forceinline__ Vals<V> load_w(const void* p, int c) {
+    Raw<WT, V> r;
+    r.load(static_cast<const WT*>(p) + c);
     return r.vals();
+}
+// f(a value of the weights' type): the branch is taken once, not once a load.
+template <typename F> __device__ __forceinline__ void with_weights(const NormParams& p, F f) {
+    if (p.w_bf16) f(__nv_bfloat16());
+    else f(0.f);
 }
 template <typename T, int V> __device__ __forceinline__ void store_v(T* p, const Vals<V>& v) {
     if constexpr (V == 1) {
@@ -242,7 +242,7 @@ template <int G, int U> struct Place {
 
 // Rows that a group takes per turn: two while a row is few registers, so that more loads are in
 // flight and, in a block, two rows share a barrier.
-template <int V, int N, int G> constexpr int rows_at_once() { return V * N <= 8 && G < 1024 ? 2 : 1; }
+template <int V, int N, int G> constexpr int rows_at_once() { return V * N <= (V == 1 ? 4 : 8) && G < 1024 ? 2 : 1; }
 
 // N loads of V elements per lane and row.
 template <typename XT, typename YT, int V, int N, int G>
@@ -253,20 +253,22 @@ __global__ void __launch_bounds__(threads<G>(), V * N <= 8 ? 1024 / threads<G>()
     Group<G, U> grp{sm, 0};
     const float inv = 1.f / (float)p.D;
     const int c0 = at.lane * V;                       // this lane's columns: c0 + j * G * V ..
-    constexpr bool KEEP = V * N <= 16;                // weights stay in registers
+    constexpr bool KEEP = V * N <= 16 && G < 1024;    // weights stay in registers
     Vals<V> w[KEEP ? N : 1], bi[KEEP ? N : 1];
-    auto weights = [&](int j, Vals<V>& wv, Vals<V>& bv) {
+    auto weights = [&](auto type, int j, Vals<V>& wv, Vals<V>& bv) {
         const int c = c0 + j * G * V;
         wv.all(1.f);
         bv.all(0.f);
         if (c < p.D) {
-            if (p.weight) wv = load_w<V>(p.weight, p.w_bf16, c);
-            if (p.bias) bv = load_w<V>(p.bias, p.w_bf16, c);
+            if (p.weight) wv = load_w<decltype(type), V>(p.weight, c);
+            if (p.bias) bv = load_w<decltype(type), V>(p.bias, c);
         }
     };
     if constexpr (KEEP) {
+        with_weights(p, [&](auto type) {
 #pragma unroll
-        for (int j = 0; j < N; ++j) weights(j, w[j], bi[j]);
+            for (int j = 0; j < N; ++j) weights(type, j, w[j], bi[j]);
+        });
     }
     const size_t jump = (size_t)at.step * p.D, next = (size_t)at.PER * p.D;
     const XT* x = static_cast<const XT*>(p.x) + (size_t)at.row * p.D + c0;      // the rows to fetch next
@@ -319,13 +321,22 @@ __global__ void __launch_bounds__(threads<G>(), V * N <= 8 ? 1024 / threads<G>()
             rstd[u] = rsqrtf(rstd[u] * inv + p.eps);
             Vals<V> rs;
             rs.all(rstd[u]);
+            auto put = [&](int j, const Vals<V>& wv, const Vals<V>& bv) {
+                const Vals<V> o = fma(v[u][j] * rs, wv, bv);
+                if (c0 + j * G * V < p.D && GDR_INB(c0 + j * G * V + V <= p.D, 901)) store_v<YT, V>(y + u * next + j * G * V, o);
+            };
+            if constexpr (KEEP) {
 #pragma unroll
-            for (int j = 0; j < N; ++j) {
-                if (c0 + j * G * V >= p.D) continue;
-                Vals<V> wv, bv;
-                if constexpr (!KEEP) weights(j, wv, bv);
-                const Vals<V> o = fma(v[u][j] * rs, KEEP ? w[KEEP ? j : 0] : wv, KEEP ? bi[KEEP ? j : 0] : bv);
-                if (GDR_INB(c0 + j * G * V + V <= p.D, 901)) store_v<YT, V>(y + u * next + j * G * V, o);
+                for (int j = 0; j < N; ++j) put(j, w[j], bi[j]);
+            } else {
+                with_weights(p, [&](auto type) {
+#pragma unroll
+                    for (int j = 0; j < N; ++j) {
+                        Vals<V> wv, bv;
+                        weights(type, j, wv, bv);
+                        put(j, wv, bv);
+                    }
+                });
             }
             if (at.lane == 0) {
                 if (p.mean) p.mean[r + u * at.PER] = mean[u];
@@ -338,7 +349,7 @@ __global__ void __launch_bounds__(threads<G>(), V * N <= 8 ? 1024 / threads<G>()
 
 // Backward: dx, and the block's share of dweight and dbias.
 template <typename XT, typename YT, int V, int N, int G>
-__global__ void __launch_bounds__(threads<G>(), V * N <= 8 && G <= 256 ? 512 / threads<G>() : 1) norm_bwd_kernel(NormParams p) {
+__global__ void __launch_bounds__(threads<G>(), G <= 256 ? 512 / threads<G>() : 1) norm_bwd_kernel(NormParams p) {
     constexpr int U = rows_at_once<V, N, G>();
     extern __shared__ float part[];                   // G <= 32: the groups' sums [PER][D], in turn
     __shared__ __align__(16) float sm[2][G > 32 ? G / 32 : 1][2 * U];
@@ -346,16 +357,15 @@ __global__ void __launch_bounds__(threads<G>(), V * N <= 8 && G <= 256 ? 512 / t
     Group<G, 2 * U> grp{sm, 0};
     const float inv = 1.f / (float)p.D;
     const int c0 = at.lane * V;
-    constexpr bool KEEP = V * N <= 8;
-    Vals<V> w[KEEP ? N : 1];
-    auto weights = [&](int j, Vals<V>& wv) {
-        wv.all(1.f);
-        if (c0 + j * G * V < p.D && p.weight) wv = load_w<V>(p.weight, p.w_bf16, c0 + j * G * V);
-    };
-    if constexpr (KEEP) {
+    static_assert(V * N <= 8, "weights, rows and sums in registers");
+    Vals<V> w[N];
+    with_weights(p, [&](auto type) {
 #pragma unroll
-        for (int j = 0; j < N; ++j) weights(j, w[j]);
-    }
+        for (int j = 0; j < N; ++j) {
+            w[j].all(1.f);
+            if (c0 + j * G * V < p.D && p.weight) w[j] = load_w<decltype(type), V>(p.weight, c0 + j * G * V);
+        }
+    });
     Vals<V> sw[N], sb[N];
 #pragma unroll
     for (int j = 0; j < N; ++j) { sw[j].all(0.f); sb[j].all(0.f); }
@@ -396,13 +406,11 @@ __global__ void __launch_bounds__(threads<G>(), V * N <= 8 && G <= 256 ? 512 / t
             off.all(-mean[u]);
 #pragma unroll
             for (int j = 0; j < N; ++j) {             // columns behind D: dy is zero
-                Vals<V> wv;
-                if constexpr (!KEEP) weights(j, wv);
                 xh[u][j] = (rx[u][j].vals() + off) * rs;
                 d[u][j] = rd[u][j].vals();
                 sw[j] = fma(d[u][j], xh[u][j], sw[j]);
                 sb[j] = sb[j] + d[u][j];
-                d[u][j] = d[u][j] * (KEEP ? w[KEEP ? j : 0] : wv);
+                d[u][j] = d[u][j] * w[j];
                 s1 = j ? s1 + d[u][j] : d[u][j];
                 s2 = j ? fma(d[u][j], xh[u][j], s2) : d[u][j] * xh[u][j];
             }
@@ -479,11 +487,13 @@ __global__ void __launch_bounds__(LONG_NT) norm_fwd_long_kernel(NormParams p) {
         for (int c = threadIdx.x; c < p.D; c += LONG_NT) { const float v = ld_f32(x + c) - mean; s[0] = fmaf(v, v, s[0]); }
         grp.sum(s);
         const float rstd = rsqrtf(s[0] * inv + p.eps);
-        for (int c = threadIdx.x; c < p.D; c += LONG_NT) {
-            const float w = p.weight ? load_w<1>(p.weight, p.w_bf16, c).v : 1.f;
-            const float b = p.bias ? load_w<1>(p.bias, p.w_bf16, c).v : 0.f;
-            st_from_f32(y + c, fmaf((ld_f32(x + c) - mean) * rstd, w, b));
-        }
+        with_weights(p, [&](auto type) {
+            for (int c = threadIdx.x; c < p.D; c += LONG_NT) {
+                const float w = p.weight ? load_w<decltype(type), 1>(p.weight, c).v : 1.f;
+                const float b = p.bias ? load_w<decltype(type), 1>(p.bias, c).v : 0.f;
+                st_from_f32(y + c, fmaf((ld_f32(x + c) - mean) * rstd, w, b));
+            }
+        });
         if (threadIdx.x == 0) {
             if (p.mean) p.mean[r] = mean;
             if (p.rstd) p.rstd[r] = rstd;
@@ -500,20 +510,24 @@ __global__ void __launch_bounds__(LONG_NT) norm_dx_long_kernel(NormParams p) {
         const YT* dy = static_cast<const YT*>(p.dy) + (size_t)r * p.D;
         const float mean = p.mean[r], rstd = p.rstd[r];
         float s[2] = {0.f, 0.f};
-        for (int c = threadIdx.x; c < p.D; c += LONG_NT) {
-            const float w = p.weight ? load_w<1>(p.weight, p.w_bf16, c).v : 1.f;
-            const float wd = w * ld_f32(dy + c);
-            s[0] += wd;
-            s[1] = fmaf(wd, (ld_f32(x + c) - mean) * rstd, s[1]);
-        }
+        with_weights(p, [&](auto type) {
+            for (int c = threadIdx.x; c < p.D; c += LONG_NT) {
+                const float w = p.weight ? load_w<decltype(type), 1>(p.weight, c).v : 1.f;
+                const float wd = w * ld_f32(dy + c);
+                s[0] += wd;
+                s[1] = fmaf(wd, (ld_f32(x + c) - mean) * rstd, s[1]);
+            }
+        });
         grp.sum(s);
         const float s1 = s[0] * inv, s2 = s[1] * inv;
         XT* dx = static_cast<XT*>(p.dx) + (size_t)r * p.D;
-        for (int c = threadIdx.x; c < p.D; c += LONG_NT) {
-            const float w = p.weight ? load_w<1>(p.weight, p.w_bf16, c).v : 1.f;
-            const float xh = (ld_f32(x + c) - mean) * rstd;
-            st_from_f32(dx + c, rstd * (w * ld_f32(dy + c) - s1 - xh * s2));
-        }
+        with_weights(p, [&](auto type) {
+            for (int c = threadIdx.x; c < p.D; c += LONG_NT) {
+                const float w = p.weight ? load_w<decltype(type), 1>(p.weight, c).v : 1.f;
+                const float xh = (ld_f32(x + c) - mean) * rstd;
+                st_from_f32(dx + c, rstd * (w * ld_f32(dy + c) - s1 - xh * s2));
+            }
+        });
     }
 }
 // The shares of dweight and dbias: rows part, part + parts, .. of one column per thread.
