@@ -48,14 +48,15 @@ static gdr_status launch_select(const BeamParams& p, cudaStream_t st) {
     if (e != cudaSuccess) return cuda_fail(e, "launch(beam rows)");
     cudaLaunchConfig_t cfg = {};        // launched ahead of the rows' end, waits for it
     cfg.gridDim = dim3(p.G);
-    cfg.blockDim = dim3(GNT);
+    const bool few = (long long)p.K * p.pieces * p.M <= 512;
+    cfg.blockDim = dim3(few ? 256 : 1024);
     cfg.stream = st;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, beam_group_kernel<XT>, p);
+    e = few ? cudaLaunchKernelEx(&cfg, beam_group_kernel<XT, 256>, p) : cudaLaunchKernelEx(&cfg, beam_group_kernel<XT, 1024>, p);
     return e == cudaSuccess ? GDR_OK : cuda_fail(e, "launch(beam groups)");
 }
 

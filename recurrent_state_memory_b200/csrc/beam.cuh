@@ -86,9 +86,58 @@ __device__ __forceinline__ int sum8(int v) {
     return v;
 }
 
+// E elements of one thread as they lie in memory: two of 16 bits a register, element 2 j + h in half h
+// of word j.
+template <typename XT, int E> struct Held;
+template <int E> struct Held<float, E> {
+    float v[E];
+    __device__ __forceinline__ void set(int j, unsigned w) { v[j] = __uint_as_float(w); }
+    __device__ __forceinline__ void one(int i, float x) { v[i] = x; }
+    __device__ __forceinline__ float top() const {                   // passes NaN over
+        float t = v[0];
+#pragma unroll
+        for (int i = 1; i < E; ++i) t = fmaxf(t, v[i]);
+        return t;
+    }
+    __device__ __forceinline__ Pair two(int j) const { return pair(v[2 * j], v[2 * j + 1]); }
+    // a bit for every element that is at least x
+    __device__ __forceinline__ unsigned reach(float x) const {
+        unsigned m = 0;
+#pragma unroll
+        for (int i = 0; i < E; ++i) m |= v[i] >= x ? 1u << i : 0u;
+        return m;
+    }
+    static __device__ __forceinline__ unsigned every() { return (unsigned)((1ull << E) - 1); }
+    static __device__ __forceinline__ int element(int bit) { return bit; }
+};
+template <int E> struct Held<__nv_bfloat16, E> {
+    __nv_bfloat162 v[E / 2];
+    __device__ __forceinline__ void set(int j, unsigned w) { v[j] = *reinterpret_cast<__nv_bfloat162*>(&w); }
+    __device__ __forceinline__ void one(int i, float x) { (i & 1 ? v[i / 2].y : v[i / 2].x) = __float2bfloat16_rn(x); }
+    __device__ __forceinline__ float top() const {
+        __nv_bfloat162 t = v[0];
+#pragma unroll
+        for (int i = 1; i < E / 2; ++i) t = __hmax2(t, v[i]);
+        return fmaxf(__low2float(t), __high2float(t));
+    }
+    __device__ __forceinline__ Pair two(int j) const {
+        const unsigned w = *reinterpret_cast<const unsigned*>(&v[j]);
+        return pair(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+    }
+    __device__ __forceinline__ unsigned reach(float x) const {       // x is one of the values: exact in 16 bits
+        const __nv_bfloat162 x2 = __float2bfloat162_rn(x);
+        unsigned m = 0;
+#pragma unroll
+        for (int j = 0; j < E / 2; ++j) m |= (__hge2_mask(v[j], x2) & 0x00010001u) << j;
+        return m;
+    }
+    static __device__ __forceinline__ unsigned every() { return ((1u << (E / 2)) - 1) * 0x00010001u; }
+    static __device__ __forceinline__ int element(int bit) { return 2 * (bit & 15) + (bit >> 4); }
+};
+
 // E elements per thread: 16-byte loads (VEC) or one by one.
 template <typename XT, int E, bool VEC>
-__global__ void __launch_bounds__(NT, E > 8 ? 4 : 6) beam_row_kernel(BeamParams p) {
+__global__ void __launch_bounds__(NT, E > 8 && sizeof(XT) == 4 ? 4 : 6) beam_row_kernel(BeamParams p) {
     __shared__ unsigned marks[MARKS], the_mark;
     __shared__ float2 sums[WARPS];
     __shared__ int count;
@@ -101,44 +150,41 @@ __global__ void __launch_bounds__(NT, E > 8 ? 4 : 6) beam_row_kernel(BeamParams 
     constexpr int W = VEC ? 16 / (int)sizeof(XT) : 1;                // elements of a load
     // element i of this thread: load i / W at (i / W * NT + thread) * W
     auto at = [&](int i) { return (i / W * NT + (int)threadIdx.x) * W + i % W; };
-    float v[E];
+    Held<XT, E> v;
 #pragma unroll
     for (int j = 0; j < E / W; ++j) {
         const int o = (j * NT + (int)threadIdx.x) * W;
         if constexpr (VEC) {
             if (o + W <= n) {
                 const uint4 q = *reinterpret_cast<const uint4*>(x + o);
-                const unsigned w[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-                for (int i = 0; i < W; ++i) {
-                    if constexpr (sizeof(XT) == 4) v[j * W + i] = __uint_as_float(w[i]);
-                    else v[j * W + i] = __uint_as_float(i & 1 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
-                }
+                v.set(4 * j, q.x); v.set(4 * j + 1, q.y); v.set(4 * j + 2, q.z); v.set(4 * j + 3, q.w);
             } else {
 #pragma unroll
-                for (int i = 0; i < W; ++i) v[j * W + i] = o + i < n ? ld_f32(x + o + i) : -INFINITY;
+                for (int i = 0; i < W; ++i) v.one(j * W + i, o + i < n ? ld_f32(x + o + i) : -INFINITY);
             }
         } else {
-            v[j] = o < n ? ld_f32(x + o) : -INFINITY;
+            v.one(j, o < n ? ld_f32(x + o) : -INFINITY);
         }
     }
     if (threadIdx.x == 0) { count = 0; the_mark = 0; }
-    float top = -INFINITY;
-#pragma unroll
-    for (int i = 0; i < E; ++i) top = fmaxf(top, v[i]);              // passes NaN over
+    const float top = v.top();
     const int active = min((n + W - 1) / W, NT), lanes = group_lanes(active, p.M);
     const unsigned key = at(0) < n ? key_of(top) : 0u, top_key = __reduce_max_sync(0xffffffffu, key);
     put_marks(key, lanes, active, marks);
     // exp(x - maximum); all masked (maximum -inf): nothing but NaN counts.  +inf gives NaN: the beam
     // drops out.
     const float big = top_key ? value_of(top_key) : -INFINITY, base = big == -INFINITY ? 0.f : big;
-    float s = 0.f;
+    const Pair off = pair(-base, -base), log2e = pair(1.44269502f, 1.44269502f);
+    Pair s2 = pair(0.f, 0.f);
 #pragma unroll
-    for (int i = 0; i < E; ++i) {
-        float e;
-        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"((v[i] - base) * 1.44269502f));
-        s += e;
+    for (int j = 0; j < E / 2; ++j) {
+        const Pair d = (v.two(j) + off) * log2e;
+        float e0, e1;
+        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e0) : "f"(lo(d)));
+        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e1) : "f"(hi(d)));
+        s2 = s2 + pair(e0, e1);
     }
+    float s = lo(s2) + hi(s2);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
     if (lane == 0) sums[warp] = make_float2(big, s);
@@ -148,17 +194,10 @@ __global__ void __launch_bounds__(NT, E > 8 ? 4 : 6) beam_row_kernel(BeamParams 
     const size_t out = (size_t)row * p.pieces + piece;
     const unsigned mark = the_mark;
     // this thread's elements that reach the mark; a mark of -inf or less lets everything through
-    unsigned hits = 0;
-    if (mark > key_of(-INFINITY)) {
-        const float least = value_of(mark);
-#pragma unroll
-        for (int i = 0; i < E; ++i) hits |= v[i] >= least ? 1u << i : 0u;
-    } else {
-        hits = (unsigned)((1ull << E) - 1);
-    }
+    unsigned hits = mark > key_of(-INFINITY) ? v.reach(value_of(mark)) : v.every();
     auto element = [&](int i) { return (unsigned long long)key_of(ld_f32(x + at(i))) << 32 | (unsigned)~at(i); };
     while (hits) {                                                   // few: read them again
-        const int i = __ffs(hits) - 1;
+        const int i = v.element(__ffs(hits) - 1);
         hits &= hits - 1;
         if (at(i) >= n) continue;
         const unsigned long long c = element(i);
@@ -235,18 +274,16 @@ __device__ __forceinline__ unsigned key_of_score(double s) { return key_of(__dou
 
 // How far two scores may be from their 64-bit values together, u = 2^-24: an exponent d = x - maximum
 // and its product with the rounded log2(e) are off by 2.25 u |d|, |d| weighted by e^d is at most
-// log V <= 22: 50 u; the exponential 3 u; 32 sums in a thread, 5 in its warp, 8 across the block and the
-// factors of warps and pieces (4 u each; the pieces are added in 64 bits) 53 u: together 106 u of the
-// sum, as much in its logarithm, whose rounding adds 17 u (it is at most 22).  123 u = 7.4e-6, twice
+// log V <= 22: 50 u; the exponential 3 u; 17 sums in a thread, 5 in its warp, 8 across the block and the
+// factors of warps and pieces (4 u each; the pieces are added in 64 bits) 38 u: together 91 u of the
+// sum, as much in its logarithm, whose rounding adds 17 u (it is at most 22).  108 u = 6.5e-6, twice
 // that for two beams.
-constexpr double TOL = 1.5e-5;
+constexpr double TOL = 1.3e-5;
 
-constexpr int GNT = 1024;               // threads of a group's block
-constexpr int GWARPS = GNT / 32;
 constexpr int HELD = 2;                 // candidates of a thread that stay in registers
 
 // The 64-bit sum over one beam's logits.
-template <typename XT>
+template <typename XT, int GNT>
 __device__ double exact_lse(const BeamParams& p, int row, double big, double* red) {
     const XT* x = static_cast<const XT*>(p.logits) + (size_t)row * p.row;
     double s = 0.0;
@@ -256,13 +293,15 @@ __device__ double exact_lse(const BeamParams& p, int row, double big, double* re
     if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = s;
     __syncthreads();
     s = 0.0;
-    for (int i = 0; i < GWARPS; ++i) s += red[i];
+    for (int i = 0; i < GNT / 32; ++i) s += red[i];
     __syncthreads();
     return big + log(s);
 }
 
-template <typename XT>
+// GNT threads: as many as there are candidates for, 256 or 1024.
+template <typename XT, int GNT>
 __global__ void __launch_bounds__(GNT) beam_group_kernel(BeamParams p) {
+    constexpr int GWARPS = GNT / 32;
     __shared__ unsigned marks[MARKS], the_mark;
     __shared__ int count;
     __shared__ Cand list[LIST];
@@ -423,7 +462,7 @@ __global__ void __launch_bounds__(GNT) beam_group_kernel(BeamParams p) {
         if (!__syncthreads_or(near)) break;
         for (int k = 0; k < p.K; ++k) {
             if (!redo[k]) continue;
-            const double l = exact_lse<XT>(p, g * p.K + k, top[k], red);
+            const double l = exact_lse<XT, GNT>(p, g * p.K + k, top[k], red);
             if (threadIdx.x == 0) lse[k] = l;
         }
         __syncthreads();

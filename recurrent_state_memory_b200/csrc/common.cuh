@@ -61,6 +61,15 @@ template <> __device__ __forceinline__ void st_from_f32<__nv_bfloat16>(__nv_bflo
     *p = __float2bfloat16_rn(x);
 }
 
+// Two fp32 values in one register pair: sm_100 adds, multiplies and fuses them in one instruction.
+struct Pair { unsigned long long v; };
+__device__ __forceinline__ Pair pair(float a, float b) { Pair p; asm("mov.b64 %0, {%1, %2};" : "=l"(p.v) : "f"(a), "f"(b)); return p; }
+__device__ __forceinline__ float lo(Pair p) { float a; asm("{\n\t.reg .f32 t;\n\tmov.b64 {%0, t}, %1;\n\t}" : "=f"(a) : "l"(p.v)); return a; }
+__device__ __forceinline__ float hi(Pair p) { float b; asm("{\n\t.reg .f32 t;\n\tmov.b64 {t, %0}, %1;\n\t}" : "=f"(b) : "l"(p.v)); return b; }
+__device__ __forceinline__ Pair operator+(Pair a, Pair b) { Pair d; asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d.v) : "l"(a.v), "l"(b.v)); return d; }
+__device__ __forceinline__ Pair operator*(Pair a, Pair b) { Pair d; asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d.v) : "l"(a.v), "l"(b.v)); return d; }
+__device__ __forceinline__ Pair fma(Pair a, Pair b, Pair c) { Pair d; asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d.v) : "l"(a.v), "l"(b.v), "l"(c.v)); return d; }
+
 // Log-decay of one gate value.  gate_mode 1: g = -softplus(a) = -(max(a,0) + log1p(e^{-|a|})),
 // the activation the workloads state; gate_mode 0: the value is g itself.
 __device__ __forceinline__ float log_decay(float a, int gate_mode) {

@@ -44,15 +44,6 @@ struct NormParams {
     int w_bf16;             // weight and bias are bf16 (else fp32)
 };
 
-// Two fp32 values in one register pair: sm_100 adds, multiplies and fuses them in one instruction.
-struct Pair { unsigned long long v; };
-__device__ __forceinline__ Pair pair(float a, float b) { Pair p; asm("mov.b64 %0, {%1, %2};" : "=l"(p.v) : "f"(a), "f"(b)); return p; }
-__device__ __forceinline__ float lo(Pair p) { float a; asm("{\n\t.reg .f32 t;\n\tmov.b64 {%0, t}, %1;\n\t}" : "=f"(a) : "l"(p.v)); return a; }
-__device__ __forceinline__ float hi(Pair p) { float b; asm("{\n\t.reg .f32 t;\n\tmov.b64 {t, %0}, %1;\n\t}" : "=f"(b) : "l"(p.v)); return b; }
-__device__ __forceinline__ Pair operator+(Pair a, Pair b) { Pair d; asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d.v) : "l"(a.v), "l"(b.v)); return d; }
-__device__ __forceinline__ Pair operator*(Pair a, Pair b) { Pair d; asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d.v) : "l"(a.v), "l"(b.v)); return d; }
-__device__ __forceinline__ Pair fma(Pair a, Pair b, Pair c) { Pair d; asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d.v) : "l"(a.v), "l"(b.v), "l"(c.v)); return d; }
-
 // A lane's V elements: pairs, or one value.
 template <int V> struct Vals {
     static constexpr int H = V / 2;
