@@ -56,7 +56,7 @@ __device__ __forceinline__ float value_of(unsigned k) { return __uint_as_float(k
 // the want-th largest of the maxima of groups of lanes.  group_lanes: the largest groups of which
 // the `active` first threads make at least 2 * want (so at most 4 * want, unless a group is one
 // lane).  0 when there are not that many; it then lets everything through.
-constexpr int MARKS = 4 * (MOST + 1);
+constexpr int MARKS = 4 * (MOST + 2);
 __device__ __forceinline__ int group_lanes(int active, int want) {
     int l = 32;
     while (l > 1 && active < 2 * want * l) l >>= 1;
@@ -65,6 +65,7 @@ __device__ __forceinline__ int group_lanes(int active, int want) {
 __device__ __forceinline__ void put_marks(unsigned key, int lanes, int active, unsigned* marks) {
     for (int o = 1; o < lanes; o <<= 1) key = max(key, __shfl_xor_sync(0xffffffffu, key, o));
     if ((threadIdx.x & (lanes - 1)) == 0 && (int)threadIdx.x < active) marks[threadIdx.x / lanes] = key;
+    if (threadIdx.x < 4) marks[(active + lanes - 1) / lanes + threadIdx.x] = 0;      // to a whole four
 }
 // Behind a barrier; *mark was set to 0 before it.  Each warp compares 32 of the n marks with all.
 template <int WARPS_> __device__ __forceinline__ void find_mark(const unsigned* marks, int n, int want, unsigned* mark) {
@@ -73,8 +74,12 @@ template <int WARPS_> __device__ __forceinline__ void find_mark(const unsigned* 
         const int i = i0 + lane;
         const unsigned k = i < n ? marks[i] : 0u;
         int rank = 0;
-#pragma unroll 8
-        for (int j = 0; j < n; ++j) rank += marks[j] > k || (marks[j] == k && j < i);
+#pragma unroll 4
+        for (int j = 0; j < n; j += 4) {
+            const uint4 q = *reinterpret_cast<const uint4*>(marks + j);
+            rank += (q.x > k || (q.x == k && j < i)) + (q.y > k || (q.y == k && j + 1 < i)) +
+                    (q.z > k || (q.z == k && j + 2 < i)) + (q.w > k || (q.w == k && j + 3 < i));
+        }
         if (i < n && rank == want - 1) *mark = k;
     }
 }
@@ -138,7 +143,8 @@ template <int E> struct Held<__nv_bfloat16, E> {
 // E elements per thread: 16-byte loads (VEC) or one by one.
 template <typename XT, int E, bool VEC>
 __global__ void __launch_bounds__(NT, E > 8 && sizeof(XT) == 4 ? 4 : 6) beam_row_kernel(BeamParams p) {
-    __shared__ unsigned marks[MARKS], the_mark;
+    __shared__ __align__(16) unsigned marks[MARKS];
+    __shared__ unsigned the_mark;
     __shared__ float2 sums[WARPS];
     __shared__ int count;
     __shared__ unsigned long long pick[WARPS];
@@ -274,11 +280,11 @@ __device__ __forceinline__ unsigned key_of_score(double s) { return key_of(__dou
 
 // How far two scores may be from their 64-bit values together, u = 2^-24: an exponent d = x - maximum
 // and its product with the rounded log2(e) are off by 2.25 u |d|, |d| weighted by e^d is at most
-// log V <= 22: 50 u; the exponential 3 u; 17 sums in a thread, 5 in its warp, 8 across the block and the
-// factors of warps and pieces (4 u each; the pieces are added in 64 bits) 38 u: together 91 u of the
-// sum, as much in its logarithm, whose rounding adds 17 u (it is at most 22).  108 u = 6.5e-6, twice
-// that for two beams.
-constexpr double TOL = 1.3e-5;
+// log V <= 22: 50 u; the exponential 3 u; 17 sums in a thread, 5 in its warp, 8 across the block, 6
+// across the pieces (each lane adds its own in 64 bits) and the factors of warps and pieces (4 u
+// each) 44 u: together 97 u of the sum, as much in its logarithm, whose rounding adds 17 u (it is at
+// most 22).  114 u = 6.8e-6, twice that for two beams.
+constexpr double TOL = 1.4e-5;
 
 constexpr int HELD = 2;                 // candidates of a thread that stay in registers
 
@@ -302,7 +308,8 @@ __device__ double exact_lse(const BeamParams& p, int row, double big, double* re
 template <typename XT, int GNT>
 __global__ void __launch_bounds__(GNT) beam_group_kernel(BeamParams p) {
     constexpr int GWARPS = GNT / 32;
-    __shared__ unsigned marks[MARKS], the_mark;
+    __shared__ __align__(16) unsigned marks[MARKS];
+    __shared__ unsigned the_mark;
     __shared__ int count;
     __shared__ Cand list[LIST];
     __shared__ Cand first[MOST + 1];                // the best in order, and the one behind
@@ -317,6 +324,8 @@ __global__ void __launch_bounds__(GNT) beam_group_kernel(BeamParams p) {
     if (warp < p.K) { sc = p.scores[(size_t)g * p.K + warp]; ended = p.finished && p.finished[(size_t)g * p.K + warp]; }
     asm volatile("griddepcontrol.wait;" ::: "memory");
 
+    float2 mine = make_float2(-INFINITY, 0.f);      // of beam `warp`, its piece `lane`
+    if (warp < p.K && lane < p.pieces) mine = p.sums[((size_t)g * p.K + warp) * p.pieces + lane];
     // this thread's candidates: beam, position in its lists, logit and token.  A warp's lanes lie
     // evenly over all beams and pieces, so that every warp has some of the best.
     const int span = (n + 31) / 32;
@@ -337,8 +346,11 @@ __global__ void __launch_bounds__(GNT) beam_group_kernel(BeamParams p) {
     for (int k = warp; k < p.K; k += GWARPS) {      // a warp per beam, lanes along its pieces
         const size_t row = (size_t)g * p.K + k;
         const float2* sums = p.sums + row * p.pieces;
-        if (k != warp) { sc = p.scores[row]; ended = p.finished && p.finished[row]; }
-        const float2 mine = lane < p.pieces ? sums[lane] : make_float2(-INFINITY, 0.f);
+        if (k != warp) {
+            sc = p.scores[row];
+            ended = p.finished && p.finished[row];
+            mine = lane < p.pieces ? sums[lane] : make_float2(-INFINITY, 0.f);
+        }
         float big = mine.x;
         for (int i = lane + 32; i < p.pieces; i += 32) big = fmaxf(big, sums[i].x);
 #pragma unroll
@@ -351,14 +363,15 @@ __global__ void __launch_bounds__(GNT) beam_group_kernel(BeamParams p) {
         };
         add(mine);
         for (int i = lane + 32; i < p.pieces; i += 32) add(sums[i]);
+        float total = (float)s;
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
         if (lane == 0) {
             const bool no_score = !(sc < INFINITY) || sc == -INFINITY;
             score[k] = sc;
             top[k] = big;
-            lse[k] = (double)big + (double)logf((float)s);
-            kind[k] = no_score ? OUT : ended ? ENDED : !(big > -INFINITY && big < INFINITY && s == s) ? OUT : LIVE;
+            lse[k] = (double)big + (double)logf(total);
+            kind[k] = no_score ? OUT : ended ? ENDED : !(big > -INFINITY && big < INFINITY && total == total) ? OUT : LIVE;
             redo[k] = 0;
         }
     }
