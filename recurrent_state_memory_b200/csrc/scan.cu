@@ -13,30 +13,33 @@ namespace scn {
 enum Pass { FWD, BWD, STEP };
 
 // Blocks of a cluster (along the tokens): enough that the grid has about two blocks per SM, as far as
-// the sequence has tiles for them.
-static int cluster_of(long long tiles, int T, int tok, int sms) {
+// the sequence has tiles for them.  Where the largest clusters still leave a block per SM at most
+// (few channels, long sequences), a block's two groups take the turns alternately: 17.0 against
+// 31.4 us at B1 T20000 D11, 10.3 against 11.5 at B1 T16384 D128; with more channels than that a
+// block more is worth more than a group (B1 T32768 D512: 45 us with 8 blocks of one group, 56 of two).
+struct Split { int cluster, groups; };
+static Split split_of(long long tiles, int T, int tok, int sms, bool two_fit) {
     int n = 1;
     while (n < MAX_CLUSTER && tiles * n * 2 <= 2LL * sms && n * tok < T) n *= 2;
-    return n;
+    return {n, two_fit && n == MAX_CLUSTER && tiles * n <= sms && (long long)n * tok < T ? 2 : 1};
 }
 
 template <typename KERN>
-static gdr_status launch_clusters(KERN kern, const ScanParams& p, const ScanMaps& maps, int tok, size_t smem,
+static gdr_status launch_clusters(KERN kern, const ScanParams& p, const ScanMaps& maps, Split sp, size_t smem,
                                   cudaStream_t st) {
     const unsigned ct = (unsigned)((p.D + CH - 1) / CH);
-    const int ncl = cluster_of((long long)ct * p.B, p.T, tok, device_sm_count());
-    smem += (size_t)(2 * ncl - 1) * CH * sizeof(float2);
+    smem = sp.groups * smem + HAND_BYTES + (size_t)sp.groups * 2 * sp.cluster * CH * sizeof(float2);
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e == cudaSuccess && ncl > 8) e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e == cudaSuccess && sp.cluster > 8) e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(scan)");
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(ncl, ct, p.B);
-    cfg.blockDim = dim3(NT);
+    cfg.gridDim = dim3(sp.cluster, ct, p.B);
+    cfg.blockDim = dim3(NT * sp.groups);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = ncl; at[0].val.clusterDim.y = 1; at[0].val.clusterDim.z = 1;
+    at[0].val.clusterDim.x = sp.cluster; at[0].val.clusterDim.y = 1; at[0].val.clusterDim.z = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
     e = cudaLaunchKernelEx(&cfg, kern, p, maps);
@@ -114,9 +117,20 @@ static gdr_status launch_v(Pass pass, ScanParams& p, cudaStream_t st) {
         if (s == GDR_OK && pass == BWD && p.dh) s = encode<OT, V>(&maps.dh, p.dh, p, p.D, tok);
         if (s != GDR_OK) return s;
     }
-    if (pass == FWD)
-        return launch_clusters(scan_fwd_kernel<XT, GT, OT, V>, p, maps, tok, sizeof(FwdSmem<XT, GT, V>), st);
-    return launch_clusters(scan_bwd_kernel<XT, GT, OT, V>, p, maps, tok, sizeof(BwdSmem<XT, GT, OT, V>), st);
+    constexpr size_t fwd = sizeof(FwdSmem<XT, GT, V>), bwd = sizeof(BwdSmem<XT, GT, OT, V>);
+    constexpr size_t room = 227 * 1024 - HAND_BYTES - 4 * MAX_CLUSTER * CH * sizeof(float2);
+    constexpr bool fwd2 = 2 * fwd <= room, bwd2 = 2 * bwd <= room;
+    const Split sp = split_of((long long)((p.D + CH - 1) / CH) * p.B, p.T, tok, device_sm_count(), pass == FWD ? fwd2 : bwd2);
+    if (pass == FWD) {
+        if constexpr (fwd2) {
+            if (sp.groups == 2) return launch_clusters(scan_fwd_kernel<XT, GT, OT, V, 2>, p, maps, sp, fwd, st);
+        }
+        return launch_clusters(scan_fwd_kernel<XT, GT, OT, V, 1>, p, maps, sp, fwd, st);
+    }
+    if constexpr (bwd2) {
+        if (sp.groups == 2) return launch_clusters(scan_bwd_kernel<XT, GT, OT, V, 2>, p, maps, sp, bwd, st);
+    }
+    return launch_clusters(scan_bwd_kernel<XT, GT, OT, V, 1>, p, maps, sp, bwd, st);
 }
 
 // Four channels per thread (and tiles by TMA) where every row of every tensor starts on 16 bytes,

@@ -57,6 +57,12 @@ constexpr int WT = NT / 32;             // warps, along the tokens
 constexpr int MAX_CLUSTER = 16;
 constexpr int STAGES = 2;
 
+// Threads of one group (of GR in a block): a barrier of its own.
+template <int GR> __device__ __forceinline__ void group_sync(int grp) {
+    if constexpr (GR == 1) __syncthreads();
+    else asm volatile("bar.sync %0, %1;" ::"r"(1 + grp), "n"(NT) : "memory");
+}
+
 __device__ __forceinline__ int seq_len(const ScanParams& p, int b) {
     return p.lengths ? min(max(p.lengths[b], 0), p.T) : p.T;
 }
@@ -141,7 +147,7 @@ template <int V, int ELEMS> struct Tile {
     static constexpr int R = ELEMS / V;         // tokens of a run
     static constexpr int TOK = WT * TL * R;     // tokens of a block
     int warp, lane_t, c;                        // warp, run in the warp, first channel in the block
-    __device__ __forceinline__ Tile() : warp(threadIdx.x >> 5), lane_t((threadIdx.x & 31) / LC),
+    __device__ __forceinline__ Tile() : warp((threadIdx.x >> 5) & (WT - 1)), lane_t((threadIdx.x & 31) / LC),
                                         c(((threadIdx.x & 31) % LC) * V) {}
     __device__ __forceinline__ int first_token() const { return (warp * TL + lane_t) * R; }
 };
@@ -214,49 +220,84 @@ __device__ __forceinline__ void warp_runs(float (&A)[V], float (&H)[V], float (&
     }
 }
 
+// The state at a turn's start goes from turn to turn.  With two groups in a block, which take the
+// turns alternately, it goes through shared memory: the warp that has it for turn k + 1 arrives at
+// the barrier that turn k + 1's warp waits at (two barriers in turn).
+template <int GR> struct Carry {
+    float v;                    // this lane's channel
+    float (*hand)[CH];          // [2]
+    __device__ __forceinline__ void take(int k) {
+        if constexpr (GR > 1) {
+            if (k == 0) return;
+            asm volatile("bar.sync %0, 64;" ::"r"(3 + ((k - 1) & 1)) : "memory");
+            v = hand[(k - 1) & 1][threadIdx.x & 31];
+        }
+    }
+    __device__ __forceinline__ void give(int k, int turns) {
+        if constexpr (GR > 1) {
+            if (k + 1 >= turns) return;
+            hand[k & 1][threadIdx.x & 31] = v;
+            asm volatile("bar.arrive %0, 64;" ::"r"(3 + (k & 1)) : "memory");
+        }
+    }
+};
+
 // The state before every warp's runs, along the scan's direction, by one warp (lane = channel).
-// agg: the block's warps' (A, H); carry: the state at the cluster's turn start, which every block
-// holds alike and moves on by the turn.  xch and bars hold two turns' worth: a block sends turn
-// k + 2's only when it has turn k + 1's from every peer, each of which sent it behind its last
-// read of turn k's.  lost: a wait ran out (status word); the block goes on without waiting.
-template <bool UP>
+// agg: the group's warps' (A, H); carry: the state at the cluster's turn start, which every block
+// holds alike and moves on by the turn.  xch and bars hold two of the group's turns j = k / GR: a
+// block sends turn j + 2's only when it has turn j + 1's from every peer, each of which sent it
+// behind its last read of turn j's.  lost: a wait ran out (status word); the block goes on without
+// waiting.
+template <bool UP, int GR>
 __device__ __forceinline__ void warp_starts(const float2 (*agg)[CH], float2 (*xch)[CH], uint64_t* bars,
-                                            float (*start)[CH], float& carry, bool& lost, int k, int rank, int ncl) {
-    const int c = threadIdx.x & 31;
+                                            float (*start)[CH], Carry<GR>& carry, bool& lost, int k, int turns, int rank,
+                                            int ncl) {
+    const int c = threadIdx.x & 31, j = k / GR;
     float2 e[WT];
 #pragma unroll
     for (int w = 0; w < WT; ++w) e[w] = agg[UP ? w : WT - 1 - w][c];
-    float s = carry;
+    float s, all;
     if (ncl > 1) {
         float A = 1.f, H = 0.f;
 #pragma unroll
         for (int w = 0; w < WT; ++w) { H = fmaf(e[w].x, H, e[w].y); A *= e[w].x; }
-        xch += (k & 1) * ncl;
-        uint64_t* bar = bars + (k & 1);
+        xch += (j & 1) * ncl;
+        uint64_t* bar = bars + (j & 1);
         if (c == 0) expect_bytes(bar, (uint32_t)(ncl * CH * sizeof(float2)));
         for (int r = 0; r < ncl; ++r) store_peer(&xch[rank][c], make_float2(A, H), bar, r);
-        if (!lost) lost = !wait_phase(bar, (uint32_t)(k >> 1) & 1u);
-        float all = carry;
+        if (!lost) lost = !wait_phase(bar, (uint32_t)(j >> 1) & 1u);
+        // the blocks before this one as one piece, then the whole turn: only one product each waits
+        // for the carry
+        float pA = 1.f, pH = 0.f;
+        A = 1.f; H = 0.f;
         for (int i = 0; i < ncl; ++i) {
             const int r = UP ? i : ncl - 1 - i;
-            if (r == rank) s = all;
+            if (r == rank) { pA = A; pH = H; }
             const float2 x = xch[r][c];
-            all = fmaf(x.x, all, x.y);
+            H = fmaf(x.x, H, x.y);
+            A *= x.x;
         }
-        carry = all;
+        carry.take(k);
+        s = fmaf(pA, carry.v, pH);
+        all = fmaf(A, carry.v, H);
+        carry.v = all;
+        carry.give(k, turns);
+    } else {
+        carry.take(k);
+        s = carry.v;
     }
 #pragma unroll
     for (int w = 0; w < WT; ++w) {
         start[UP ? w : WT - 1 - w][c] = s;
         s = fmaf(e[w].x, s, e[w].y);
     }
-    if (ncl == 1) carry = s;
+    if (ncl == 1) { carry.v = s; carry.give(k, turns); }
 }
 
-// Before the first turn: the barriers (n of them), and the peers' shared memory exists.
-__device__ __forceinline__ void barriers_begin(uint64_t* bars, int n, int ncl) {
+// Before the first turn: every group's barriers (n of them), and the peers' shared memory exists.
+template <typename S> __device__ __forceinline__ void barriers_begin(S* sm, int groups, int n, int ncl) {
     if (threadIdx.x == 0) {
-        for (int i = 0; i < n; ++i) tc::mbar_init(&bars[i], 1);
+        for (int i = 0; i < groups * n; ++i) tc::mbar_init(&sm[i / n].bars[i % n], 1);
         tc::fence_mbar_init();
     }
     if (ncl > 1) cluster_sync();
@@ -287,18 +328,24 @@ template <typename XT, typename GT, int V> struct FwdSmem {
     float2 agg[WT][CH];
     float start[WT][CH];
     uint64_t bars[2 + STAGES];          // the exchange's, the stages'
-    float2 xch[1][CH];                  // [2][cluster][CH]: the launch adds the rest
 };
+// Behind the groups' parts: the carry's hand-over [2][CH], then every group's xch [2][cluster][CH].
+constexpr size_t HAND_BYTES = 2 * CH * sizeof(float);
 
-template <typename XT, typename GT, typename OT, int V>
-__global__ void __launch_bounds__(NT, V > 1 ? 2 : 3) scan_fwd_kernel(ScanParams p, const __grid_constant__ ScanMaps maps) {
+// GR groups of 8 warps in a block take the turns alternately: where there is a block per SM at most,
+// the second group computes while the first one waits for the cluster.
+template <typename XT, typename GT, typename OT, int V, int GR>
+__global__ void __launch_bounds__(NT * GR, GR > 1 ? 1 : V > 1 ? 2 : 3) scan_fwd_kernel(ScanParams p, const __grid_constant__ ScanMaps maps) {
     using L = Tile<V, fwd_elems<V>()>;
     using S = FwdSmem<XT, GT, V>;
     constexpr int R = L::R;
     extern __shared__ __align__(128) unsigned char raw[];
-    S& sm = *reinterpret_cast<S*>(raw);
     const L l;
-    const int rank = (int)cluster_rank(), ncl = (int)cluster_size();
+    const int rank = (int)cluster_rank(), ncl = (int)cluster_size(), grp = GR > 1 ? threadIdx.x / NT : 0;
+    S* const parts = reinterpret_cast<S*>(raw);
+    S& sm = parts[grp];
+    float (*const hand)[CH] = reinterpret_cast<float (*)[CH]>(parts + GR);
+    float2 (*const xch)[CH] = reinterpret_cast<float2 (*)[CH]>(reinterpret_cast<unsigned char*>(parts + GR) + HAND_BYTES) + grp * 2 * ncl;
     const int b = blockIdx.z, c0 = blockIdx.y * CH, c = c0 + l.c;
     const bool on = c < p.D;                              // V divides D, or V = 1
     const int len = seq_len(p, b), nck = (p.T + CKPT - 1) / CKPT;
@@ -309,9 +356,9 @@ __global__ void __launch_bounds__(NT, V > 1 ? 2 : 3) scan_fwd_kernel(ScanParams 
     const int tile = rank * L::TOK, first = tile + l.first_token();     // of turn 0: this block's, this thread's
     bool lost = false;
 
-    barriers_begin(sm.bars, 2 + STAGES, ncl);
+    barriers_begin(parts, GR, 2 + STAGES, ncl);
     auto fetch = [&](int k) {                             // turn k's tile, unless it lies behind the sequence
-        const int t = k * turn + tile, st = k % STAGES;
+        const int t = k * turn + tile, st = k / GR % STAGES;
         if (l.warp != 0 || k >= turns || t >= len) return;
         uint64_t* bar = &sm.bars[2 + st];
         const int lane = threadIdx.x & 31;
@@ -329,7 +376,7 @@ __global__ void __launch_bounds__(NT, V > 1 ? 2 : 3) scan_fwd_kernel(ScanParams 
         }
     };
 #pragma unroll
-    for (int k = 0; k < STAGES; ++k) fetch(k);
+    for (int j = 0; j < STAGES; ++j) fetch(grp + j * GR);
 
     int skew_g[V > 1 ? 1 : TileOf<GT, 1, L::TOK>::P], skew_x[V > 1 ? 1 : TileOf<XT, 1, L::TOK>::P];
     if constexpr (V == 1) {
@@ -337,15 +384,17 @@ __global__ void __launch_bounds__(NT, V > 1 ? 2 : 3) scan_fwd_kernel(ScanParams 
         skews(sm.g[0], p.g, p.g_row, c0, n0, skew_g);
         skews(sm.x[0], p.x, p.x_row, c0, n0, skew_x);
     }
-    float carry = 0.f;                                    // of warp 0: the state at the turn's start
-    if (threadIdx.x < CH && c0 + (int)threadIdx.x < p.D && p.h0) carry = p.h0[(size_t)b * p.D + c0 + threadIdx.x];
+    // of a group's warp 0: the state at the turn's start, of the lane's channel
+    const int lane_c = c0 + (int)(threadIdx.x & 31);
+    Carry<GR> carry{0.f, hand};
+    if (l.warp == 0 && lane_c < p.D && p.h0) carry.v = p.h0[(size_t)b * p.D + lane_c];
 
-    for (int k = 0; k < turns; ++k) {
+    for (int k = grp; k < turns; k += GR) {
         const int t0 = k * turn + first;
         float a[R][V], bb[R][V], A[V], H[V], exA[V], exH[V];
         if (k * turn + tile < len) {
-            const int st = k % STAGES;
-            if ((V > 1 || p.covered > 0) && !lost) lost = !wait_phase(&sm.bars[2 + st], (uint32_t)(k / STAGES) & 1u);
+            const int st = k / GR % STAGES;
+            if ((V > 1 || p.covered > 0) && !lost) lost = !wait_phase(&sm.bars[2 + st], (uint32_t)(k / GR / STAGES) & 1u);
             if constexpr (V > 1) {
 #pragma unroll
                 for (int r = 0; r < R; ++r) {
@@ -396,10 +445,10 @@ __global__ void __launch_bounds__(NT, V > 1 ? 2 : 3) scan_fwd_kernel(ScanParams 
 #pragma unroll
             for (int i = 0; i < V; ++i) sm.agg[l.warp][l.c + i] = make_float2(A[i], H[i]);
         }
-        __syncthreads();
-        fetch(k + STAGES);                                // the stage of turn k is in registers
-        if (l.warp == 0) warp_starts<true>(sm.agg, sm.xch, sm.bars, sm.start, carry, lost, k, rank, ncl);
-        __syncthreads();
+        group_sync<GR>(grp);
+        fetch(k + STAGES * GR);                           // the stage of turn k is in registers
+        if (l.warp == 0) warp_starts<true, GR>(sm.agg, xch, sm.bars, sm.start, carry, lost, k, turns, rank, ncl);
+        group_sync<GR>(grp);
         float s[V];
         run_start<V>(&sm.start[l.warp][l.c], exA, exH, s);
         if (on && p.ckpt && t0 % CKPT == 0 && t0 < p.T) {
@@ -433,8 +482,8 @@ __global__ void __launch_bounds__(NT, V > 1 ? 2 : 3) scan_fwd_kernel(ScanParams 
         }
     }
     if (ncl > 1) cluster_sync_relaxed();                  // no peer still sends here
-    if (p.h_T && rank == 0 && threadIdx.x < CH && c0 + (int)threadIdx.x < p.D)
-        p.h_T[(size_t)b * p.D + c0 + threadIdx.x] = carry;
+    if (p.h_T && rank == 0 && l.warp == 0 && grp == (turns - 1) % GR && lane_c < p.D)
+        p.h_T[(size_t)b * p.D + lane_c] = carry.v;
 }
 
 template <typename XT, typename GT, typename OT, int V> struct BwdSmem {
@@ -447,21 +496,23 @@ template <typename XT, typename GT, typename OT, int V> struct BwdSmem {
     float before[WT][CH];
     float start[WT][CH];
     uint64_t bars[2 + STAGES];
-    float2 xch[1][CH];
 };
 
 // The states inside a tile come from the checkpoint at its first token (a tile is a whole number of
 // CKPT tokens), so only the gradient's direction goes through the cluster.
-template <typename XT, typename GT, typename OT, int V>
-__global__ void __launch_bounds__(NT, 2) scan_bwd_kernel(ScanParams p, const __grid_constant__ ScanMaps maps) {
+template <typename XT, typename GT, typename OT, int V, int GR>
+__global__ void __launch_bounds__(NT * GR, GR > 1 ? 1 : 2) scan_bwd_kernel(ScanParams p, const __grid_constant__ ScanMaps maps) {
     using L = Tile<V, BWD_ELEMS>;
     using S = BwdSmem<XT, GT, OT, V>;
     constexpr int R = L::R;
     static_assert(L::TOK % CKPT == 0, "a tile starts at a checkpoint");
     extern __shared__ __align__(128) unsigned char raw[];
-    S& sm = *reinterpret_cast<S*>(raw);
     const L l;
-    const int rank = (int)cluster_rank(), ncl = (int)cluster_size();
+    const int rank = (int)cluster_rank(), ncl = (int)cluster_size(), grp = GR > 1 ? threadIdx.x / NT : 0;
+    S* const parts = reinterpret_cast<S*>(raw);
+    S& sm = parts[grp];
+    float (*const hand)[CH] = reinterpret_cast<float (*)[CH]>(parts + GR);
+    float2 (*const xch)[CH] = reinterpret_cast<float2 (*)[CH]>(reinterpret_cast<unsigned char*>(parts + GR) + HAND_BYTES) + grp * 2 * ncl;
     const int b = blockIdx.z, c0 = blockIdx.y * CH, c = c0 + l.c;
     const bool on = c < p.D;
     const int len = seq_len(p, b), nck = (p.T + CKPT - 1) / CKPT;
@@ -475,14 +526,15 @@ __global__ void __launch_bounds__(NT, 2) scan_bwd_kernel(ScanParams p, const __g
     const bool with_dh = p.dh != nullptr;
     bool lost = false;
 
-    barriers_begin(sm.bars, 2 + STAGES, ncl);
+    barriers_begin(parts, GR, 2 + STAGES, ncl);
     // turn k walks from the end: its tokens start at (turns - 1 - k) * turn.  Tiles behind the
     // sequence are not fetched, so the stages count the fetched ones, from turn `skip` on.
     const int live = (len - tile + turn - 1) / turn;      // turns of this block with tokens (len > tile), else <= 0
     const int skip = turns - max(live, 0);
+    const int from = skip + (GR > 1 ? (skip ^ grp) & 1 : 0);            // this group's first fetched turn
     auto fetch = [&](int k) {
         if (l.warp != 0 || k < skip || k >= turns) return;
-        const int t = (turns - 1 - k) * turn + tile, st = (k - skip) % STAGES, lane = threadIdx.x & 31;
+        const int t = (turns - 1 - k) * turn + tile, st = (k - from) / GR % STAGES, lane = threadIdx.x & 31;
         uint64_t* bar = &sm.bars[2 + st];
         const uint32_t bytes = sizeof(sm.g[0]) + sizeof(sm.x[0]) + (with_dh ? sizeof(sm.dh[0]) : 0);
         if constexpr (V > 1) {
@@ -501,7 +553,7 @@ __global__ void __launch_bounds__(NT, 2) scan_bwd_kernel(ScanParams p, const __g
         }
     };
 #pragma unroll
-    for (int k = 0; k < STAGES; ++k) fetch(skip + k);
+    for (int j = 0; j < STAGES; ++j) fetch(from + j * GR);
 
     int skew_g[V > 1 ? 1 : TileOf<GT, 1, L::TOK>::P], skew_x[V > 1 ? 1 : TileOf<XT, 1, L::TOK>::P],
         skew_d[V > 1 ? 1 : TileOf<OT, 1, L::TOK>::P];
@@ -511,16 +563,18 @@ __global__ void __launch_bounds__(NT, 2) scan_bwd_kernel(ScanParams p, const __g
         skews(sm.x[0], p.x, p.x_row, c0, n0, skew_x);
         skews(sm.dh[0], p.dh, p.D, c0, n0, skew_d);
     }
-    float carry = 0.f;                                    // of warp 0: a_{t+1} lam_{t+1} behind the turn
-    if (threadIdx.x < CH && c0 + (int)threadIdx.x < p.D && p.dh_T) carry = p.dh_T[(size_t)b * p.D + c0 + threadIdx.x];
+    // of a group's warp 0: a_{t+1} lam_{t+1} behind the turn
+    const int lane_c = c0 + (int)(threadIdx.x & 31);
+    Carry<GR> carry{0.f, hand};
+    if (l.warp == 0 && lane_c < p.D && p.dh_T) carry.v = p.dh_T[(size_t)b * p.D + lane_c];
 
-    for (int k = 0; k < turns; ++k) {
+    for (int k = grp; k < turns; k += GR) {
         const int base = (turns - 1 - k) * turn, t0 = base + first;
         // of warp 1: the state before the tile
-        float state = 0.f;
+        Carry<1> state{0.f, nullptr};
         if (l.warp == 1) {
-            const int j = (base + tile) / CKPT, ch = c0 + (threadIdx.x & 31);
-            if (j < nck && ch < p.D) state = p.ckpt[((size_t)b * nck + j) * p.D + ch];
+            const int j = (base + tile) / CKPT;
+            if (j < nck && lane_c < p.D) state.v = p.ckpt[((size_t)b * nck + j) * p.D + lane_c];
         }
         float a[R][V], rest[R][V], xv[R][V], d[R][V];
 #pragma unroll
@@ -528,8 +582,8 @@ __global__ void __launch_bounds__(NT, 2) scan_bwd_kernel(ScanParams p, const __g
 #pragma unroll
             for (int i = 0; i < V; ++i) d[r][i] = 0.f;
         if (k >= skip) {
-            const int st = (k - skip) % STAGES;
-            if ((V > 1 || p.covered > 0) && !lost) lost = !wait_phase(&sm.bars[2 + st], (uint32_t)((k - skip) / STAGES) & 1u);
+            const int st = (k - from) / GR % STAGES;
+            if ((V > 1 || p.covered > 0) && !lost) lost = !wait_phase(&sm.bars[2 + st], (uint32_t)((k - from) / GR / STAGES) & 1u);
             if constexpr (V > 1) {
 #pragma unroll
                 for (int r = 0; r < R; ++r) {
@@ -597,11 +651,11 @@ __global__ void __launch_bounds__(NT, 2) scan_bwd_kernel(ScanParams p, const __g
 #pragma unroll
             for (int i = 0; i < V; ++i) sm.down[l.warp][l.c + i] = make_float2(dA[i], M[i]);
         }
-        __syncthreads();
-        if (k >= skip) fetch(k + STAGES);                 // the stage of turn k is in registers
-        if (l.warp == 0) warp_starts<false>(sm.down, sm.xch, sm.bars, sm.start, carry, lost, k, rank, ncl);
-        else if (l.warp == 1) warp_starts<true>(sm.up, nullptr, nullptr, sm.before, state, lost, k, 0, 1);
-        __syncthreads();
+        group_sync<GR>(grp);
+        if (k >= skip) fetch(k + STAGES * GR);            // the stage of turn k is in registers
+        if (l.warp == 0) warp_starts<false, GR>(sm.down, xch, sm.bars, sm.start, carry, lost, k, turns, rank, ncl);
+        else if (l.warp == 1) warp_starts<true, 1>(sm.up, nullptr, nullptr, sm.before, state, lost, k, turns, 0, 1);
+        group_sync<GR>(grp);
         float s[V], m[V], before[R][V];
         run_start<V>(&sm.before[l.warp][l.c], exA, exH, s);
         run_start<V>(&sm.start[l.warp][l.c], exD, exM, m);
@@ -642,8 +696,8 @@ __global__ void __launch_bounds__(NT, 2) scan_bwd_kernel(ScanParams p, const __g
         });
     }
     if (ncl > 1) cluster_sync_relaxed();
-    if (p.dh0 && rank == 0 && threadIdx.x < CH && c0 + (int)threadIdx.x < p.D)
-        p.dh0[(size_t)b * p.D + c0 + threadIdx.x] = carry;
+    if (p.dh0 && rank == 0 && l.warp == 0 && grp == (turns - 1) % GR && lane_c < p.D)
+        p.dh0[(size_t)b * p.D + lane_c] = carry.v;
 }
 
 // One token per sequence: elementwise, V channels per thread.
