@@ -470,6 +470,8 @@ GDR_API gdr_status gdr_raven_fwd(const gdr_raven_desc* desc, const void* q, cons
  * lengths (device memory, int [B], 4-byte aligned, or NULL: all T): sequence b has min(max(lengths[b], 0), T)
  * tokens.  What lies behind them in x, g and dh is not read; h, dx and dg are written as zero
  * there, and h_T is the state after the last token (h0 for an empty sequence).
+ *
+ * Alignment: h, ckpt, dx and dg 16 bytes where they are written, all other pointers their elements'.
  */
 #define GDR_SCAN_CKPT 64
 typedef struct {
@@ -484,8 +486,7 @@ typedef struct {
 } gdr_scan_desc;
 
 /*
- * Forward.  x [B,T,D] x_dtype, g [B,T,D] g_dtype (rows x_row / g_row apart; these two pointers need
- * only their element's alignment);  h0 [B,D] fp32 or NULL (zero);  h [B,T,D] out_dtype (written);
+ * Forward.  x [B,T,D] x_dtype, g [B,T,D] g_dtype (rows x_row / g_row apart);  h0 [B,D] fp32 or NULL (zero);  h [B,T,D] out_dtype (written);
  * h_T [B,D] fp32 or NULL (may alias h0);  ckpt [B, ceil(T/64), D] fp32 or NULL: the states before
  * tokens 0, 64, 128, .. (the state after the last token where the sequence has ended), which
  * gdr_scan_bwd starts from.  One launch, no workspace.
@@ -517,7 +518,8 @@ GDR_API gdr_status gdr_scan_step(const gdr_scan_desc* desc, const void* x, const
  *
  *     y = (x - mean) * rstd * weight + bias,    rstd = 1 / sqrt(mean((x - mean)^2) + eps)
  *
- * Statistics and sums are fp32, the variance from the centred values.
+ * Statistics and sums are fp32, the variance from the centred values.  Pointers need their elements'
+ * alignment (rows that start on 16 bytes are read by 16-byte loads), the workspace 16 bytes.
  */
 typedef struct {
     long long rows;       /* >= 0 */
@@ -587,7 +589,7 @@ GDR_API gdr_status gdr_beam_select(const gdr_beam_desc* desc, const void* logits
  *     S[l, g, j] <- S[l, g, parent[g, j]]   (the values before the call)
  *
  * S is [L, G, K] states of state_bytes each (decode states [N,H,dv,dk] with N = G * K, Raven's
- * slots, the scan's h; any element type), parent [G,K] int (4-byte aligned).  Beams that keep their state are not
+ * slots, the scan's h; any element type and alignment), parent [G,K] int (4-byte aligned).  Beams that keep their state are not
  * moved.  A parent outside 0 .. K-1 leaves its beam as it is and sets the status word
  * (gdr_query_device_status -> GDR_ERR_INDEX).  One launch, no workspace.
  */

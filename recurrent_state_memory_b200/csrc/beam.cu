@@ -136,17 +136,17 @@ gdr_status gdr_state_reorder(const gdr_reorder_desc* d, void* S, const int* pare
     if ((long long)d->L * d->G > 65535) return fail(GDR_ERR_UNSUPPORTED, "L * G must be at most 65535%s");
     if (d->L == 0 || d->G == 0 || d->state_bytes == 0) return GDR_OK;
     if (!S || !parent) return fail(GDR_ERR_INVALID_ARG, "S and parent are required%s");
-    if (!aligned16(S) || !aligned4(parent))
-        return fail(GDR_ERR_INVALID_ARG, "S must be 16-byte and parent 4-byte aligned%s");
+    if (!aligned4(parent)) return fail(GDR_ERR_INVALID_ARG, "parent must be 4-byte aligned%s");
     bms::ReorderParams p = {};
     p.G = d->G; p.K = d->K; p.S = static_cast<char*>(S); p.parent = parent;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    const size_t n = d->state_bytes;        // every state starts at a multiple of it
-    if (n % 16 == 0 && d->K <= 16) return bms::launch_reorder<uint4>(d->L, p, n, st);
-    if (n % 8 == 0 && d->K <= 16) return bms::launch_reorder<uint2>(d->L, p, n, st);
-    if (n % 4 == 0) return bms::launch_reorder<unsigned int>(d->L, p, n, st);
-    if (n % 2 == 0) return bms::launch_reorder<unsigned short>(d->L, p, n, st);
-    return bms::launch_reorder<unsigned char>(d->L, p, n, st);
+    // the widest access that every state's start and size allow
+    const size_t n = d->state_bytes | (reinterpret_cast<uintptr_t>(S) & 15u);
+    if (n % 16 == 0 && d->K <= 16) return bms::launch_reorder<uint4>(d->L, p, d->state_bytes, st);
+    if (n % 8 == 0 && d->K <= 16) return bms::launch_reorder<uint2>(d->L, p, d->state_bytes, st);
+    if (n % 4 == 0) return bms::launch_reorder<unsigned int>(d->L, p, d->state_bytes, st);
+    if (n % 2 == 0) return bms::launch_reorder<unsigned short>(d->L, p, d->state_bytes, st);
+    return bms::launch_reorder<unsigned char>(d->L, p, d->state_bytes, st);
 }
 
 }  // extern "C"

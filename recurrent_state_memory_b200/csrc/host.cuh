@@ -30,6 +30,8 @@ inline bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3
 inline bool dtype_ok(gdr_dtype t) { return t == GDR_F32 || t == GDR_BF16; }
 inline size_t dtype_bytes(gdr_dtype t) { return t == GDR_BF16 ? 2 : 4; }
 
+inline bool aligned_to(const void* p, gdr_dtype t) { return reinterpret_cast<uintptr_t>(p) % dtype_bytes(t) == 0; }
+
 inline int device_sm_count() {
     int dev = 0, n = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) { cudaGetLastError(); return 148; }

@@ -86,7 +86,10 @@ static gdr_status launch_plan(const Plan& q, const NormParams& p, cudaStream_t s
 template <typename XT, typename YT>
 static gdr_status launch(const gdr_norm_desc* d, bool bwd, NormParams& p, cudaStream_t st) {
     constexpr int V = sizeof(XT) == 2 && sizeof(YT) == 2 ? 8 : 4;
-    const Plan q = plan_of(p.D, vector_of(d), bwd);
+    // one element a load where a tensor does not start on 16 bytes
+    bool on16 = true;
+    for (const void* a : {p.x, p.dy, p.weight, p.bias, (const void*)p.y, (const void*)p.dx}) on16 = on16 && aligned16(a);
+    const Plan q = plan_of(p.D, on16 ? vector_of(d) : 1, bwd);
     p.w_bf16 = d->w_dtype == GDR_BF16;
     gdr_status s = GDR_OK;
     if (p.rows > 0) {
@@ -170,8 +173,9 @@ gdr_status gdr_layernorm_fwd(const gdr_norm_desc* d, const void* x, const void* 
     t_detail[0] = 0;
     const gdr_status s = lnm::check_desc(d);
     if (s != GDR_OK) return s;
-    for (const void* q : {x, weight, bias, (const void*)y, (const void*)mean, (const void*)rstd})
-        if (q && !aligned16(q)) return fail(GDR_ERR_INVALID_ARG, "pointers must be 16-byte aligned%s");
+    if (!aligned_to(x, d->x_dtype) || !aligned_to(y, d->y_dtype) || !aligned_to(weight, d->w_dtype) ||
+        !aligned_to(bias, d->w_dtype) || !aligned4(mean) || !aligned4(rstd))
+        return fail(GDR_ERR_INVALID_ARG, "pointers must be aligned to their elements%s");
     if (d->rows == 0) return GDR_OK;
     if (!x || !y) return fail(GDR_ERR_INVALID_ARG, "x and y are required%s");
     lnm::NormParams p = {};
@@ -191,9 +195,10 @@ gdr_status gdr_layernorm_bwd(const gdr_norm_desc* d, const void* x, const void* 
     t_detail[0] = 0;
     const gdr_status s = lnm::check_desc(d);
     if (s != GDR_OK) return s;
-    for (const void* q : {x, dy, weight, (const void*)mean, (const void*)rstd, (const void*)dx, (const void*)dweight,
-                          (const void*)dbias, (const void*)workspace})
-        if (q && !aligned16(q)) return fail(GDR_ERR_INVALID_ARG, "pointers must be 16-byte aligned%s");
+    if (!aligned_to(x, d->x_dtype) || !aligned_to(dx, d->x_dtype) || !aligned_to(dy, d->y_dtype) ||
+        !aligned_to(weight, d->w_dtype) || !aligned4(mean) || !aligned4(rstd) || !aligned4(dweight) || !aligned4(dbias))
+        return fail(GDR_ERR_INVALID_ARG, "pointers must be aligned to their elements%s");
+    if (!aligned16(workspace)) return fail(GDR_ERR_INVALID_ARG, "workspace must be 16-byte aligned%s");
     if (!dx && !dweight && !dbias) return GDR_OK;
     if (d->rows > 0 && (!x || !dy || !mean || !rstd))
         return fail(GDR_ERR_INVALID_ARG, "x, dy, mean and rstd are required%s");

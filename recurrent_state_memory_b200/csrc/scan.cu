@@ -143,7 +143,8 @@ static gdr_status launch(Pass pass, ScanParams& p, cudaStream_t st) {
                (unsigned long long)p.T * row * el < (1ull << 40);
     };
     const bool vec = p.D % 4 == 0 && fits(p.x, p.x_row, sizeof(XT)) && fits(p.g, p.g_row, sizeof(GT)) &&
-                     (pass != BWD || fits(p.dh, p.D, sizeof(OT)));
+                     (pass != BWD || fits(p.dh, p.D, sizeof(OT))) &&
+                     (pass != STEP || (aligned16(p.h_T) && fits(p.h, p.D, sizeof(OT))));
     return vec ? launch_v<XT, GT, OT, 4>(pass, p, st) : launch_v<XT, GT, OT, 1>(pass, p, st);
 }
 
@@ -173,8 +174,6 @@ static gdr_status check_desc(const gdr_scan_desc* d) {
         return fail(GDR_ERR_UNSUPPORTED, "B must be at most 65535, T 2^30, D 4194240%s");
     return GDR_OK;
 }
-
-static bool aligned_to(const void* p, gdr_dtype t) { return reinterpret_cast<uintptr_t>(p) % dtype_bytes(t) == 0; }
 
 static ScanParams params(const gdr_scan_desc* d, const void* x, const void* g) {
     ScanParams p = {};
@@ -211,12 +210,12 @@ gdr_status gdr_scan_fwd(const gdr_scan_desc* d, const void* x, const void* g, co
     if (s != GDR_OK) return s;
     if (d->B == 0 || d->D == 0) return GDR_OK;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    for (const void* q : {(const void*)h0, (const void*)h, (const void*)h_T, (const void*)ckpt})
-        if (q && !aligned16(q)) return fail(GDR_ERR_INVALID_ARG, "pointers must be 16-byte aligned%s");
-    if (!aligned4(lengths)) return fail(GDR_ERR_INVALID_ARG, "lengths must be 4-byte aligned%s");
+    if (!aligned16(h) || !aligned16(ckpt)) return fail(GDR_ERR_INVALID_ARG, "h and ckpt must be 16-byte aligned%s");
+    if (!aligned4(lengths) || !aligned4(h0) || !aligned4(h_T))
+        return fail(GDR_ERR_INVALID_ARG, "lengths, h0 and h_T must be 4-byte aligned%s");
     if (d->T == 0) return scn::copy_state(h_T, h0, (size_t)d->B * d->D, st);
     if (!x || !g || !h) return fail(GDR_ERR_INVALID_ARG, "x, g and h are required%s");
-    if (!scn::aligned_to(x, d->x_dtype) || !scn::aligned_to(g, d->g_dtype))
+    if (!aligned_to(x, d->x_dtype) || !aligned_to(g, d->g_dtype))
         return fail(GDR_ERR_INVALID_ARG, "x and g must be aligned to their elements%s");
     scn::ScanParams p = scn::params(d, x, g);
     p.h0 = h0; p.lengths = lengths; p.h = h; p.h_T = h_T; p.ckpt = ckpt;
@@ -230,13 +229,12 @@ gdr_status gdr_scan_bwd(const gdr_scan_desc* d, const void* x, const void* g, co
     if (s != GDR_OK) return s;
     if (d->B == 0 || d->D == 0) return GDR_OK;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    for (const void* q : {(const void*)ckpt, dh, (const void*)dh_T, (const void*)dx,
-                          (const void*)dg, (const void*)dh0})
-        if (q && !aligned16(q)) return fail(GDR_ERR_INVALID_ARG, "pointers must be 16-byte aligned%s");
-    if (!aligned4(lengths)) return fail(GDR_ERR_INVALID_ARG, "lengths must be 4-byte aligned%s");
+    if (!aligned16(dx) || !aligned16(dg)) return fail(GDR_ERR_INVALID_ARG, "dx and dg must be 16-byte aligned%s");
+    if (!aligned4(lengths) || !aligned4(ckpt) || !aligned4(dh_T) || !aligned4(dh0) || !aligned_to(dh, d->out_dtype))
+        return fail(GDR_ERR_INVALID_ARG, "lengths, ckpt, dh, dh_T and dh0 must be aligned to their elements%s");
     if (d->T == 0) return scn::copy_state(dh0, dh_T, (size_t)d->B * d->D, st);
     if (!x || !g || !ckpt || !dx || !dg) return fail(GDR_ERR_INVALID_ARG, "x, g, ckpt, dx and dg are required%s");
-    if (!scn::aligned_to(x, d->x_dtype) || !scn::aligned_to(g, d->g_dtype))
+    if (!aligned_to(x, d->x_dtype) || !aligned_to(g, d->g_dtype))
         return fail(GDR_ERR_INVALID_ARG, "x and g must be aligned to their elements%s");
     scn::ScanParams p = scn::params(d, x, g);
     p.ckpt = const_cast<float*>(ckpt); p.lengths = lengths; p.dh = dh; p.dh_T = dh_T;
@@ -251,8 +249,9 @@ gdr_status gdr_scan_step(const gdr_scan_desc* d, const void* x, const void* g, f
     if (s != GDR_OK) return s;
     if (d->B == 0 || d->D == 0) return GDR_OK;
     if (!x || !g || !h) return fail(GDR_ERR_INVALID_ARG, "x, g and h are required%s");
-    if (!aligned16(h) || (o && !aligned16(o))) return fail(GDR_ERR_INVALID_ARG, "pointers must be 16-byte aligned%s");
-    if (!scn::aligned_to(x, d->x_dtype) || !scn::aligned_to(g, d->g_dtype))
+    if (!aligned4(h) || !aligned_to(o, d->out_dtype))
+        return fail(GDR_ERR_INVALID_ARG, "h and o must be aligned to their elements%s");
+    if (!aligned_to(x, d->x_dtype) || !aligned_to(g, d->g_dtype))
         return fail(GDR_ERR_INVALID_ARG, "x and g must be aligned to their elements%s");
     scn::ScanParams p = scn::params(d, x, g);
     p.h_T = h; p.h = o;

@@ -19,6 +19,7 @@ def G():
 P = ctypes.c_void_p(1 << 20)            # never dereferenced: every call below fails its checks first
 ODD = ctypes.c_void_p((1 << 20) + 1)
 HALF = ctypes.c_void_p((1 << 20) + 2)
+FOUR = ctypes.c_void_p((1 << 20) + 4)
 
 
 def test_exports(G):
@@ -51,14 +52,16 @@ def test_scan_refusals(G):
         assert call(desc(), g=HALF) == G.GDR_ERR_INVALID_ARG
         assert call(desc(B=0)) == G.GDR_OK and call(desc(D=0), x=None) == G.GDR_OK
     assert fwd(desc(), h=None) == G.GDR_ERR_INVALID_ARG
-    assert fwd(desc(), h0=HALF) == G.GDR_ERR_INVALID_ARG
+    assert fwd(desc(), h0=HALF) == G.GDR_ERR_INVALID_ARG and fwd(desc(), hT=HALF) == G.GDR_ERR_INVALID_ARG
+    assert fwd(desc(), h=FOUR) == G.GDR_ERR_INVALID_ARG and fwd(desc(), ck=FOUR) == G.GDR_ERR_INVALID_ARG
     assert fwd(desc(), n=HALF) == G.GDR_ERR_INVALID_ARG
     assert fwd(desc(T=0), x=None, g=None, h=None, h0=None, hT=None) == G.GDR_OK
     for missing in ("ck", "dx", "dg"):
         assert bwd(desc(), **{missing: None}) == G.GDR_ERR_INVALID_ARG
         assert bwd(desc(), **{missing: HALF}) == G.GDR_ERR_INVALID_ARG
     assert step(desc(), h=None) == G.GDR_ERR_INVALID_ARG
-    assert step(desc(), o=HALF) == G.GDR_ERR_INVALID_ARG
+    assert step(desc(), o=ODD) == G.GDR_ERR_INVALID_ARG and step(desc(), h=HALF) == G.GDR_ERR_INVALID_ARG
+    assert bwd(desc(), dh=ODD) == G.GDR_ERR_INVALID_ARG
 
 
 def test_layernorm_refusals(G):
@@ -80,13 +83,14 @@ def test_layernorm_refusals(G):
         assert call(desc(D=0)) == G.GDR_ERR_UNSUPPORTED and call(desc(D=(1 << 20) + 1)) == G.GDR_ERR_UNSUPPORTED
         assert call(desc(rows=(1 << 40) + 1)) == G.GDR_ERR_UNSUPPORTED
         assert call(desc(), x=None) == G.GDR_ERR_INVALID_ARG
-        assert call(desc(), x=HALF) == G.GDR_ERR_INVALID_ARG
+        assert call(desc(), x=ODD) == G.GDR_ERR_INVALID_ARG
     assert fwd(desc(), y=None) == G.GDR_ERR_INVALID_ARG and fwd(desc(), w=HALF) == G.GDR_ERR_INVALID_ARG
     assert bwd(desc(), dy=None) == G.GDR_ERR_INVALID_ARG and bwd(desc(), mean=None) == G.GDR_ERR_INVALID_ARG
     need = lambda d, w, b: L.gdr_layernorm_bwd_workspace_bytes(d, w, b)
     assert need(desc(), 0, 0) == 0 and need(desc(D=0), 1, 1) == 0
     assert need(desc(), 1, 1) == 2 * need(desc(), 1, 0) > 0
     assert bwd(desc(), ws=None) == G.GDR_ERR_WORKSPACE
+    assert bwd(desc(), ws=FOUR) == G.GDR_ERR_INVALID_ARG and bwd(desc(), mean=HALF) == G.GDR_ERR_INVALID_ARG
     assert bwd(desc(), n=need(desc(), 1, 1) - 1) == G.GDR_ERR_WORKSPACE
 
 
@@ -127,7 +131,7 @@ def test_reorder_refusals(G):
     assert call(k=0) == G.GDR_ERR_UNSUPPORTED and call(k=65) == G.GDR_ERR_UNSUPPORTED
     assert call(L_=300, g=300) == G.GDR_ERR_UNSUPPORTED
     assert call(S=None) == G.GDR_ERR_INVALID_ARG and call(p=None) == G.GDR_ERR_INVALID_ARG
-    assert call(S=HALF) == G.GDR_ERR_INVALID_ARG and call(p=HALF) == G.GDR_ERR_INVALID_ARG
+    assert call(p=HALF) == G.GDR_ERR_INVALID_ARG
     assert call(n=0) == G.GDR_OK and call(L_=0, S=None) == G.GDR_OK and call(g=0) == G.GDR_OK
 
 

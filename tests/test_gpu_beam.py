@@ -230,6 +230,16 @@ def test_reorder_of_one_byte_states_and_bad_parents(G):
     assert G.query_device_status() == G.GDR_OK
 
 
+def test_reorder_at_any_alignment(G):
+    import torch
+    for dt, at in ((torch.uint8, 3), (torch.bfloat16, 1), (torch.float32, 1), (torch.float32, 2)):
+        S = torch.randint(0, 100, (8 * 64 + at,), device="cuda").to(dt)[at:].view(8, 64)
+        p = torch.tensor([[3, 0, 0, 2], [1, 1, 2, 0]], dtype=torch.int32, device="cuda")
+        ref = O.state_reorder(S.float().cpu().numpy(), p.cpu().numpy())
+        G.state_reorder(S, p)
+        assert np.array_equal(S.float().cpu().numpy(), ref)
+
+
 def test_reorder_of_nothing(G):
     import torch
     G.state_reorder(torch.empty((0, 5), device="cuda"), torch.empty((0, 4), dtype=torch.int32, device="cuda"))

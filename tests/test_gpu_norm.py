@@ -111,6 +111,24 @@ def test_optional_weights(G, weight, bias, D):
     _check(G, 40, D, weight=weight, bias=bias)
 
 
+@pytest.mark.parametrize("x", ["bf16", "f32"])
+def test_tensors_that_start_on_no_16_bytes(G, x):
+    """Contiguous slices of larger tensors: the results are those of copies (other loads, the same
+    order of sums within a row up to the lanes' split, so within the tests' bounds of each other)."""
+    import torch
+    gen = torch.Generator("cuda").manual_seed(3)
+    flat = torch.randn(2 * 40 * 96 + 2, generator=gen, device="cuda").to(_dt(x))
+    a, dy = flat[1:1 + 40 * 96].view(40, 96), flat[2 + 40 * 96:].view(40, 96)
+    w = torch.randn(97, generator=gen, device="cuda")[1:]
+    y, m, r = G.layernorm_fwd(a, w)
+    d = G.layernorm_bwd(a, dy, m, r, w)
+    y2, m2, r2 = G.layernorm_fwd(a.clone(), w.clone())
+    d2 = G.layernorm_bwd(a.clone(), dy.clone(), m2, r2, w.clone())
+    for got, ref in ((y, y2), (m, m2), (r, r2), (d["x"], d2["x"]), (d["weight"], d2["weight"]), (d["bias"], d2["bias"])):
+        scale = ref.double().abs().max()
+        assert (got.double() - ref.double()).abs().max() <= (2.0 ** -7 if got.dtype == torch.bfloat16 else 200 * U) * scale
+
+
 def test_rows_far_from_zero(G):
     """A row's offset is a hundred times its spread: the variance comes from the centred values."""
     _check(G, 30, 512, x="f32", offset=100.0)

@@ -171,6 +171,25 @@ def test_slices_of_a_projection(G, D):
     _check(G, Case(2, 200, D, x="bf16", g="bf16", slices=True))
 
 
+@pytest.mark.parametrize("D", [64, 30])
+def test_tensors_that_start_on_no_16_bytes(G, D):
+    """Contiguous x, g, dh, h0 and step states at odd places of larger tensors."""
+    import torch
+    c = Case(2, 150, D)
+
+    def moved(v):
+        flat = torch.empty(v.numel() + 1, dtype=v.dtype, device="cuda")
+        flat[1:] = v.reshape(-1)
+        return flat[1:].view(v.shape)
+
+    c.x, c.g, c.dh, c.h0, c.dhT = map(moved, (c.x, c.g, c.dh, c.h0, c.dhT))
+    assert c.x.data_ptr() % 4 and c.x.is_contiguous()
+    _check(G, c)
+    s, ref = moved(c.h0), c.h0.clone()
+    o = G.scan_step(c.x[:, 0], c.g[:, 0], s)
+    assert torch.equal(o, G.scan_step(c.x[:, 0].contiguous(), c.g[:, 0].contiguous(), ref)) and torch.equal(s, ref)
+
+
 @pytest.mark.parametrize("gate_mode,gates", [(1, [-np.inf, np.inf, 90.0, -90.0, 200.0, 0.0, -17.0]),
                                              (0, [-np.inf, 0.0, -1e-9, -100.0, -1e30, -0.5])])
 @pytest.mark.parametrize("tied", [False, True])
