@@ -547,8 +547,13 @@ __global__ void __launch_bounds__(SUM_NT) norm_sum_kernel(NormParams p) {
     asm volatile("griddepcontrol.wait;" ::: "memory");  // launched ahead of the partial rows' end
     float s = 0.f;
     if (c < p.D) {
-#pragma unroll 4
-        for (int i = warp; i < p.parts; i += 32) s += from[(size_t)i * p.D + c];
+        for (int i0 = warp; i0 < p.parts; i0 += 32 * 10) {     // ten loads at once: 296 partial rows in one turn
+            float v[10];
+#pragma unroll
+            for (int u = 0; u < 10; ++u) v[u] = i0 + 32 * u < p.parts ? from[(size_t)(i0 + 32 * u) * p.D + c] : 0.f;
+#pragma unroll
+            for (int u = 0; u < 10; ++u) s += v[u];
+        }
     }
     sm[warp][lane] = s;
     __syncthreads();
