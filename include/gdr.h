@@ -465,7 +465,8 @@ GDR_API gdr_status gdr_raven_fwd(const gdr_raven_desc* desc, const void* q, cons
  * with the decay a_t from the gate g_t by the library's gate modes (GDR_GATE_LOGDECAY: exp(g),
  * GDR_GATE_NEG_SOFTPLUS: exp(-softplus(g)) = sigmoid(-g)) and w_t = 1, or w_t = 1 - a_t with
  * tied = 1 (a moving average of x).  States, decays and sums are fp32; h, dx and dg are rounded
- * once, when they are stored.  Every result is the same from run to run.
+ * once, when they are stored.  Every result is the same from run to run.  Decays are expected at or
+ * below one (log-decays g <= 0); the products of larger ones over some hundred tokens must not overflow.
  *
  * lengths (device memory, int [B], 4-byte aligned, or NULL: all T): sequence b has min(max(lengths[b], 0), T)
  * tokens.  What lies behind them in x, g and dh is not read; h, dx and dg are written as zero
@@ -475,7 +476,7 @@ GDR_API gdr_status gdr_raven_fwd(const gdr_raven_desc* desc, const void* q, cons
  */
 #define GDR_SCAN_CKPT 64
 typedef struct {
-    int B, T, D;          /* sequences, tokens (T >= 0), channels */
+    int B, T, D;          /* sequences (at most 2^26), tokens (0 .. 2^30), channels (at most 2097120) */
     long long x_row;      /* elements from one token of x to the next (>= D; 0: D); a sequence is   */
     long long g_row;      /*   T rows, so x may be a slice of a wider [B,T,..] tensor; same for g   */
     gdr_dtype x_dtype;    /* x and dx */
@@ -566,7 +567,8 @@ GDR_API gdr_status gdr_layernorm_bwd(const gdr_norm_desc* desc, const void* x, c
  * closer than that allows, the beams' sums are formed again in 64 bits before they are ordered.
  */
 typedef struct {
-    int G, K, V, M;       /* groups, beams (1..64), vocabulary, candidates out (1..64, <= K * V); K * V < 2^31 */
+    int G, K, V, M;       /* groups, beams (1..64), vocabulary, candidates out (1..64, <= K * V); K * V < 2^31,
+                             G * K < 2^31, V at most 134215680 */
     long long row;        /* elements from one beam's logits to the next (>= V; 0: V) */
     gdr_dtype x_dtype;    /* logits */
     int eos;              /* 0 .. V - 1; read only with `finished` */
@@ -594,7 +596,7 @@ GDR_API gdr_status gdr_beam_select(const gdr_beam_desc* desc, const void* logits
  * (gdr_query_device_status -> GDR_ERR_INDEX).  One launch, no workspace.
  */
 typedef struct {
-    int L, G, K;          /* layers, groups, beams per group (1..64) */
+    int L, G, K;          /* layers, groups (L * G < 2^31), beams per group (1..64) */
     size_t state_bytes;   /* bytes of one beam's state in one layer */
 } gdr_reorder_desc;
 

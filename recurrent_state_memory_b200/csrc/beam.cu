@@ -34,7 +34,7 @@ static size_t workspace_of(const gdr_beam_desc* d, BeamParams* p, void* base) {
 
 template <typename XT>
 static gdr_status launch_select(const BeamParams& p, cudaStream_t st) {
-    const dim3 grid(p.pieces, p.G * p.K);
+    const dim3 grid(p.G * p.K, p.pieces);
     // 16-byte loads where every row starts on them
     const bool vec = reinterpret_cast<uintptr_t>(p.logits) % 16 == 0 && p.row * sizeof(XT) % 16 == 0;
     if (p.piece == 8192) {
@@ -67,7 +67,8 @@ static gdr_status check_desc(const gdr_beam_desc* d) {
     if (d->V < 1) return fail(GDR_ERR_INVALID_ARG, "V must be >= 1%s");
     const long long n = (long long)d->K * d->V;
     if (n > 0x7fffffffLL) return fail(GDR_ERR_UNSUPPORTED, "K * V must be below 2^31%s");
-    if ((long long)d->G * d->K > 65535) return fail(GDR_ERR_UNSUPPORTED, "G * K must be at most 65535%s");
+    if ((long long)d->G * d->K > 0x7fffffffLL) return fail(GDR_ERR_UNSUPPORTED, "G * K must be below 2^31%s");
+    if (d->V > 65535 * 2048) return fail(GDR_ERR_UNSUPPORTED, "V must be at most 134215680%s");
     if (d->M > n) return fail(GDR_ERR_INVALID_ARG, "M must be at most K * V%s");
     if (d->row != 0 && d->row < d->V) return fail(GDR_ERR_INVALID_ARG, "row must be 0 or at least V%s");
     if (!dtype_ok(d->x_dtype)) return fail(GDR_ERR_INVALID_ARG, "bad dtype%s");
@@ -78,7 +79,7 @@ template <typename VT>
 static gdr_status launch_reorder(int L, ReorderParams p, size_t bytes, cudaStream_t st) {
     p.n = bytes / sizeof(VT);
     const size_t blocks = (p.n + NT - 1) / NT;
-    const dim3 grid((unsigned)(blocks < 1024 ? blocks : 1024), (unsigned)((long long)L * p.G));
+    const dim3 grid((unsigned)((long long)L * p.G), (unsigned)(blocks < 1024 ? blocks : 1024));
     if (p.K <= 4) reorder_kernel<VT, 4><<<grid, NT, 0, st>>>(p);
     else if (p.K <= 8) reorder_kernel<VT, 8><<<grid, NT, 0, st>>>(p);
     else if (p.K <= 16) reorder_kernel<VT, 16><<<grid, NT, 0, st>>>(p);
@@ -133,7 +134,7 @@ gdr_status gdr_state_reorder(const gdr_reorder_desc* d, void* S, const int* pare
     if (!d) return fail(GDR_ERR_INVALID_ARG, "desc is NULL%s");
     if (d->L < 0 || d->G < 0) return fail(GDR_ERR_INVALID_ARG, "L and G must be >= 0%s");
     if (d->K < 1 || d->K > 64) return fail(GDR_ERR_UNSUPPORTED, "K must be 1 .. 64%s");
-    if ((long long)d->L * d->G > 65535) return fail(GDR_ERR_UNSUPPORTED, "L * G must be at most 65535%s");
+    if ((long long)d->L * d->G > 0x7fffffffLL) return fail(GDR_ERR_UNSUPPORTED, "L * G must be below 2^31%s");
     if (d->L == 0 || d->G == 0 || d->state_bytes == 0) return GDR_OK;
     if (!S || !parent) return fail(GDR_ERR_INVALID_ARG, "S and parent are required%s");
     if (!aligned4(parent)) return fail(GDR_ERR_INVALID_ARG, "parent must be 4-byte aligned%s");

@@ -149,7 +149,7 @@ __global__ void __launch_bounds__(NT, E > 8 && sizeof(XT) == 4 ? 4 : 6) beam_row
     __shared__ int count;
     __shared__ unsigned long long pick[WARPS];
     __shared__ unsigned long long list[LIST];       // key, then the token's complement: larger is better
-    const int row = blockIdx.y, piece = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int row = blockIdx.x, piece = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     asm volatile("griddepcontrol.launch_dependents;");               // the groups' blocks may come; they wait
     const int v0 = piece * p.piece, n = min(p.piece, p.V - v0);      // this block's tokens
     const XT* x = static_cast<const XT*>(p.logits) + (size_t)row * p.row + v0;
@@ -503,14 +503,14 @@ struct ReorderParams {
 // over, and only then writes, so that the exchange needs no second buffer and no other thread.
 template <typename VT, int KMAX>
 __global__ void __launch_bounds__(NT) reorder_kernel(ReorderParams p) {
-    const int g = blockIdx.y % p.G;
+    const int g = blockIdx.x % p.G;
     const int* parent = p.parent + (size_t)g * p.K;
-    VT* S = reinterpret_cast<VT*>(p.S) + (size_t)blockIdx.y * p.K * p.n;
-    if (blockIdx.x == 0 && blockIdx.y < p.G && threadIdx.x < p.K) {
+    VT* S = reinterpret_cast<VT*>(p.S) + (size_t)blockIdx.x * p.K * p.n;
+    if (blockIdx.y == 0 && blockIdx.x < p.G && threadIdx.x < p.K) {
         const int q = parent[threadIdx.x];
         if (q < 0 || q >= p.K) atomicOr(&g_device_status, STATUS_INDEX);
     }
-    for (size_t i = (size_t)blockIdx.x * NT + threadIdx.x; i < p.n; i += (size_t)gridDim.x * NT) {
+    for (size_t i = (size_t)blockIdx.y * NT + threadIdx.x; i < p.n; i += (size_t)gridDim.y * NT) {
         VT v[KMAX];
         bool moves[KMAX];
 #pragma unroll

@@ -33,7 +33,7 @@ static gdr_status launch_clusters(KERN kern, const ScanParams& p, const ScanMaps
     if (e == cudaSuccess && sp.cluster > 8) e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(scan)");
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(sp.cluster, ct, p.B);
+    cfg.gridDim = dim3((unsigned)(sp.cluster * p.B), ct);        // a sequence's cluster, 32 channels
     cfg.blockDim = dim3(NT * sp.groups);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
@@ -170,8 +170,15 @@ static gdr_status check_desc(const gdr_scan_desc* d) {
     if (d->tied != 0 && d->tied != 1) return fail(GDR_ERR_INVALID_ARG, "tied must be 0 or 1%s");
     if ((d->x_row != 0 && d->x_row < d->D) || (d->g_row != 0 && d->g_row < d->D))
         return fail(GDR_ERR_INVALID_ARG, "x_row and g_row must be 0 or at least D%s");
-    if (d->B > 65535 || d->T > (1 << 30) || d->D > 65535 * CH)
-        return fail(GDR_ERR_UNSUPPORTED, "B must be at most 65535, T 2^30, D 4194240%s");
+    return GDR_OK;
+}
+
+// What the grid and the tokens' 32-bit arithmetic of whole sequences hold.
+static gdr_status check_sequences(const gdr_scan_desc* d) {
+    const gdr_status s = check_desc(d);
+    if (s != GDR_OK) return s;
+    if (d->B > (1 << 26) || d->T > (1 << 30) || d->D > 65535 * CH)
+        return fail(GDR_ERR_UNSUPPORTED, "B must be at most 2^26, T 2^30, D 2097120%s");
     return GDR_OK;
 }
 
@@ -206,7 +213,7 @@ extern "C" {
 gdr_status gdr_scan_fwd(const gdr_scan_desc* d, const void* x, const void* g, const float* h0, const int* lengths,
                         void* h, float* h_T, float* ckpt, gdr_stream_t stream) {
     t_detail[0] = 0;
-    const gdr_status s = scn::check_desc(d);
+    const gdr_status s = scn::check_sequences(d);
     if (s != GDR_OK) return s;
     if (d->B == 0 || d->D == 0) return GDR_OK;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
@@ -225,7 +232,7 @@ gdr_status gdr_scan_fwd(const gdr_scan_desc* d, const void* x, const void* g, co
 gdr_status gdr_scan_bwd(const gdr_scan_desc* d, const void* x, const void* g, const float* ckpt, const int* lengths,
                         const void* dh, const float* dh_T, void* dx, void* dg, float* dh0, gdr_stream_t stream) {
     t_detail[0] = 0;
-    const gdr_status s = scn::check_desc(d);
+    const gdr_status s = scn::check_sequences(d);
     if (s != GDR_OK) return s;
     if (d->B == 0 || d->D == 0) return GDR_OK;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);

@@ -346,7 +346,7 @@ __global__ void __launch_bounds__(NT * GR, GR > 1 ? 1 : V > 1 ? 2 : 3) scan_fwd_
     S& sm = parts[grp];
     float (*const hand)[CH] = reinterpret_cast<float (*)[CH]>(parts + GR);
     float2 (*const xch)[CH] = reinterpret_cast<float2 (*)[CH]>(reinterpret_cast<unsigned char*>(parts + GR) + HAND_BYTES) + grp * 2 * ncl;
-    const int b = blockIdx.z, c0 = blockIdx.y * CH, c = c0 + l.c;
+    const int b = blockIdx.x / ncl, c0 = blockIdx.y * CH, c = c0 + l.c;
     const bool on = c < p.D;                              // V divides D, or V = 1
     const int len = seq_len(p, b), nck = (p.T + CKPT - 1) / CKPT;
     const XT* x = static_cast<const XT*>(p.x) + (size_t)b * p.T * p.x_row + c;
@@ -513,7 +513,7 @@ __global__ void __launch_bounds__(NT * GR, GR > 1 ? 1 : 2) scan_bwd_kernel(ScanP
     S& sm = parts[grp];
     float (*const hand)[CH] = reinterpret_cast<float (*)[CH]>(parts + GR);
     float2 (*const xch)[CH] = reinterpret_cast<float2 (*)[CH]>(reinterpret_cast<unsigned char*>(parts + GR) + HAND_BYTES) + grp * 2 * ncl;
-    const int b = blockIdx.z, c0 = blockIdx.y * CH, c = c0 + l.c;
+    const int b = blockIdx.x / ncl, c0 = blockIdx.y * CH, c = c0 + l.c;
     const bool on = c < p.D;
     const int len = seq_len(p, b), nck = (p.T + CKPT - 1) / CKPT;
     const XT* x = static_cast<const XT*>(p.x) + (size_t)b * p.T * p.x_row + c;

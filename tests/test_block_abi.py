@@ -59,6 +59,8 @@ def test_scan_refusals(G):
     for missing in ("ck", "dx", "dg"):
         assert bwd(desc(), **{missing: None}) == G.GDR_ERR_INVALID_ARG
         assert bwd(desc(), **{missing: HALF}) == G.GDR_ERR_INVALID_ARG
+    for bad in (dict(B=1 << 27), dict(T=(1 << 30) + 1), dict(D=65535 * 32 + 1)):
+        assert fwd(desc(**bad)) == G.GDR_ERR_UNSUPPORTED and bwd(desc(**bad)) == G.GDR_ERR_UNSUPPORTED
     assert step(desc(), h=None) == G.GDR_ERR_INVALID_ARG
     assert step(desc(), o=ODD) == G.GDR_ERR_INVALID_ARG and step(desc(), h=HALF) == G.GDR_ERR_INVALID_ARG
     assert bwd(desc(), dh=ODD) == G.GDR_ERR_INVALID_ARG
@@ -109,7 +111,8 @@ def test_beam_refusals(G):
     assert call(None) == G.GDR_ERR_INVALID_ARG
     for bad in (dict(G=-1), dict(V=0), dict(row=99), dict(x_dtype=5), dict(V=2, K=3, M=7)):
         assert call(desc(**bad)) == G.GDR_ERR_INVALID_ARG, bad
-    for bad in (dict(K=0), dict(K=65), dict(M=0), dict(M=65), dict(V=1 << 29), dict(G=1 << 30)):
+    for bad in (dict(K=0), dict(K=65), dict(M=0), dict(M=65), dict(V=1 << 29), dict(K=1, V=(1 << 27)),
+                dict(G=1 << 30)):
         assert call(desc(**bad)) == G.GDR_ERR_UNSUPPORTED, bad
         assert L.gdr_beam_select_workspace_bytes(desc(**bad)) == 0
     for eos in (-1, 100):
@@ -129,7 +132,7 @@ def test_reorder_refusals(G):
     assert L.gdr_state_reorder(None, P, P, None) == G.GDR_ERR_INVALID_ARG
     assert call(L_=-1) == G.GDR_ERR_INVALID_ARG and call(g=-1) == G.GDR_ERR_INVALID_ARG
     assert call(k=0) == G.GDR_ERR_UNSUPPORTED and call(k=65) == G.GDR_ERR_UNSUPPORTED
-    assert call(L_=300, g=300) == G.GDR_ERR_UNSUPPORTED
+    assert call(L_=1 << 16, g=1 << 16) == G.GDR_ERR_UNSUPPORTED
     assert call(S=None) == G.GDR_ERR_INVALID_ARG and call(p=None) == G.GDR_ERR_INVALID_ARG
     assert call(p=HALF) == G.GDR_ERR_INVALID_ARG
     assert call(n=0) == G.GDR_OK and call(L_=0, S=None) == G.GDR_OK and call(g=0) == G.GDR_OK

@@ -187,6 +187,19 @@ def test_selection_twice_on_a_stream_and_in_graphs(G):
         assert all(torch.equal(x, y) for x, y in zip(f, h))
 
 
+def test_very_many_groups(G):
+    """More beams than a grid's second dimension holds; every group by the definition's top-1."""
+    import torch
+    z, s = _make(40000, 2, 40, "bf16", seed=11, banned=0)
+    sc, p, t = G.beam_select(z, s, 1)
+    c = (z.double().log_softmax(2) + s.double()[..., None]).view(40000, 80)
+    top = c.topk(2, dim=1)
+    at = p[:, 0].long() * 40 + t[:, 0].long()
+    assert torch.equal(c.gather(1, at[:, None]), top.values[:, :1])
+    clear = top.values[:, 0] > top.values[:, 1]
+    assert torch.equal(at[clear], top.indices[:, 0][clear])
+
+
 # ---------------------------------------------------------------- reorder ----
 
 
@@ -228,6 +241,16 @@ def test_reorder_of_one_byte_states_and_bad_parents(G):
     assert np.array_equal(S.cpu().numpy(), ref)
     assert G.query_device_status() == G.GDR_ERR_INDEX
     assert G.query_device_status() == G.GDR_OK
+
+
+def test_reorder_of_very_many_groups(G):
+    import torch
+    S = torch.randn(3, 140000, 5, device="cuda")
+    p = torch.randint(0, 2, (70000, 2), device="cuda", dtype=torch.int32)
+    at = (torch.arange(70000, device="cuda")[:, None] * 2 + p).view(-1)
+    ref = S[:, at]
+    G.state_reorder(S, p, layers=True)
+    assert torch.equal(S, ref)
 
 
 def test_reorder_at_any_alignment(G):

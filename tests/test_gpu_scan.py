@@ -265,6 +265,21 @@ def test_step_equals_the_forward(G, N, D, tied, gt):
     _near(s, last, err[:, -1], U)
 
 
+def test_very_many_sequences(G):
+    """More sequences than a grid's third dimension holds: the same as in two halves."""
+    import torch
+    gen = torch.Generator("cuda").manual_seed(9)
+    x, g = torch.randn(2, 70001, 3, 5, generator=gen, device="cuda")
+    h, hT, ck = G.scan_fwd(x, g, want_ckpt=True)
+    a, b = G.scan_fwd(x[:35000], g[:35000]), G.scan_fwd(x[35000:], g[35000:])
+    assert torch.equal(h, torch.cat([a[0], b[0]])) and torch.equal(hT, torch.cat([a[1], b[1]]))
+    d = G.scan_bwd(x, g, ck, h)
+    e = G.scan_bwd(x[35000:], g[35000:], ck[35000:], h[35000:])
+    assert torch.equal(d["x"][35000:], e["x"]) and torch.equal(d["g"][35000:], e["g"])
+    s, o = hT.clone(), G.scan_step(x[:, 0], g[:, 0], hT)
+    assert torch.equal(o, G.scan_fwd(x[:, :1].contiguous(), g[:, :1].contiguous(), s)[0][:, 0])
+
+
 def test_no_tokens_no_sequences(G):
     import torch
     x = torch.empty((3, 0, 8), device="cuda")
