@@ -100,20 +100,22 @@ template <int V> __device__ __forceinline__ Vals<V> fma(const Vals<V>& a, const 
 template <typename T, int V> struct Raw {
     static constexpr int BYTES = V * (int)sizeof(T), WORDS = BYTES < 4 ? 1 : BYTES / 4;
     unsigned w[WORDS];
-    __device__ __forceinline__ void load(const T* p) {
+    // ONCE: streamed (evicted first), for rows that are read once: 2 to 8 % of the kernels' time.
+    template <bool ONCE = true> __device__ __forceinline__ void load(const T* p) {
+        auto get = [](const auto* q) { return ONCE ? __ldcs(q) : *q; };
         if constexpr (BYTES == 32) {
-            const uint4 a = reinterpret_cast<const uint4*>(p)[0], b = reinterpret_cast<const uint4*>(p)[1];
+            const uint4 a = get(reinterpret_cast<const uint4*>(p)), b = get(reinterpret_cast<const uint4*>(p) + 1);
             w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w; w[4] = b.x; w[5] = b.y; w[6] = b.z; w[7] = b.w;
         } else if constexpr (BYTES == 16) {
-            const uint4 a = *reinterpret_cast<const uint4*>(p);
+            const uint4 a = get(reinterpret_cast<const uint4*>(p));
             w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
         } else if constexpr (BYTES == 8) {
-            const uint2 a = *reinterpret_cast<const uint2*>(p);
+            const uint2 a = get(reinterpret_cast<const uint2*>(p));
             w[0] = a.x; w[1] = a.y;
         } else if constexpr (BYTES == 4) {
-            w[0] = *reinterpret_cast<const unsigned*>(p);
+            w[0] = get(reinterpret_cast<const unsigned*>(p));
         } else {
-            w[0] = *reinterpret_cast<const unsigned short*>(p);
+            w[0] = get(reinterpret_cast<const unsigned short*>(p));
         }
     }
     __device__ __forceinline__ void zero() {
@@ -137,7 +139,7 @@ template <typename T, int V> struct Raw {
 // V weights or biases from column c on.
 template <typename WT, int V> __device__ __forceinline__ Vals<V> load_w(const void* p, int c) {
     Raw<WT, V> r;
-    r.load(static_cast<const WT*>(p) + c);
+    r.template load<false>(static_cast<const WT*>(p) + c);
     return r.vals();
 }
 // f(a value of the weights' type): the branch is taken once, not once a load.
