@@ -56,7 +56,7 @@ def build_binding(force: bool = False) -> str:
     for p in paths:
         cmd += ["-isystem", p]
     cmd += [f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", src, "-o", tmp, "-L", libs,
-            "-ltorch", "-ltorch_cpu", "-ltorch_python", "-lc10", "-lc10_cuda", "-ldl"]
+            "-ltorch", "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python", "-lc10", "-lc10_cuda", "-ldl"]
     subprocess.run(cmd, check=True)
     os.replace(tmp, BINDING)
     return BINDING

@@ -4,6 +4,7 @@
 // long as a handful of Python statements; the same steps in Python cost 8 to 17 us a call.
 #include <dlfcn.h>
 
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Dtype.h>
@@ -109,7 +110,7 @@ struct Call {
 };
 
 Tensor make(at::IntArrayRef shape, at::ScalarType type, at::Device dev) {
-    return at::empty(shape, at::TensorOptions().dtype(type).device(dev));
+    return at::detail::empty_cuda(shape, type, dev, std::nullopt);
 }
 template <typename T = void> T* at_(const MaybeTensor& t) { return t ? static_cast<T*>(t->data_ptr()) : nullptr; }
 template <typename T = void> T* at_(const Tensor& t) { return static_cast<T*>(t.data_ptr()); }

@@ -227,9 +227,9 @@ def kernel_launches(desc: FwdDesc) -> int:
 def use_library(path: str) -> None:
     """Load the library from `path` from now on (the debug build with index checks,
     libgdr_debug.so, for example); the next call loads it."""
-    global LIB_PATH, _lib
+    global LIB_PATH, _lib, _binding
     LIB_PATH = path
-    _lib = None
+    _lib = _binding = None
 
 
 def debug_bounds_site() -> int:
@@ -504,7 +504,7 @@ _binding = None
 def _ops():
     """The native binding, calling the library that lib() has loaded."""
     global _binding
-    if _lib is None or _binding is None:
+    if _binding is None:
         lib()
         if not os.path.exists(BINDING_PATH):
             raise RuntimeError(f"{BINDING_PATH} is missing: build it with "
@@ -530,7 +530,7 @@ def scan_fwd(x, g, h0=None, *, gate_mode=GATE_NEG_SOFTPLUS, tied=False, lengths=
     lengths [B] int32 or None: tokens of each sequence (h is zero behind them).  Returns
     (h [B,T,D], h_T [B,D] fp32), or (h, h_T, ckpt) with want_ckpt: the states that ``scan_bwd``
     starts from.  h_T is None unless want_state."""
-    return _ops().scan_fwd(x, g, h0, gate_mode, tied, lengths, out_dtype, want_state, want_ckpt, stream)
+    return (_binding or _ops()).scan_fwd(x, g, h0, gate_mode, tied, lengths, out_dtype, want_state, want_ckpt, stream)
 
 
 def scan_bwd(x, g, ckpt, dh=None, dh_T=None, *, gate_mode=GATE_NEG_SOFTPLUS, tied=False, lengths=None,
@@ -538,13 +538,13 @@ def scan_bwd(x, g, ckpt, dh=None, dh_T=None, *, gate_mode=GATE_NEG_SOFTPLUS, tie
     """Backward of ``scan_fwd``: the gradients of x, g and h0 given ckpt (from the forward of the same
     inputs), dh [B,T,D] (like h) and dh_T [B,D] fp32; either may be None (zero).  Returns a dict
     "x" (x's dtype), "g" (g's dtype), "h0" (fp32; None unless want_dh0)."""
-    return _ops().scan_bwd(x, g, ckpt, dh, dh_T, gate_mode, tied, lengths, want_dh0, stream)
+    return (_binding or _ops()).scan_bwd(x, g, ckpt, dh, dh_T, gate_mode, tied, lengths, want_dh0, stream)
 
 
 def scan_step(x, g, h, *, gate_mode=GATE_NEG_SOFTPLUS, tied=False, out_dtype=None, o=None, stream=None):
     """One token of ``scan_fwd`` for N sequences: x, g [N,D]; h [N,D] fp32 is updated in place.
     Returns o [N,D], the new state in out_dtype (default: x's)."""
-    return _ops().scan_step(x, g, h, gate_mode, tied, out_dtype, o, stream)
+    return (_binding or _ops()).scan_step(x, g, h, gate_mode, tied, out_dtype, o, stream)
 
 
 def norm_desc(rows, D, x_dtype, y_dtype, w_dtype=torch.float32, eps=1e-5) -> NormDesc:
@@ -555,14 +555,14 @@ def layernorm_fwd(x, weight=None, bias=None, *, eps=1e-5, out_dtype=None, want_s
     """Layer norm over the last dimension (``gdr_layernorm_fwd``): x [..., D] bf16 or fp32, weight and
     bias [D] (one dtype) or None.  Returns (y [..., D] out_dtype, mean [...], rstd [...] fp32); the
     statistics are None unless want_stats."""
-    return _ops().layernorm_fwd(x, weight, bias, eps, out_dtype, want_stats, stream)
+    return (_binding or _ops()).layernorm_fwd(x, weight, bias, eps, out_dtype, want_stats, stream)
 
 
 def layernorm_bwd(x, dy, mean, rstd, weight=None, *, with_bias=True, want_dx=True, workspace=None, stream=None):
     """Backward of ``layernorm_fwd`` given dy (like y) and the forward's mean and rstd.  Returns a dict
     "x" (x's dtype; None unless want_dx), "weight" (fp32; None without weight) and "bias" (fp32; None
     unless with_bias)."""
-    return _ops().layernorm_bwd(x, dy, mean, rstd, weight, with_bias, want_dx, workspace, stream)
+    return (_binding or _ops()).layernorm_bwd(x, dy, mean, rstd, weight, with_bias, want_dx, workspace, stream)
 
 
 def beam_desc(G, K, V, M, x_dtype, row=0, eos=0) -> BeamDesc:
@@ -578,7 +578,7 @@ def beam_select(logits, scores, n_out=None, *, finished=None, eos=0, workspace=N
     [G,K,V] bf16 or fp32 (rows may be slices of wider ones), scores [G,K] fp32 summed log
     probabilities, finished [G,K] bool or None.  Returns (scores fp32, parent int32, token int32),
     each [G, n_out], best first; parent is the beam within its group, as ``state_reorder`` takes it."""
-    return _ops().beam_select(logits, scores, n_out, finished, eos, workspace, stream)
+    return (_binding or _ops()).beam_select(logits, scores, n_out, finished, eos, workspace, stream)
 
 
 def state_reorder(S, parent, *, layers=False, stream=None):
@@ -586,7 +586,7 @@ def state_reorder(S, parent, *, layers=False, stream=None):
     [G * K, ...] (decode_step's states, scan_step's, Raven's slots), or [L, G * K, ...] with layers;
     parent [G,K] int32.  Returns S.  A parent outside 0 .. K - 1 keeps its beam's state and shows as
     GDR_ERR_INDEX in query_device_status."""
-    return _ops().state_reorder(S, parent, layers, stream)
+    return (_binding or _ops()).state_reorder(S, parent, layers, stream)
 
 
 def query_device_status(stream=None) -> int:
