@@ -476,7 +476,7 @@ GDR_API gdr_status gdr_raven_fwd(const gdr_raven_desc* desc, const void* q, cons
  */
 #define GDR_SCAN_CKPT 64
 typedef struct {
-    int B, T, D;          /* sequences (at most 2^26), tokens (0 .. 2^30), channels (at most 2097120) */
+    int B, T, D;          /* sequences (at most 2^26), tokens (0 .. 2^30), channels (at most 1048560) */
     long long x_row;      /* elements from one token of x to the next (>= D; 0: D); a sequence is   */
     long long g_row;      /*   T rows, so x may be a slice of a wider [B,T,..] tensor; same for g   */
     gdr_dtype x_dtype;    /* x and dx */

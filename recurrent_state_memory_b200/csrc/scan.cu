@@ -13,33 +13,38 @@ namespace scn {
 enum Pass { FWD, BWD, STEP };
 
 // Blocks of a cluster (along the tokens): enough that the grid has about two blocks per SM, as far as
-// the sequence has tiles for them.  Where the largest clusters still leave a block per SM at most
-// (few channels, long sequences), a block's two groups take the turns alternately: 17.0 against
-// 31.4 us at B1 T20000 D11, 10.3 against 11.5 at B1 T16384 D128; with more channels than that a
-// block more is worth more than a group (B1 T32768 D512: 45 us with 8 blocks of one group, 56 of two).
-struct Split { int cluster, groups; };
-static Split split_of(long long tiles, int T, int tok, int sms, bool two_fit) {
+// the sequence has tiles for them.
+static int cluster_of(long long tiles, int T, int tok, int sms) {
     int n = 1;
     while (n < MAX_CLUSTER && tiles * n * 2 <= 2LL * sms && n * tok < T) n *= 2;
-    return {n, two_fit && n == MAX_CLUSTER && tiles * n <= sms && (long long)n * tok < T ? 2 : 1};
+    return n;
+}
+// Channels of a block: 16 where blocks of 32 and clusters of 8 would leave a block per SM at most (two
+// blocks of an SM hide one another's turns: 36.0 against 45.2 us at B1 T32768 D512, its backward 60.7
+// against 88.4), or where 32 would leave half of the lanes idle (17.8 against 28.9 us at B1 T20000
+// D11); else 32, whose rows are longer (46.5 against 58.1 us at B4 T4096 D2048).
+static int channels_of(const ScanParams& p, int sms) {
+    const long long wide = (p.D + 31) / 32;
+    return p.D <= 16 || wide * p.B * 8 <= sms ? 16 : 32;
 }
 
 template <typename KERN>
-static gdr_status launch_clusters(KERN kern, const ScanParams& p, const ScanMaps& maps, Split sp, size_t smem,
+static gdr_status launch_clusters(KERN kern, const ScanParams& p, const ScanMaps& maps, int channels, int tok, size_t smem,
                                   cudaStream_t st) {
-    const unsigned ct = (unsigned)((p.D + CH - 1) / CH);
-    smem = sp.groups * smem + HAND_BYTES + (size_t)sp.groups * 2 * sp.cluster * CH * sizeof(float2);
+    const unsigned ct = (unsigned)((p.D + channels - 1) / channels);
+    const int ncl = cluster_of((long long)ct * p.B, p.T, tok, device_sm_count());
+    smem += (size_t)2 * ncl * channels * sizeof(float2);
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e == cudaSuccess && sp.cluster > 8) e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e == cudaSuccess && ncl > 8) e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(scan)");
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(sp.cluster * p.B), ct);        // a sequence's cluster, 32 channels
-    cfg.blockDim = dim3(NT * sp.groups);
+    cfg.gridDim = dim3((unsigned)(ncl * p.B), ct);                // a sequence's cluster, its channels
+    cfg.blockDim = dim3(NT);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = sp.cluster; at[0].val.clusterDim.y = 1; at[0].val.clusterDim.z = 1;
+    at[0].val.clusterDim.x = ncl; at[0].val.clusterDim.y = 1; at[0].val.clusterDim.z = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
     e = cudaLaunchKernelEx(&cfg, kern, p, maps);
@@ -47,16 +52,16 @@ static gdr_status launch_clusters(KERN kern, const ScanParams& p, const ScanMaps
 }
 
 // A [B][T] tensor of rows `row` elements apart, the first D of each row: the map {D, 1, T, B} with
-// boxes of CH channels x tok tokens.  What lies outside reads as zero.
+// boxes of `channels` x tok tokens.  What lies outside reads as zero.
 template <typename T>
-static gdr_status encode_rows(CUtensorMap* m, const void* base, const ScanParams& p, long long row, int tok) {
+static gdr_status encode_rows(CUtensorMap* m, const void* base, const ScanParams& p, long long row, int channels, int tok) {
     EncodeTiledFn fn = nullptr;
     const gdr_status s = encode_fn(&fn);
     if (s != GDR_OK) return s;
     const cuuint64_t dims[4] = {(cuuint64_t)p.D, 1u, (cuuint64_t)p.T, (cuuint64_t)p.B};
     const cuuint64_t bytes = (cuuint64_t)row * sizeof(T);
     const cuuint64_t strides[3] = {bytes, bytes, bytes * (cuuint64_t)p.T};
-    const cuuint32_t box[4] = {CH, 1u, (cuuint32_t)tok, 1u}, estr[4] = {1u, 1u, 1u, 1u};
+    const cuuint32_t box[4] = {(cuuint32_t)channels, 1u, (cuuint32_t)(tok < BOX_ROWS ? tok : BOX_ROWS), 1u}, estr[4] = {1u, 1u, 1u, 1u};
     const CUresult r = fn(m, sizeof(T) == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4,
                           const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
                           CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
@@ -68,7 +73,7 @@ static gdr_status encode_rows(CUtensorMap* m, const void* base, const ScanParams
 
 // The same tensor for rows that start anywhere (Phases in scan.cuh): P rows as one long row.
 template <typename T>
-static gdr_status encode_phases(CUtensorMap* m, const void* base, const ScanParams& p, long long row, int tok) {
+static gdr_status encode_phases(CUtensorMap* m, const void* base, const ScanParams& p, long long row, int channels, int tok) {
     EncodeTiledFn fn = nullptr;
     const gdr_status s = encode_fn(&fn);
     if (s != GDR_OK) return s;
@@ -77,7 +82,7 @@ static gdr_status encode_phases(CUtensorMap* m, const void* base, const ScanPara
     const cuuint64_t bytes = (cuuint64_t)P * row * sizeof(T), rows = (cuuint64_t)p.covered / P;
     const cuuint64_t dims[4] = {(cuuint64_t)(lead + (P - 1) * row + p.D), 1u, rows, 1u};
     const cuuint64_t strides[3] = {bytes, bytes, bytes * rows};
-    const cuuint32_t box[4] = {CH + P, 1u, (cuuint32_t)(tok / P), 1u}, estr[4] = {1u, 1u, 1u, 1u};
+    const cuuint32_t box[4] = {(cuuint32_t)(channels + P), 1u, (cuuint32_t)(tok / P), 1u}, estr[4] = {1u, 1u, 1u, 1u};
     const CUresult r = fn(m, sizeof(T) == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4,
                           reinterpret_cast<void*>(at - at % 16), dims, strides, box, estr,
                           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
@@ -88,8 +93,33 @@ static gdr_status encode_phases(CUtensorMap* m, const void* base, const ScanPara
 }
 
 template <typename T, int V>
-static gdr_status encode(CUtensorMap* m, const void* base, const ScanParams& p, long long row, int tok) {
-    return V > 1 ? encode_rows<T>(m, base, p, row, tok) : encode_phases<T>(m, base, p, row, tok);
+static gdr_status encode(CUtensorMap* m, const void* base, const ScanParams& p, long long row, int channels, int tok) {
+    return V > 1 ? encode_rows<T>(m, base, p, row, channels, tok) : encode_phases<T>(m, base, p, row, channels, tok);
+}
+
+template <typename XT, typename GT, typename OT, int V, int CH>
+static gdr_status launch_sequences(Pass pass, ScanParams& p, cudaStream_t st) {
+    const int tok = pass == FWD ? Tile<V, fwd_elems<V>(), CH>::TOK : Tile<V, BWD_ELEMS, CH>::TOK;
+    ScanMaps maps = {};
+    // V = 1: whole groups of 8 rows, where the copies' coordinates and sizes fit their types
+    const long long rows = (long long)p.B * p.T, wide = p.x_row > p.g_row ? p.x_row : p.g_row;
+    auto inside = [&](const void* q, long long row, size_t el) {    // a long row does not reach into the next one
+        const long long lead = (long long)(reinterpret_cast<uintptr_t>(q) % 16 / el);
+        return lead == 0 || lead + p.D <= row;
+    };
+    const bool fits = rows / 8 < (1LL << 31) - 1 && wide < (1LL << 27) && rows * wide < (1LL << 37) &&
+                      inside(p.x, p.x_row, sizeof(XT)) && inside(p.g, p.g_row, sizeof(GT)) &&
+                      (pass != BWD || inside(p.dh, p.D, sizeof(OT)));
+    p.covered = fits ? rows / 8 * 8 : 0;
+    if (V > 1 || p.covered > 0) {
+        gdr_status s = encode<XT, V>(&maps.x, p.x, p, p.x_row, CH, tok);
+        if (s == GDR_OK) s = encode<GT, V>(&maps.g, p.g, p, p.g_row, CH, tok);
+        if (s == GDR_OK && pass == BWD && p.dh) s = encode<OT, V>(&maps.dh, p.dh, p, p.D, CH, tok);
+        if (s != GDR_OK) return s;
+    }
+    if (pass == FWD)
+        return launch_clusters(scan_fwd_kernel<XT, GT, OT, V, CH>, p, maps, CH, tok, sizeof(FwdSmem<XT, GT, V, CH>), st);
+    return launch_clusters(scan_bwd_kernel<XT, GT, OT, V, CH>, p, maps, CH, tok, sizeof(BwdSmem<XT, GT, OT, V, CH>), st);
 }
 
 template <typename XT, typename GT, typename OT, int V>
@@ -100,37 +130,8 @@ static gdr_status launch_v(Pass pass, ScanParams& p, cudaStream_t st) {
         const cudaError_t e = cudaGetLastError();
         return e == cudaSuccess ? GDR_OK : cuda_fail(e, "launch(scan step)");
     }
-    const int tok = pass == FWD ? Tile<V, fwd_elems<V>()>::TOK : Tile<V, BWD_ELEMS>::TOK;
-    ScanMaps maps = {};
-    // V = 1: whole groups of 8 rows, where the copies' coordinates and sizes fit their types
-    const long long rows = (long long)p.B * p.T, wide = p.x_row > p.g_row ? p.x_row : p.g_row;
-    auto inside = [&](const void* q, long long row, size_t el) {    // a long row does not reach into the next one
-        const long long lead = (long long)(reinterpret_cast<uintptr_t>(q) % 16 / el);
-        return lead == 0 || lead + p.D <= row;
-    };
-    const bool fits = rows / 8 < (1LL << 31) - 1 && wide < (1LL << 27) && rows * wide < (1LL << 37) &&
-                      inside(p.x, p.x_row, sizeof(XT)) && inside(p.g, p.g_row, sizeof(GT));
-    p.covered = fits ? rows / 8 * 8 : 0;
-    if (V > 1 || p.covered > 0) {
-        gdr_status s = encode<XT, V>(&maps.x, p.x, p, p.x_row, tok);
-        if (s == GDR_OK) s = encode<GT, V>(&maps.g, p.g, p, p.g_row, tok);
-        if (s == GDR_OK && pass == BWD && p.dh) s = encode<OT, V>(&maps.dh, p.dh, p, p.D, tok);
-        if (s != GDR_OK) return s;
-    }
-    constexpr size_t fwd = sizeof(FwdSmem<XT, GT, V>), bwd = sizeof(BwdSmem<XT, GT, OT, V>);
-    constexpr size_t room = 227 * 1024 - HAND_BYTES - 4 * MAX_CLUSTER * CH * sizeof(float2);
-    constexpr bool fwd2 = 2 * fwd <= room, bwd2 = 2 * bwd <= room;
-    const Split sp = split_of((long long)((p.D + CH - 1) / CH) * p.B, p.T, tok, device_sm_count(), pass == FWD ? fwd2 : bwd2);
-    if (pass == FWD) {
-        if constexpr (fwd2) {
-            if (sp.groups == 2) return launch_clusters(scan_fwd_kernel<XT, GT, OT, V, 2>, p, maps, sp, fwd, st);
-        }
-        return launch_clusters(scan_fwd_kernel<XT, GT, OT, V, 1>, p, maps, sp, fwd, st);
-    }
-    if constexpr (bwd2) {
-        if (sp.groups == 2) return launch_clusters(scan_bwd_kernel<XT, GT, OT, V, 2>, p, maps, sp, bwd, st);
-    }
-    return launch_clusters(scan_bwd_kernel<XT, GT, OT, V, 1>, p, maps, sp, bwd, st);
+    return channels_of(p, device_sm_count()) == 16 ? launch_sequences<XT, GT, OT, V, 16>(pass, p, st)
+                                                   : launch_sequences<XT, GT, OT, V, 32>(pass, p, st);
 }
 
 // Four channels per thread (and tiles by TMA) where every row of every tensor starts on 16 bytes,
@@ -177,8 +178,8 @@ static gdr_status check_desc(const gdr_scan_desc* d) {
 static gdr_status check_sequences(const gdr_scan_desc* d) {
     const gdr_status s = check_desc(d);
     if (s != GDR_OK) return s;
-    if (d->B > (1 << 26) || d->T > (1 << 30) || d->D > 65535 * CH)
-        return fail(GDR_ERR_UNSUPPORTED, "B must be at most 2^26, T 2^30, D 2097120%s");
+    if (d->B > (1 << 26) || d->T > (1 << 30) || d->D > 65535 * 16)
+        return fail(GDR_ERR_UNSUPPORTED, "B must be at most 2^26, T 2^30, D 1048560%s");
     return GDR_OK;
 }
 

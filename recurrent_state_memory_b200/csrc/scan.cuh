@@ -10,8 +10,8 @@
 //
 // Bound: HBM (a forward moves 6 to 12 bytes per element for about 20 instructions).
 //
-// Split.  A block of 8 warps owns 32 channels x TOK tokens per turn and walks the sequence in
-// turns.  Where the channels alone do not fill the GPU, a cluster of up to 16 blocks takes that
+// Split.  A block of 8 warps owns CH = 32 or 16 channels x TOK tokens per turn and walks the sequence
+// in turns.  Where the channels alone do not fill the GPU, a cluster of up to 16 blocks takes that
 // many neighbouring tiles per turn: the blocks send one another their tiles' (A, H) by
 // asynchronous stores into distributed shared memory, which an mbarrier counts (a cluster barrier
 // per turn would also wait for the turn's output stores: 96 against 90 us); every block folds them
@@ -52,16 +52,10 @@ struct ScanParams {
 
 constexpr int CKPT = GDR_SCAN_CKPT;
 constexpr int NT = 256;
-constexpr int CH = 32;                  // channels of a block
 constexpr int WT = NT / 32;             // warps, along the tokens
+constexpr int BOX_ROWS = 256;           // of one tensor copy at most
 constexpr int MAX_CLUSTER = 16;
 constexpr int STAGES = 2;
-
-// Threads of one group (of GR in a block): a barrier of its own.
-template <int GR> __device__ __forceinline__ void group_sync(int grp) {
-    if constexpr (GR == 1) __syncthreads();
-    else asm volatile("bar.sync %0, %1;" ::"r"(1 + grp), "n"(NT) : "memory");
-}
 
 __device__ __forceinline__ int seq_len(const ScanParams& p, int b) {
     return p.lengths ? min(max(p.lengths[b], 0), p.T) : p.T;
@@ -139,15 +133,15 @@ __device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity) {
     return true;
 }
 
-// How a block's threads lie over its tile.  V = 4: 8 lanes x 4 channels and 4 runs per warp; V = 1
-// (rows that start on no 16 bytes): 32 lanes x 1 channel.
-template <int V, int ELEMS> struct Tile {
-    static constexpr int LC = 32 / V;           // lanes along the channels
+// How a block's threads lie over its tile of CH channels: lanes of V = 4 channels, or of one (rows that
+// start on no 16 bytes), the warp's other lanes along the tokens.
+template <int V, int ELEMS, int CH> struct Tile {
+    static constexpr int LC = CH / V;           // lanes along the channels
     static constexpr int TL = 32 / LC;          // runs in a warp
     static constexpr int R = ELEMS / V;         // tokens of a run
     static constexpr int TOK = WT * TL * R;     // tokens of a block
     int warp, lane_t, c;                        // warp, run in the warp, first channel in the block
-    __device__ __forceinline__ Tile() : warp((threadIdx.x >> 5) & (WT - 1)), lane_t((threadIdx.x & 31) / LC),
+    __device__ __forceinline__ Tile() : warp(threadIdx.x >> 5), lane_t((threadIdx.x & 31) / LC),
                                         c(((threadIdx.x & 31) % LC) * V) {}
     __device__ __forceinline__ int first_token() const { return (warp * TL + lane_t) * R; }
 };
@@ -158,7 +152,7 @@ template <int V, int ELEMS> struct Tile {
 // elements wider than the channels and started at the 16 bytes before them: slot q holds the
 // tile's tokens q, q + P, .. .  The last B * T mod 8 rows, which no whole long row holds, are
 // read from global memory.
-template <typename T, int TOK> struct Phases {
+template <typename T, int TOK, int CH> struct Phases {
     static constexpr int P = 16 / (int)sizeof(T), W = CH + P, ROWS = TOK / P;
     alignas(128) T v[P][ROWS][W];
     static __device__ __forceinline__ int lead(const void* base) { return (int)(reinterpret_cast<uintptr_t>(base) % 16 / sizeof(T)); }
@@ -174,18 +168,17 @@ template <typename T, int TOK> struct Phases {
 };
 // R tokens of one lane's channel: tile tokens i0 .. (a multiple of P), row n0 of the tensor first.
 // skew[q]: where slot q's rows hold the lane's channel.
-template <typename T, int TOK, int R>
-__device__ __forceinline__ void read_run(const Phases<T, TOK>& ph, const int (&skew)[Phases<T, TOK>::P], int i0, float (&v)[R][1]) {
-    constexpr int P = Phases<T, TOK>::P;
+template <typename T, int TOK, int CH, int R>
+__device__ __forceinline__ void read_run(const Phases<T, TOK, CH>& ph, const int (&skew)[16 / sizeof(T)], int i0, float (&v)[R][1]) {
+    constexpr int P = Phases<T, TOK, CH>::P;
 #pragma unroll
     for (int r = 0; r < R; ++r) v[r][0] = ld_f32(&ph.v[r % P][(i0 + r) / P][skew[r % P]]);
 }
-template <typename T, int TOK>
-__device__ __forceinline__ void skews(const Phases<T, TOK>& ph, const void* base, long long row, int c0, long long n0,
-                                      int (&skew)[Phases<T, TOK>::P]) {
+template <typename T, int TOK, int CH>
+__device__ __forceinline__ void skews(const Phases<T, TOK, CH>& ph, const void* base, long long row, int c0, long long n0,
+                                      int c, int (&skew)[16 / sizeof(T)]) {
 #pragma unroll
-    for (int q = 0; q < Phases<T, TOK>::P; ++q)
-        skew[q] = (int)(Phases<T, TOK>::start(base, row, c0, n0, q) % Phases<T, TOK>::P) + (int)(threadIdx.x & 31);
+    for (int q = 0; q < ph.P; ++q) skew[q] = (int)(ph.start(base, row, c0, n0, q) % ph.P) + c;
 }
 template <typename T, int R>
 __device__ __forceinline__ void read_run_global(const T* src, long long row, int have, float (&v)[R][1]) {
@@ -220,84 +213,50 @@ __device__ __forceinline__ void warp_runs(float (&A)[V], float (&H)[V], float (&
     }
 }
 
-// The state at a turn's start goes from turn to turn.  With two groups in a block, which take the
-// turns alternately, it goes through shared memory: the warp that has it for turn k + 1 arrives at
-// the barrier that turn k + 1's warp waits at (two barriers in turn).
-template <int GR> struct Carry {
-    float v;                    // this lane's channel
-    float (*hand)[CH];          // [2]
-    __device__ __forceinline__ void take(int k) {
-        if constexpr (GR > 1) {
-            if (k == 0) return;
-            asm volatile("bar.sync %0, 64;" ::"r"(3 + ((k - 1) & 1)) : "memory");
-            v = hand[(k - 1) & 1][threadIdx.x & 31];
-        }
-    }
-    __device__ __forceinline__ void give(int k, int turns) {
-        if constexpr (GR > 1) {
-            if (k + 1 >= turns) return;
-            hand[k & 1][threadIdx.x & 31] = v;
-            asm volatile("bar.arrive %0, 64;" ::"r"(3 + (k & 1)) : "memory");
-        }
-    }
-};
-
 // The state before every warp's runs, along the scan's direction, by one warp (lane = channel).
-// agg: the group's warps' (A, H); carry: the state at the cluster's turn start, which every block
-// holds alike and moves on by the turn.  xch and bars hold two of the group's turns j = k / GR: a
-// block sends turn j + 2's only when it has turn j + 1's from every peer, each of which sent it
-// behind its last read of turn j's.  lost: a wait ran out (status word); the block goes on without
-// waiting.
-template <bool UP, int GR>
+// agg: the block's warps' (A, H); carry: the state at the cluster's turn start, which every block
+// holds alike and moves on by the turn.  xch and bars hold two turns' worth: a block sends turn
+// k + 2's only when it has turn k + 1's from every peer, each of which sent it behind its last
+// read of turn k's.  lost: a wait ran out (status word); the block goes on without waiting.
+template <bool UP, int CH>
 __device__ __forceinline__ void warp_starts(const float2 (*agg)[CH], float2 (*xch)[CH], uint64_t* bars,
-                                            float (*start)[CH], Carry<GR>& carry, bool& lost, int k, int turns, int rank,
-                                            int ncl) {
-    const int c = threadIdx.x & 31, j = k / GR;
+                                            float (*start)[CH], float& carry, bool& lost, int k, int rank, int ncl) {
+    const int c = threadIdx.x & 31;
+    if (CH < 32 && c >= CH) return;
     float2 e[WT];
 #pragma unroll
     for (int w = 0; w < WT; ++w) e[w] = agg[UP ? w : WT - 1 - w][c];
-    float s, all;
+    float s = carry;
     if (ncl > 1) {
         float A = 1.f, H = 0.f;
 #pragma unroll
         for (int w = 0; w < WT; ++w) { H = fmaf(e[w].x, H, e[w].y); A *= e[w].x; }
-        xch += (j & 1) * ncl;
-        uint64_t* bar = bars + (j & 1);
+        xch += (k & 1) * ncl;
+        uint64_t* bar = bars + (k & 1);
         if (c == 0) expect_bytes(bar, (uint32_t)(ncl * CH * sizeof(float2)));
         for (int r = 0; r < ncl; ++r) store_peer(&xch[rank][c], make_float2(A, H), bar, r);
-        if (!lost) lost = !wait_phase(bar, (uint32_t)(j >> 1) & 1u);
-        // the blocks before this one as one piece, then the whole turn: only one product each waits
-        // for the carry
-        float pA = 1.f, pH = 0.f;
-        A = 1.f; H = 0.f;
+        if (!lost) lost = !wait_phase(bar, (uint32_t)(k >> 1) & 1u);
+        float all = carry;
         for (int i = 0; i < ncl; ++i) {
             const int r = UP ? i : ncl - 1 - i;
-            if (r == rank) { pA = A; pH = H; }
+            if (r == rank) s = all;
             const float2 x = xch[r][c];
-            H = fmaf(x.x, H, x.y);
-            A *= x.x;
+            all = fmaf(x.x, all, x.y);
         }
-        carry.take(k);
-        s = fmaf(pA, carry.v, pH);
-        all = fmaf(A, carry.v, H);
-        carry.v = all;
-        carry.give(k, turns);
-    } else {
-        carry.take(k);
-        s = carry.v;
+        carry = all;
     }
 #pragma unroll
     for (int w = 0; w < WT; ++w) {
         start[UP ? w : WT - 1 - w][c] = s;
         s = fmaf(e[w].x, s, e[w].y);
     }
-    if (ncl == 1) { carry.v = s; carry.give(k, turns); }
+    if (ncl == 1) carry = s;
 }
 
-// Before the first turn: every group's barriers (n of them), and the peers' shared memory exists.
-template <typename S> __device__ __forceinline__ void barriers_begin(S* sm, int groups, int n, int ncl) {
+// Before the first turn: the barriers (n of them), and the peers' shared memory exists.
+__device__ __forceinline__ void barriers_begin(uint64_t* bars, int n, int ncl) {
     if (threadIdx.x == 0) {
-        for (int i = 0; i < groups * n; ++i) tc::mbar_init(&sm[i / n].bars[i % n], 1);
+        for (int i = 0; i < n; ++i) tc::mbar_init(&bars[i], 1);
         tc::fence_mbar_init();
     }
     if (ncl > 1) cluster_sync();
@@ -312,8 +271,14 @@ __device__ __forceinline__ void run_start(const float* start, const float (&exA)
 }
 
 // A tile in shared memory.
-template <typename T, int TOK> struct Rows { alignas(128) T v[TOK][CH]; };
-template <typename T, int V, int TOK> using TileOf = std::conditional_t<(V > 1), Rows<T, TOK>, Phases<T, TOK>>;
+template <typename T, int TOK, int CH> struct Rows {
+    alignas(128) T v[TOK][CH];
+    __device__ __forceinline__ void copy(const CUtensorMap* map, int c0, int t, int b, uint64_t* bar) {
+#pragma unroll
+        for (int r = 0; r < TOK; r += BOX_ROWS) tc::tma_load_4d(smem_addr(v[r]), map, c0, 0, t + r, b, bar);
+    }
+};
+template <typename T, int V, int TOK, int CH> using TileOf = std::conditional_t<(V > 1), Rows<T, TOK, CH>, Phases<T, TOK, CH>>;
 
 // The tensor maps of a call.
 struct ScanMaps { CUtensorMap x, g, dh; };
@@ -321,31 +286,26 @@ struct ScanMaps { CUtensorMap x, g, dh; };
 template <int V> constexpr int fwd_elems() { return V > 1 ? 32 : 16; }  // of a thread: 2 registers each
 constexpr int BWD_ELEMS = 16;                                           // 5 registers each
 
-template <typename XT, typename GT, int V> struct FwdSmem {
-    static constexpr int TOK = Tile<V, fwd_elems<V>()>::TOK;
-    TileOf<GT, V, TOK> g[STAGES];
-    TileOf<XT, V, TOK> x[STAGES];
+template <typename XT, typename GT, int V, int CH> struct FwdSmem {
+    static constexpr int TOK = Tile<V, fwd_elems<V>(), CH>::TOK;
+    TileOf<GT, V, TOK, CH> g[STAGES];
+    TileOf<XT, V, TOK, CH> x[STAGES];
     float2 agg[WT][CH];
     float start[WT][CH];
     uint64_t bars[2 + STAGES];          // the exchange's, the stages'
 };
-// Behind the groups' parts: the carry's hand-over [2][CH], then every group's xch [2][cluster][CH].
-constexpr size_t HAND_BYTES = 2 * CH * sizeof(float);
+// Behind it: xch [2][cluster][CH].
 
-// GR groups of 8 warps in a block take the turns alternately: where there is a block per SM at most,
-// the second group computes while the first one waits for the cluster.
-template <typename XT, typename GT, typename OT, int V, int GR>
-__global__ void __launch_bounds__(NT * GR, GR > 1 ? 1 : V > 1 ? 2 : 3) scan_fwd_kernel(ScanParams p, const __grid_constant__ ScanMaps maps) {
-    using L = Tile<V, fwd_elems<V>()>;
-    using S = FwdSmem<XT, GT, V>;
+template <typename XT, typename GT, typename OT, int V, int CH>
+__global__ void __launch_bounds__(NT, V > 1 ? 2 : 3) scan_fwd_kernel(ScanParams p, const __grid_constant__ ScanMaps maps) {
+    using L = Tile<V, fwd_elems<V>(), CH>;
+    using S = FwdSmem<XT, GT, V, CH>;
     constexpr int R = L::R;
     extern __shared__ __align__(128) unsigned char raw[];
     const L l;
-    const int rank = (int)cluster_rank(), ncl = (int)cluster_size(), grp = GR > 1 ? threadIdx.x / NT : 0;
-    S* const parts = reinterpret_cast<S*>(raw);
-    S& sm = parts[grp];
-    float (*const hand)[CH] = reinterpret_cast<float (*)[CH]>(parts + GR);
-    float2 (*const xch)[CH] = reinterpret_cast<float2 (*)[CH]>(reinterpret_cast<unsigned char*>(parts + GR) + HAND_BYTES) + grp * 2 * ncl;
+    const int rank = (int)cluster_rank(), ncl = (int)cluster_size();
+    S& sm = *reinterpret_cast<S*>(raw);
+    float2 (*const xch)[CH] = reinterpret_cast<float2 (*)[CH]>(&sm + 1);
     const int b = blockIdx.x / ncl, c0 = blockIdx.y * CH, c = c0 + l.c;
     const bool on = c < p.D;                              // V divides D, or V = 1
     const int len = seq_len(p, b), nck = (p.T + CKPT - 1) / CKPT;
@@ -356,17 +316,17 @@ __global__ void __launch_bounds__(NT * GR, GR > 1 ? 1 : V > 1 ? 2 : 3) scan_fwd_
     const int tile = rank * L::TOK, first = tile + l.first_token();     // of turn 0: this block's, this thread's
     bool lost = false;
 
-    barriers_begin(parts, GR, 2 + STAGES, ncl);
+    barriers_begin(sm.bars, 2 + STAGES, ncl);
     auto fetch = [&](int k) {                             // turn k's tile, unless it lies behind the sequence
-        const int t = k * turn + tile, st = k / GR % STAGES;
+        const int t = k * turn + tile, st = k % STAGES;
         if (l.warp != 0 || k >= turns || t >= len) return;
         uint64_t* bar = &sm.bars[2 + st];
         const int lane = threadIdx.x & 31;
         if constexpr (V > 1) {
             if (lane != 0) return;
             expect_bytes(bar, sizeof(sm.g[0]) + sizeof(sm.x[0]));
-            tc::tma_load_4d(smem_addr(sm.g[st].v), &maps.g, c0, 0, t, b, bar);
-            tc::tma_load_4d(smem_addr(sm.x[st].v), &maps.x, c0, 0, t, b, bar);
+            sm.g[st].copy(&maps.g, c0, t, b, bar);
+            sm.x[st].copy(&maps.x, c0, t, b, bar);
         } else if (p.covered > 0) {
             if (lane == 0) expect_bytes(bar, sizeof(sm.g[0]) + sizeof(sm.x[0]));
             __syncwarp();
@@ -376,25 +336,26 @@ __global__ void __launch_bounds__(NT * GR, GR > 1 ? 1 : V > 1 ? 2 : 3) scan_fwd_
         }
     };
 #pragma unroll
-    for (int j = 0; j < STAGES; ++j) fetch(grp + j * GR);
+    for (int k = 0; k < STAGES; ++k) fetch(k);
 
-    int skew_g[V > 1 ? 1 : TileOf<GT, 1, L::TOK>::P], skew_x[V > 1 ? 1 : TileOf<XT, 1, L::TOK>::P];
+    int skew_g[V > 1 ? 1 : 16 / sizeof(GT)], skew_x[V > 1 ? 1 : 16 / sizeof(XT)];
     if constexpr (V == 1) {
         const long long n0 = (long long)b * p.T;          // tiles start a multiple of P tokens later
-        skews(sm.g[0], p.g, p.g_row, c0, n0, skew_g);
-        skews(sm.x[0], p.x, p.x_row, c0, n0, skew_x);
+        skews(sm.g[0], p.g, p.g_row, c0, n0, l.c, skew_g);
+        skews(sm.x[0], p.x, p.x_row, c0, n0, l.c, skew_x);
     }
-    // of a group's warp 0: the state at the turn's start, of the lane's channel
+    // of warp 0: the state at the turn's start, of the lane's channel
     const int lane_c = c0 + (int)(threadIdx.x & 31);
-    Carry<GR> carry{0.f, hand};
-    if (l.warp == 0 && lane_c < p.D && p.h0) carry.v = p.h0[(size_t)b * p.D + lane_c];
+    const bool lane_on = l.warp == 0 && (int)(threadIdx.x & 31) < CH && lane_c < p.D;
+    float carry = 0.f;
+    if (lane_on && p.h0) carry = p.h0[(size_t)b * p.D + lane_c];
 
-    for (int k = grp; k < turns; k += GR) {
+    for (int k = 0; k < turns; ++k) {
         const int t0 = k * turn + first;
         float a[R][V], bb[R][V], A[V], H[V], exA[V], exH[V];
         if (k * turn + tile < len) {
-            const int st = k / GR % STAGES;
-            if ((V > 1 || p.covered > 0) && !lost) lost = !wait_phase(&sm.bars[2 + st], (uint32_t)(k / GR / STAGES) & 1u);
+            const int st = k % STAGES;
+            if ((V > 1 || p.covered > 0) && !lost) lost = !wait_phase(&sm.bars[2 + st], (uint32_t)(k / STAGES) & 1u);
             if constexpr (V > 1) {
 #pragma unroll
                 for (int r = 0; r < R; ++r) {
@@ -445,10 +406,10 @@ __global__ void __launch_bounds__(NT * GR, GR > 1 ? 1 : V > 1 ? 2 : 3) scan_fwd_
 #pragma unroll
             for (int i = 0; i < V; ++i) sm.agg[l.warp][l.c + i] = make_float2(A[i], H[i]);
         }
-        group_sync<GR>(grp);
-        fetch(k + STAGES * GR);                           // the stage of turn k is in registers
-        if (l.warp == 0) warp_starts<true, GR>(sm.agg, xch, sm.bars, sm.start, carry, lost, k, turns, rank, ncl);
-        group_sync<GR>(grp);
+        __syncthreads();
+        fetch(k + STAGES);                           // the stage of turn k is in registers
+        if (l.warp == 0) warp_starts<true, CH>(sm.agg, xch, sm.bars, sm.start, carry, lost, k, rank, ncl);
+        __syncthreads();
         float s[V];
         run_start<V>(&sm.start[l.warp][l.c], exA, exH, s);
         if (on && p.ckpt && t0 % CKPT == 0 && t0 < p.T) {
@@ -482,15 +443,14 @@ __global__ void __launch_bounds__(NT * GR, GR > 1 ? 1 : V > 1 ? 2 : 3) scan_fwd_
         }
     }
     if (ncl > 1) cluster_sync_relaxed();                  // no peer still sends here
-    if (p.h_T && rank == 0 && l.warp == 0 && grp == (turns - 1) % GR && lane_c < p.D)
-        p.h_T[(size_t)b * p.D + lane_c] = carry.v;
+    if (p.h_T && rank == 0 && lane_on) p.h_T[(size_t)b * p.D + lane_c] = carry;
 }
 
-template <typename XT, typename GT, typename OT, int V> struct BwdSmem {
-    static constexpr int TOK = Tile<V, BWD_ELEMS>::TOK;
-    TileOf<GT, V, TOK> g[STAGES];
-    TileOf<XT, V, TOK> x[STAGES];
-    TileOf<OT, V, TOK> dh[STAGES];
+template <typename XT, typename GT, typename OT, int V, int CH> struct BwdSmem {
+    static constexpr int TOK = Tile<V, BWD_ELEMS, CH>::TOK;
+    TileOf<GT, V, TOK, CH> g[STAGES];
+    TileOf<XT, V, TOK, CH> x[STAGES];
+    TileOf<OT, V, TOK, CH> dh[STAGES];
     float2 up[WT][CH];
     float2 down[WT][CH];
     float before[WT][CH];
@@ -500,19 +460,17 @@ template <typename XT, typename GT, typename OT, int V> struct BwdSmem {
 
 // The states inside a tile come from the checkpoint at its first token (a tile is a whole number of
 // CKPT tokens), so only the gradient's direction goes through the cluster.
-template <typename XT, typename GT, typename OT, int V, int GR>
-__global__ void __launch_bounds__(NT * GR, GR > 1 ? 1 : 2) scan_bwd_kernel(ScanParams p, const __grid_constant__ ScanMaps maps) {
-    using L = Tile<V, BWD_ELEMS>;
-    using S = BwdSmem<XT, GT, OT, V>;
+template <typename XT, typename GT, typename OT, int V, int CH>
+__global__ void __launch_bounds__(NT, 2) scan_bwd_kernel(ScanParams p, const __grid_constant__ ScanMaps maps) {
+    using L = Tile<V, BWD_ELEMS, CH>;
+    using S = BwdSmem<XT, GT, OT, V, CH>;
     constexpr int R = L::R;
     static_assert(L::TOK % CKPT == 0, "a tile starts at a checkpoint");
     extern __shared__ __align__(128) unsigned char raw[];
     const L l;
-    const int rank = (int)cluster_rank(), ncl = (int)cluster_size(), grp = GR > 1 ? threadIdx.x / NT : 0;
-    S* const parts = reinterpret_cast<S*>(raw);
-    S& sm = parts[grp];
-    float (*const hand)[CH] = reinterpret_cast<float (*)[CH]>(parts + GR);
-    float2 (*const xch)[CH] = reinterpret_cast<float2 (*)[CH]>(reinterpret_cast<unsigned char*>(parts + GR) + HAND_BYTES) + grp * 2 * ncl;
+    const int rank = (int)cluster_rank(), ncl = (int)cluster_size();
+    S& sm = *reinterpret_cast<S*>(raw);
+    float2 (*const xch)[CH] = reinterpret_cast<float2 (*)[CH]>(&sm + 1);
     const int b = blockIdx.x / ncl, c0 = blockIdx.y * CH, c = c0 + l.c;
     const bool on = c < p.D;
     const int len = seq_len(p, b), nck = (p.T + CKPT - 1) / CKPT;
@@ -526,23 +484,22 @@ __global__ void __launch_bounds__(NT * GR, GR > 1 ? 1 : 2) scan_bwd_kernel(ScanP
     const bool with_dh = p.dh != nullptr;
     bool lost = false;
 
-    barriers_begin(parts, GR, 2 + STAGES, ncl);
+    barriers_begin(sm.bars, 2 + STAGES, ncl);
     // turn k walks from the end: its tokens start at (turns - 1 - k) * turn.  Tiles behind the
     // sequence are not fetched, so the stages count the fetched ones, from turn `skip` on.
     const int live = (len - tile + turn - 1) / turn;      // turns of this block with tokens (len > tile), else <= 0
     const int skip = turns - max(live, 0);
-    const int from = skip + (GR > 1 ? (skip ^ grp) & 1 : 0);            // this group's first fetched turn
     auto fetch = [&](int k) {
         if (l.warp != 0 || k < skip || k >= turns) return;
-        const int t = (turns - 1 - k) * turn + tile, st = (k - from) / GR % STAGES, lane = threadIdx.x & 31;
+        const int t = (turns - 1 - k) * turn + tile, st = (k - skip) % STAGES, lane = threadIdx.x & 31;
         uint64_t* bar = &sm.bars[2 + st];
         const uint32_t bytes = sizeof(sm.g[0]) + sizeof(sm.x[0]) + (with_dh ? sizeof(sm.dh[0]) : 0);
         if constexpr (V > 1) {
             if (lane != 0) return;
             expect_bytes(bar, bytes);
-            tc::tma_load_4d(smem_addr(sm.g[st].v), &maps.g, c0, 0, t, b, bar);
-            tc::tma_load_4d(smem_addr(sm.x[st].v), &maps.x, c0, 0, t, b, bar);
-            if (with_dh) tc::tma_load_4d(smem_addr(sm.dh[st].v), &maps.dh, c0, 0, t, b, bar);
+            sm.g[st].copy(&maps.g, c0, t, b, bar);
+            sm.x[st].copy(&maps.x, c0, t, b, bar);
+            if (with_dh) sm.dh[st].copy(&maps.dh, c0, t, b, bar);
         } else if (p.covered > 0) {
             if (lane == 0) expect_bytes(bar, bytes);
             __syncwarp();
@@ -553,28 +510,29 @@ __global__ void __launch_bounds__(NT * GR, GR > 1 ? 1 : 2) scan_bwd_kernel(ScanP
         }
     };
 #pragma unroll
-    for (int j = 0; j < STAGES; ++j) fetch(from + j * GR);
+    for (int k = 0; k < STAGES; ++k) fetch(skip + k);
 
-    int skew_g[V > 1 ? 1 : TileOf<GT, 1, L::TOK>::P], skew_x[V > 1 ? 1 : TileOf<XT, 1, L::TOK>::P],
-        skew_d[V > 1 ? 1 : TileOf<OT, 1, L::TOK>::P];
+    int skew_g[V > 1 ? 1 : 16 / sizeof(GT)], skew_x[V > 1 ? 1 : 16 / sizeof(XT)],
+        skew_d[V > 1 ? 1 : 16 / sizeof(OT)];
     if constexpr (V == 1) {
         const long long n0 = (long long)b * p.T;
-        skews(sm.g[0], p.g, p.g_row, c0, n0, skew_g);
-        skews(sm.x[0], p.x, p.x_row, c0, n0, skew_x);
-        skews(sm.dh[0], p.dh, p.D, c0, n0, skew_d);
+        skews(sm.g[0], p.g, p.g_row, c0, n0, l.c, skew_g);
+        skews(sm.x[0], p.x, p.x_row, c0, n0, l.c, skew_x);
+        skews(sm.dh[0], p.dh, p.D, c0, n0, l.c, skew_d);
     }
-    // of a group's warp 0: a_{t+1} lam_{t+1} behind the turn
+    // of warp 0: a_{t+1} lam_{t+1} behind the turn, of the lane's channel
     const int lane_c = c0 + (int)(threadIdx.x & 31);
-    Carry<GR> carry{0.f, hand};
-    if (l.warp == 0 && lane_c < p.D && p.dh_T) carry.v = p.dh_T[(size_t)b * p.D + lane_c];
+    const bool lane_on = l.warp == 0 && (int)(threadIdx.x & 31) < CH && lane_c < p.D;
+    float carry = 0.f;
+    if (lane_on && p.dh_T) carry = p.dh_T[(size_t)b * p.D + lane_c];
 
-    for (int k = grp; k < turns; k += GR) {
+    for (int k = 0; k < turns; ++k) {
         const int base = (turns - 1 - k) * turn, t0 = base + first;
         // of warp 1: the state before the tile
-        Carry<1> state{0.f, nullptr};
+        float state = 0.f;
         if (l.warp == 1) {
             const int j = (base + tile) / CKPT;
-            if (j < nck && lane_c < p.D) state.v = p.ckpt[((size_t)b * nck + j) * p.D + lane_c];
+            if (j < nck && lane_c < p.D) state = p.ckpt[((size_t)b * nck + j) * p.D + lane_c];
         }
         float a[R][V], rest[R][V], xv[R][V], d[R][V];
 #pragma unroll
@@ -582,8 +540,8 @@ __global__ void __launch_bounds__(NT * GR, GR > 1 ? 1 : 2) scan_bwd_kernel(ScanP
 #pragma unroll
             for (int i = 0; i < V; ++i) d[r][i] = 0.f;
         if (k >= skip) {
-            const int st = (k - from) / GR % STAGES;
-            if ((V > 1 || p.covered > 0) && !lost) lost = !wait_phase(&sm.bars[2 + st], (uint32_t)((k - from) / GR / STAGES) & 1u);
+            const int st = (k - skip) % STAGES;
+            if ((V > 1 || p.covered > 0) && !lost) lost = !wait_phase(&sm.bars[2 + st], (uint32_t)((k - skip) / STAGES) & 1u);
             if constexpr (V > 1) {
 #pragma unroll
                 for (int r = 0; r < R; ++r) {
@@ -651,11 +609,11 @@ __global__ void __launch_bounds__(NT * GR, GR > 1 ? 1 : 2) scan_bwd_kernel(ScanP
 #pragma unroll
             for (int i = 0; i < V; ++i) sm.down[l.warp][l.c + i] = make_float2(dA[i], M[i]);
         }
-        group_sync<GR>(grp);
-        if (k >= skip) fetch(k + STAGES * GR);            // the stage of turn k is in registers
-        if (l.warp == 0) warp_starts<false, GR>(sm.down, xch, sm.bars, sm.start, carry, lost, k, turns, rank, ncl);
-        else if (l.warp == 1) warp_starts<true, 1>(sm.up, nullptr, nullptr, sm.before, state, lost, k, turns, 0, 1);
-        group_sync<GR>(grp);
+        __syncthreads();
+        if (k >= skip) fetch(k + STAGES);            // the stage of turn k is in registers
+        if (l.warp == 0) warp_starts<false, CH>(sm.down, xch, sm.bars, sm.start, carry, lost, k, rank, ncl);
+        else if (l.warp == 1) warp_starts<true, CH>(sm.up, nullptr, nullptr, sm.before, state, lost, k, 0, 1);
+        __syncthreads();
         float s[V], m[V], before[R][V];
         run_start<V>(&sm.before[l.warp][l.c], exA, exH, s);
         run_start<V>(&sm.start[l.warp][l.c], exD, exM, m);
@@ -696,8 +654,7 @@ __global__ void __launch_bounds__(NT * GR, GR > 1 ? 1 : 2) scan_bwd_kernel(ScanP
         });
     }
     if (ncl > 1) cluster_sync_relaxed();
-    if (p.dh0 && rank == 0 && l.warp == 0 && grp == (turns - 1) % GR && lane_c < p.D)
-        p.dh0[(size_t)b * p.D + lane_c] = carry.v;
+    if (p.dh0 && rank == 0 && lane_on) p.dh0[(size_t)b * p.D + lane_c] = carry;
 }
 
 // One token per sequence: elementwise, V channels per thread.

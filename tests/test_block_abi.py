@@ -59,7 +59,7 @@ def test_scan_refusals(G):
     for missing in ("ck", "dx", "dg"):
         assert bwd(desc(), **{missing: None}) == G.GDR_ERR_INVALID_ARG
         assert bwd(desc(), **{missing: HALF}) == G.GDR_ERR_INVALID_ARG
-    for bad in (dict(B=1 << 27), dict(T=(1 << 30) + 1), dict(D=65535 * 32 + 1)):
+    for bad in (dict(B=1 << 27), dict(T=(1 << 30) + 1), dict(D=65535 * 16 + 1)):
         assert fwd(desc(**bad)) == G.GDR_ERR_UNSUPPORTED and bwd(desc(**bad)) == G.GDR_ERR_UNSUPPORTED
     assert step(desc(), h=None) == G.GDR_ERR_INVALID_ARG
     assert step(desc(), o=ODD) == G.GDR_ERR_INVALID_ARG and step(desc(), h=HALF) == G.GDR_ERR_INVALID_ARG
