@@ -326,10 +326,16 @@ __global__ void __launch_bounds__(GNT) beam_group_kernel(BeamParams p) {
 
     float2 mine = make_float2(-INFINITY, 0.f);      // of beam `warp`, its piece `lane`
     if (warp < p.K && lane < p.pieces) mine = p.sums[((size_t)g * p.K + warp) * p.pieces + lane];
-    // this thread's candidates: beam, position in its lists, logit and token.  A warp's lanes lie
-    // evenly over all beams and pieces, so that every warp has some of the best.
+    // this thread's candidates: beam, position in its lists, logit and token.  Few of them: a warp's
+    // lanes lie evenly over all beams and pieces, so that every warp has some of the best; many: one
+    // behind the other, so that every thread has some of every beam.
+    const bool few = n <= HELD * GNT;
     const int span = (n + 31) / 32;
-    auto index = [&](int u) { const int j = warp + u * GWARPS; return j < span ? lane * span + j : n; };
+    auto index = [&](int u) {
+        if (!few) return (int)threadIdx.x + u * GNT;
+        const int j = warp + u * GWARPS;
+        return j < span ? lane * span + j : n;
+    };
     int hk[HELD], hj[HELD], ht[HELD];
     float hx[HELD];
 #pragma unroll
@@ -400,12 +406,21 @@ __global__ void __launch_bounds__(GNT) beam_group_kernel(BeamParams p) {
             Cand c;
             if (index(u) < n && score_of(hk[u], hj[u], ht[u], hx[u], c)) f(c);
         }
-        for (int u = HELD; warp + u * GWARPS < span; ++u) {
-            const int i = index(u);
-            if (i >= n) continue;
-            const size_t at = (size_t)g * n + i;
-            Cand c;
-            if (score_of(i / per, i % per, p.token[at], p.best[at], c)) f(c);
+        if (few) return;
+        for (int i0 = threadIdx.x + HELD * GNT; i0 < n; i0 += 4 * GNT) {
+            int t[4];
+            float x[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {           // four loads in flight
+                const int i = i0 + u * GNT;
+                if (i < n) { t[u] = p.token[(size_t)g * n + i]; x[u] = p.best[(size_t)g * n + i]; }
+            }
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const int i = i0 + u * GNT;
+                Cand c;
+                if (i < n && score_of(i / per, i % per, t[u], x[u], c)) f(c);
+            }
         }
     };
     // one more than asked for: the candidate behind the last may be too near to it
@@ -414,7 +429,7 @@ __global__ void __launch_bounds__(GNT) beam_group_kernel(BeamParams p) {
     for (int turn = 0; turn < 2; ++turn) {
         unsigned mine = 0;
         each([&](const Cand& c) { mine = max(mine, key_of_score(c.s)); });
-        const int active = 32 * min(GWARPS, span), lanes = group_lanes(active, want);
+        const int active = few ? 32 * min(GWARPS, span) : GNT, lanes = group_lanes(active, want);
         put_marks(mine, lanes, active, marks);
         if (threadIdx.x == 0) { count = 0; the_mark = 0; }
         if (threadIdx.x <= p.M) first[threadIdx.x] = Cand{-INFINITY, -1};
