@@ -568,7 +568,7 @@ GDR_API gdr_status gdr_layernorm_bwd(const gdr_norm_desc* desc, const void* x, c
  */
 typedef struct {
     int G, K, V, M;       /* groups, beams (1..64), vocabulary, candidates out (1..64, <= K * V); K * V < 2^31,
-                             G * K < 2^31, V at most 134215680 */
+                             G * K < 2^31 */
     long long row;        /* elements from one beam's logits to the next (>= V; 0: V) */
     gdr_dtype x_dtype;    /* logits */
     int eos;              /* 0 .. V - 1; read only with `finished` */
@@ -593,7 +593,8 @@ GDR_API gdr_status gdr_beam_select(const gdr_beam_desc* desc, const void* logits
  * S is [L, G, K] states of state_bytes each (decode states [N,H,dv,dk] with N = G * K, Raven's
  * slots, the scan's h; any element type and alignment), parent [G,K] int (4-byte aligned).  Beams that keep their state are not
  * moved.  A parent outside 0 .. K-1 leaves its beam as it is and sets the status word
- * (gdr_query_device_status -> GDR_ERR_INDEX).  One launch, no workspace.
+ * (gdr_query_device_status -> GDR_ERR_INDEX).  One launch for 65535 groups (of all layers), no
+ * workspace.
  */
 typedef struct {
     int L, G, K;          /* layers, groups (L * G < 2^31), beams per group (1..64) */

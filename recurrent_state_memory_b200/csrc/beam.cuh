@@ -149,7 +149,9 @@ __global__ void __launch_bounds__(NT, E > 8 && sizeof(XT) == 4 ? 4 : 6) beam_row
     __shared__ int count;
     __shared__ unsigned long long pick[WARPS];
     __shared__ unsigned long long list[LIST];       // key, then the token's complement: larger is better
-    const int row = blockIdx.x, piece = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int row = blockIdx.z * gridDim.y + blockIdx.y, piece = blockIdx.x;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    if (row >= p.G * p.K) return;
     asm volatile("griddepcontrol.launch_dependents;");               // the groups' blocks may come; they wait
     const int v0 = piece * p.piece, n = min(p.piece, p.V - v0);      // this block's tokens
     const XT* x = static_cast<const XT*>(p.logits) + (size_t)row * p.row + v0;
@@ -304,8 +306,8 @@ __device__ double exact_lse(const BeamParams& p, int row, double big, double* re
     return big + log(s);
 }
 
-// GNT threads: as many as there are candidates for, 256 or 1024.
-template <typename XT, int GNT>
+// GNT threads: as many as there are candidates for, 256 or 1024.  FEW: all of them stay in registers.
+template <typename XT, int GNT, bool FEW>
 __global__ void __launch_bounds__(GNT) beam_group_kernel(BeamParams p) {
     constexpr int GWARPS = GNT / 32;
     __shared__ __align__(16) unsigned marks[MARKS];
@@ -329,10 +331,9 @@ __global__ void __launch_bounds__(GNT) beam_group_kernel(BeamParams p) {
     // this thread's candidates: beam, position in its lists, logit and token.  Few of them: a warp's
     // lanes lie evenly over all beams and pieces, so that every warp has some of the best; many: one
     // behind the other, so that every thread has some of every beam.
-    const bool few = n <= HELD * GNT;
     const int span = (n + 31) / 32;
     auto index = [&](int u) {
-        if (!few) return (int)threadIdx.x + u * GNT;
+        if (!FEW) return (int)threadIdx.x + u * GNT;
         const int j = warp + u * GWARPS;
         return j < span ? lane * span + j : n;
     };
@@ -406,8 +407,7 @@ __global__ void __launch_bounds__(GNT) beam_group_kernel(BeamParams p) {
             Cand c;
             if (index(u) < n && score_of(hk[u], hj[u], ht[u], hx[u], c)) f(c);
         }
-        if (few) return;
-        for (int i0 = threadIdx.x + HELD * GNT; i0 < n; i0 += 4 * GNT) {
+        for (int i0 = threadIdx.x + HELD * GNT; !FEW && i0 < n; i0 += 4 * GNT) {
             int t[4];
             float x[4];
 #pragma unroll
@@ -429,7 +429,7 @@ __global__ void __launch_bounds__(GNT) beam_group_kernel(BeamParams p) {
     for (int turn = 0; turn < 2; ++turn) {
         unsigned mine = 0;
         each([&](const Cand& c) { mine = max(mine, key_of_score(c.s)); });
-        const int active = few ? 32 * min(GWARPS, span) : GNT, lanes = group_lanes(active, want);
+        const int active = FEW ? 32 * min(GWARPS, span) : GNT, lanes = group_lanes(active, want);
         put_marks(mine, lanes, active, marks);
         if (threadIdx.x == 0) { count = 0; the_mark = 0; }
         if (threadIdx.x <= p.M) first[threadIdx.x] = Cand{-INFINITY, -1};
@@ -509,6 +509,7 @@ __global__ void __launch_bounds__(GNT) beam_group_kernel(BeamParams p) {
 
 struct ReorderParams {
     int G, K;
+    int first;              // layer * G + group of the grid's first
     size_t n;               // elements (of the kernel's width) of one state
     char* S;
     const int* parent;
@@ -518,14 +519,14 @@ struct ReorderParams {
 // over, and only then writes, so that the exchange needs no second buffer and no other thread.
 template <typename VT, int KMAX>
 __global__ void __launch_bounds__(NT) reorder_kernel(ReorderParams p) {
-    const int g = blockIdx.x % p.G;
+    const int g = (p.first + blockIdx.y) % p.G;
     const int* parent = p.parent + (size_t)g * p.K;
-    VT* S = reinterpret_cast<VT*>(p.S) + (size_t)blockIdx.x * p.K * p.n;
-    if (blockIdx.y == 0 && blockIdx.x < p.G && threadIdx.x < p.K) {
+    VT* S = reinterpret_cast<VT*>(p.S) + (size_t)blockIdx.y * p.K * p.n;
+    if (blockIdx.x == 0 && p.first + (int)blockIdx.y < p.G && threadIdx.x < p.K) {
         const int q = parent[threadIdx.x];
         if (q < 0 || q >= p.K) atomicOr(&g_device_status, STATUS_INDEX);
     }
-    for (size_t i = (size_t)blockIdx.y * NT + threadIdx.x; i < p.n; i += (size_t)gridDim.y * NT) {
+    for (size_t i = (size_t)blockIdx.x * NT + threadIdx.x; i < p.n; i += (size_t)gridDim.x * NT) {
         VT v[KMAX];
         bool moves[KMAX];
 #pragma unroll

@@ -111,8 +111,7 @@ def test_beam_refusals(G):
     assert call(None) == G.GDR_ERR_INVALID_ARG
     for bad in (dict(G=-1), dict(V=0), dict(row=99), dict(x_dtype=5), dict(V=2, K=3, M=7)):
         assert call(desc(**bad)) == G.GDR_ERR_INVALID_ARG, bad
-    for bad in (dict(K=0), dict(K=65), dict(M=0), dict(M=65), dict(V=1 << 29), dict(K=1, V=(1 << 27)),
-                dict(G=1 << 30)):
+    for bad in (dict(K=0), dict(K=65), dict(M=0), dict(M=65), dict(V=1 << 29), dict(G=1 << 30)):
         assert call(desc(**bad)) == G.GDR_ERR_UNSUPPORTED, bad
         assert L.gdr_beam_select_workspace_bytes(desc(**bad)) == 0
     for eos in (-1, 100):
