@@ -11,16 +11,18 @@ namespace gdr {
 namespace lnm {
 
 // How a row of D elements is held: V elements a load, N loads a lane, G lanes (of a warp, or a block
-// of G threads); N = 0: the row is too long for a block's registers.
-struct Plan { int V, N, G; };
+// of G threads); N = 0: the row is too long for a block's registers.  Shifted: rows of V-element
+// chunks that begin and end inside one.
+struct Plan { int V, N, G; bool shift; };
 
 // A warp while a lane holds at most 16 elements (one by one, and in the backward, which also holds
-// dy, the weights and two sums: 8), then the smallest block whose threads hold the row in as many.
-// (Forward of 33.5 M bf16 elements: rows of 1024 in 32 elements a lane of a warp 32.3 us, in 8 of 128
-// threads 28.6; rows of 4096 in 32 of 128 threads 34.0, in 16 of 256 32.0.)
-static Plan plan_of(int D, int V, bool bwd) {
-    Plan q{V, 0, 32};
-    const int nv = (D + V - 1) / V;             // loads of a row
+// dy, the weights and two sums: 8), then the block that holds the fewest elements beside the row.
+// 33.5 M bf16 elements: rows of 1024 in 32 elements a lane of a warp 32.3 us forward, in 8 of 128
+// threads 28.0; rows of 2560 in 16 of 192 27.8, of 256 37.7; backward, rows of 512 in 64 threads
+// 39.7 us, in 128 54.2, rows of 6144 in 768 49.1, in 1024 56.6.
+static Plan plan_of(int D, int V, bool bwd, bool shift) {
+    Plan q{V, 0, 32, shift};
+    const int nv = (D + (shift ? 2 * V - 2 : V - 1)) / V;       // loads of a row
     if (nv <= 32) {                             // one load a lane, as few lanes as hold the row
         q.N = 1;
         for (q.G = 1; q.G < nv; q.G *= 2) {}
@@ -29,58 +31,75 @@ static Plan plan_of(int D, int V, bool bwd) {
     const int most = (bwd || V == 1 ? 8 : 16) / V;
     for (int n = 2; n <= most; n *= 2)
         if (nv <= 32 * n) { q.N = n; return q; }
-    for (int g : {128, 256, 512, 1024})
-        for (int n = V == 1 ? 4 : bwd ? most : 1; n <= most; n *= 2)
-            if (nv <= g * n) { q.G = g; q.N = n; return q; }
-    if (!bwd && V == 1 && nv <= 16 * 1024) { q.G = 1024; q.N = 16; }
+    int held = 1 << 20;
+    for (int g : {64, 96, 128, 192, 256, 384, 512, 768, 1024})
+        for (int n = V == 1 || bwd ? most : 1; n <= most; n *= 2) {
+            if (nv > g * n || g * n > held || (n < most && g > 128)) continue;
+            held = g * n;
+            q.G = g;
+            q.N = n;
+        }
+    if (!bwd && V == 1 && !q.N && nv <= 16 * 1024) { q.G = 1024; q.N = 16; }
     return q;
 }
-static int rows_of_block(const Plan& q) { return q.N && q.G <= 32 ? WARP_NT / q.G : 1; }
-static int vector_of(const gdr_norm_desc* d) {  // elements of a load: 16 bytes, where every row starts on them
-    const int V = d->x_dtype == GDR_BF16 && d->y_dtype == GDR_BF16 ? 8 : 4;
-    return d->D % V == 0 ? V : 1;
+// Rows of D elements where 16-byte access takes V of them.  Rows that are not multiples of it:
+// shifted, where that holds no more elements than one by one, and forward with weights in registers
+// and, of fp32, one load a lane.  (33.5 M bf16 elements, shifted against one by one: backward rows of
+// 9 66 and 247 us, 333 60 and 73, 5001 68 and 117; but 250, a block in place of a warp, 77 and 52.
+// Forward 9 68 and 147, 5001 44 and 59; 16.8 M fp32, rows of 2047 64 and 23.)
+static Plan plan(int D, int V, bool bwd) {
+    if (D % V == 0) return plan_of(D, V, bwd, false);
+    const Plan one = plan_of(D, 1, bwd, false), q = plan_of(D, V, bwd, true);
+    const bool fits = q.N && q.V * q.N * q.G <= (one.N ? one.N * one.G : 1 << 20) && (bwd || (q.G < 1024 && (V == 8 || q.N == 1)));
+    return D > V && fits ? q : one;             // D > V: a chunk reaches into one neighbouring row at most
 }
+static int rows_of_block(const Plan& q) { return q.N && q.G <= 32 ? WARP_NT / q.G : 1; }
+static int vector_of(const gdr_norm_desc* d) { return d->x_dtype == GDR_BF16 && d->y_dtype == GDR_BF16 ? 8 : 4; }
 
-template <typename XT, typename YT, int V, int N, int G, bool BWD>
+template <typename XT, typename YT, int V, int N, int G, bool BWD, bool SHIFT>
 static gdr_status launch_one(const NormParams& p, cudaStream_t st) {
     constexpr int NTH = threads<G>(), per = NTH / G, U = rows_at_once<V, N, G>();
     if constexpr (!BWD) {
-        const long long blocks = (p.rows + per * U - 1) / (per * U), cap = (long long)device_sm_count() * (1024 / NTH);
-        norm_fwd_kernel<XT, YT, V, N, G><<<(unsigned)(blocks < cap ? blocks : cap), NTH, 0, st>>>(p);
+        constexpr int M = SHIFT && per % V ? V : 1;    // shifted: the grid's groups in multiples of V
+        const long long blocks = (p.rows + per * U - 1) / (per * U), cap = (long long)device_sm_count() * fwd_blocks<SHIFT>(V, N, NTH);
+        const long long grid = blocks + M - 1 < cap ? blocks + M - 1 : cap;
+        norm_fwd_kernel<XT, YT, V, N, G, SHIFT><<<(unsigned)(grid < M ? M : grid / M * M), NTH, 0, st>>>(p);
     } else {
         // the groups' sums in turn: at most 256 threads x 16 columns
         const size_t smem = per == 1 || !(p.part_w || p.part_b) ? 0 : (size_t)per * p.D * sizeof(float);
-        norm_bwd_kernel<XT, YT, V, N, G><<<p.parts, NTH, smem, st>>>(p);
+        norm_bwd_kernel<XT, YT, V, N, G, SHIFT><<<p.parts, NTH, smem, st>>>(p);
     }
     const cudaError_t e = cudaGetLastError();
     return e == cudaSuccess ? GDR_OK : cuda_fail(e, "launch(layer norm)");
 }
 
 // The kernels that plan_of reaches.
-template <typename XT, typename YT, int V, bool BWD>
+template <typename XT, typename YT, int V, bool BWD, bool SHIFT>
 static gdr_status launch_plan(const Plan& q, const NormParams& p, cudaStream_t st) {
-#define GDR_NORM(n, g) if (q.N == n && q.G == g) return launch_one<XT, YT, V, n, g, BWD>(p, st)
-    GDR_NORM(1, 1); GDR_NORM(1, 2); GDR_NORM(1, 4); GDR_NORM(1, 8); GDR_NORM(1, 16); GDR_NORM(1, 32);
-    if constexpr (!BWD) {
-        GDR_NORM(2, 32);
-        if constexpr (V == 8) {
-            GDR_NORM(1, 128); GDR_NORM(2, 128); GDR_NORM(2, 256); GDR_NORM(2, 512); GDR_NORM(2, 1024);
-        } else if constexpr (V == 4) {
-            GDR_NORM(4, 32); GDR_NORM(2, 128); GDR_NORM(4, 128); GDR_NORM(4, 256); GDR_NORM(4, 512); GDR_NORM(4, 1024);
-        } else {
-            GDR_NORM(4, 32); GDR_NORM(8, 32);
-            GDR_NORM(4, 128); GDR_NORM(8, 128); GDR_NORM(8, 256); GDR_NORM(8, 512); GDR_NORM(8, 1024); GDR_NORM(16, 1024);
-        }
-    } else if constexpr (V == 8) {
-        GDR_NORM(1, 128); GDR_NORM(1, 256); GDR_NORM(1, 512); GDR_NORM(1, 1024);
-    } else if constexpr (V == 4) {
-        GDR_NORM(2, 32); GDR_NORM(2, 128); GDR_NORM(2, 256); GDR_NORM(2, 512); GDR_NORM(2, 1024);
-    } else {
-        GDR_NORM(2, 32); GDR_NORM(4, 32); GDR_NORM(8, 32);
-        GDR_NORM(4, 128); GDR_NORM(8, 128); GDR_NORM(8, 256); GDR_NORM(8, 512); GDR_NORM(8, 1024);
+#define GDR_NORM(n, g) if (q.N == n && q.G == g) return launch_one<XT, YT, V, n, g, BWD, SHIFT>(p, st)
+    constexpr int MOST = (BWD || V == 1 ? 8 : 16) / V;
+    if constexpr (!SHIFT) GDR_NORM(1, 1);
+    GDR_NORM(1, 2); GDR_NORM(1, 4); GDR_NORM(1, 8); GDR_NORM(1, 16); GDR_NORM(1, 32);
+    if constexpr (BWD || V != 4 || !SHIFT) {
+        if constexpr (MOST >= 2) GDR_NORM(2, 32);
+        if constexpr (MOST >= 4) GDR_NORM(4, 32);
+        if constexpr (MOST >= 8) GDR_NORM(8, 32);
+        if constexpr (V == 8 && !BWD) { GDR_NORM(1, 96); GDR_NORM(1, 128); }
+        if constexpr (V == 4 && !BWD) { GDR_NORM(2, 96); GDR_NORM(2, 128); }
+        if constexpr (V == 1 || BWD) GDR_NORM(MOST, 64);
+        GDR_NORM(MOST, 96); GDR_NORM(MOST, 128); GDR_NORM(MOST, 192); GDR_NORM(MOST, 256); GDR_NORM(MOST, 384);
+        GDR_NORM(MOST, 512); GDR_NORM(MOST, 768);
+        if constexpr (BWD || !SHIFT) GDR_NORM(MOST, 1024);
+        if constexpr (V == 1 && !BWD) GDR_NORM(16, 1024);
     }
 #undef GDR_NORM
     return fail(GDR_ERR_UNSUPPORTED, "layer norm: no kernel for this plan%s");
+}
+
+template <typename XT, typename YT, int V, bool BWD>
+static gdr_status launch_width(const Plan& q, const NormParams& p, cudaStream_t st) {
+    if (q.V == 1) return launch_plan<XT, YT, 1, BWD, false>(q, p, st);
+    return q.shift ? launch_plan<XT, YT, V, BWD, true>(q, p, st) : launch_plan<XT, YT, V, BWD, false>(q, p, st);
 }
 
 template <typename XT, typename YT>
@@ -89,12 +108,12 @@ static gdr_status launch(const gdr_norm_desc* d, bool bwd, NormParams& p, cudaSt
     // one element a load where a tensor does not start on 16 bytes
     bool on16 = true;
     for (const void* a : {p.x, p.dy, p.weight, p.bias, (const void*)p.y, (const void*)p.dx}) on16 = on16 && aligned16(a);
-    const Plan q = plan_of(p.D, on16 ? vector_of(d) : 1, bwd);
+    const Plan q = plan(p.D, on16 ? vector_of(d) : 1, bwd);
     p.w_bf16 = d->w_dtype == GDR_BF16;
     gdr_status s = GDR_OK;
     if (p.rows > 0) {
-        if (q.N && bwd) s = q.V > 1 ? launch_plan<XT, YT, V, true>(q, p, st) : launch_plan<XT, YT, 1, true>(q, p, st);
-        else if (q.N) s = q.V > 1 ? launch_plan<XT, YT, V, false>(q, p, st) : launch_plan<XT, YT, 1, false>(q, p, st);
+        if (q.N && bwd) s = launch_width<XT, YT, V, true>(q, p, st);
+        else if (q.N) s = launch_width<XT, YT, V, false>(q, p, st);
         else {
             const unsigned grid = (unsigned)(p.rows < 2 * device_sm_count() ? p.rows : 2 * device_sm_count());
             if (!bwd) norm_fwd_long_kernel<XT, YT><<<grid, LONG_NT, 0, st>>>(p);
@@ -133,10 +152,12 @@ static gdr_status launch(const gdr_norm_desc* d, bool bwd, NormParams& p, cudaSt
 // Blocks of the backward, each with a partial row of its own: 512 threads per SM, and at least
 // eight rows for each of a block's groups, so that the partial rows stay few against the rows.
 static int parts_of(const gdr_norm_desc* d) {
-    const Plan q = plan_of(d->D, vector_of(d), true);
+    const Plan q = plan(d->D, vector_of(d), true);
     const long long per = rows_of_block(q), n = (d->rows + 8 * per - 1) / (8 * per);
-    const long long cap = (long long)device_sm_count() * (q.N && q.G < 512 ? 512 / (q.G > 32 ? q.G : WARP_NT) : q.N ? 1 : 2);
-    return (int)(n < 1 ? 1 : n < cap ? n : cap);
+    const long long cap = (long long)device_sm_count() * (q.N ? bwd_blocks(q.G > 32 ? q.G : WARP_NT) : 2);
+    // shifted rows of a block: blocks in multiples of V, but no more than stay on the GPU
+    const long long M = q.shift && per % q.V ? q.V : 1, parts = n < cap ? n + M - 1 : cap;
+    return (int)(parts < M ? M : (parts < cap ? parts : cap) / M * M);
 }
 
 static gdr_status dispatch(const gdr_norm_desc* d, bool bwd, NormParams& p, cudaStream_t st) {

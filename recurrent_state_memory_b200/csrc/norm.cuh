@@ -122,6 +122,25 @@ template <typename T, int V> struct Raw {
 #pragma unroll
         for (int i = 0; i < WORDS; ++i) w[i] = 0u;
     }
+    __device__ __forceinline__ void ones(int c, int D) {                // ones where column c + i is in the row
+        zero();
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            if ((unsigned)(c + i) < (unsigned)D) w[i * (int)sizeof(T) / 4] |= sizeof(T) == 4 ? 0xffffffffu : i & 1 ? 0xffff0000u : 0xffffu;
+    }
+    __device__ __forceinline__ void operator&=(const Raw& m) {
+#pragma unroll
+        for (int i = 0; i < WORDS; ++i) w[i] &= m.w[i];
+    }
+    __device__ __forceinline__ void load_part(const T* p, int n) {      // the first n elements; the others 0
+        zero();
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            if (i >= n) continue;
+            if constexpr (sizeof(T) == 4) w[i] = *reinterpret_cast<const unsigned*>(p + i);
+            else w[i / 2] |= (unsigned)*reinterpret_cast<const unsigned short*>(p + i) << (i & 1 ? 16 : 0);
+        }
+    }
     __device__ __forceinline__ float get(int i) const {
         if constexpr (sizeof(T) == 4) return __uint_as_float(w[i]);
         else return __uint_as_float(i & 1 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
@@ -222,30 +241,85 @@ constexpr int WARP_NT = 256;            // threads of a block of the warp kernel
 // Threads of a block whose rows belong to G lanes each.
 template <int G> constexpr int threads() { return G > 32 ? G : WARP_NT; }
 
-// Where this thread stands: its lane in its row's group, its (first) row in the block's first
-// turn, and the rows of a turn of the grid.  A group's U rows of a turn are PER apart.
-template <int G, int U> struct Place {
+// Blocks on an SM (and of the grid, which walks the rows): forward 1024 threads of 64 registers, 768
+// of 80 where rows are shifted or two loads of pairs are held, 512 of 128 where a lane holds 16
+// elements; backward 512 of 128.
+template <bool SHIFT> __host__ __device__ constexpr int fwd_blocks(int V, int N, int threads) {
+    const int most = V * N > 8 ? (threads <= 192 && !SHIFT ? 576 : 512) : SHIFT || (V > 1 && N > 1) ? 768 : 1024;
+    return threads <= most ? most / threads : 1;
+}
+__host__ __device__ constexpr int bwd_blocks(int threads) { return threads <= 256 ? 512 / threads : 1; }
+
+// Where this thread stands: its lane in its row's group, its (first) row in the first turn, the
+// distance of a group's U rows of a turn, the rows of a turn of the grid, and the thread's first
+// column.  Shifted: rows that do not start on 16 bytes.  Rows V apart start alike, so a group whose
+// rows are multiples of V apart (the host makes the grid's groups one) still has columns of its own:
+// its chunks are the tensor's 16-byte chunks, and the row begins and ends inside one.
+template <int V, int G, int U, bool SHIFT> struct Place {
     static constexpr int PER = threads<G>() / G;      // groups of a block
-    int lane;
-    long long row, step;
-    __device__ __forceinline__ Place()
-        : lane(threadIdx.x % G), row((long long)blockIdx.x * (PER * U) + threadIdx.x / G),
-          step((long long)gridDim.x * (PER * U)) {}
+    int lane, c0;
+    long long row, dist, step;
+    __device__ __forceinline__ Place(int D)
+        : lane(threadIdx.x % G), row((long long)blockIdx.x * (SHIFT ? PER : PER * U) + threadIdx.x / G),
+          dist(SHIFT ? (long long)gridDim.x * PER : PER), step((long long)gridDim.x * (PER * U)) {
+        c0 = lane * V - (SHIFT ? (int)((unsigned long long)row * (unsigned)D % V) : 0);
+    }
 };
+// A chunk with columns outside of the row.
+template <int V, bool SHIFT> __device__ __forceinline__ bool ragged(int c, int D) { return SHIFT && (c < 0 || c + V > D); }
+template <int V> __device__ __forceinline__ void only_row(Vals<V>& v, int c, int D) {
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+        if ((unsigned)(c + i) >= (unsigned)D) v.set(i, 0.f);
+}
+// A row's last chunk at the tensor's end: left out of the loads ahead (a load within a branch would
+// wait there), read by elements where it is used.  Elsewhere a chunk is read whole; its other
+// columns are the neighbouring rows'.
+template <int V, bool SHIFT> __device__ __forceinline__ bool at_end(int c, int D, bool last) { return SHIFT && last && c + V > D; }
+template <bool SHIFT, typename T, int V> __device__ __forceinline__ void store_chunk(T* p, const Vals<V>& v, int c, int D) {
+    if (ragged<V, SHIFT>(c, D)) {
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            if ((unsigned)(c + i) < (unsigned)D) st_from_f32(p + i, v.get(i));
+    } else {
+        store_v<T, V>(p, v);
+    }
+}
+// Sums: the partial rows' starts are not shifted, so a shifted chunk has no alignment there.
+template <bool SHIFT, int V> __device__ __forceinline__ void store_part(float* p, const Vals<V>& v, int c, int D) {
+    if constexpr (SHIFT) {
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            if ((unsigned)(c + i) < (unsigned)D) p[i] = v.get(i);
+    } else {
+        store_v<float, V>(p, v);
+    }
+}
+// Weights or biases of a chunk; outside of the row: 0.
+template <typename WT, int V, bool SHIFT> __device__ __forceinline__ Vals<V> load_chunk_w(const void* p, int c, int D) {
+    if constexpr (SHIFT) {
+        Vals<V> v;
+#pragma unroll
+        for (int i = 0; i < V; ++i) v.set(i, (unsigned)(c + i) < (unsigned)D ? load_w<WT, 1>(p, c + i).v : 0.f);
+        return v;
+    } else {
+        return load_w<WT, V>(p, c);
+    }
+}
 
 // Rows that a group takes per turn: two while a row is few registers, so that more loads are in
 // flight and, in a block, two rows share a barrier.
-template <int V, int N, int G> constexpr int rows_at_once() { return V * N <= (V == 1 ? 4 : 8) && G < 1024 ? 2 : 1; }
+template <int V, int N, int G> constexpr int rows_at_once() { return V * N <= (V == 1 ? 4 : 8) && G < 768 ? 2 : 1; }
 
 // N loads of V elements per lane and row.
-template <typename XT, typename YT, int V, int N, int G>
-__global__ void __launch_bounds__(threads<G>(), V * N <= 8 ? 1024 / threads<G>() : 1) norm_fwd_kernel(NormParams p) {
+template <typename XT, typename YT, int V, int N, int G, bool SHIFT>
+__global__ void __launch_bounds__(threads<G>(), fwd_blocks<SHIFT>(V, N, threads<G>())) norm_fwd_kernel(NormParams p) {
     constexpr int U = rows_at_once<V, N, G>();
     __shared__ __align__(16) float sm[2][G > 32 ? G / 32 : 1][U];
-    const Place<G, U> at;
+    const Place<V, G, U, SHIFT> at(p.D);
     Group<G, U> grp{sm, 0};
     const float inv = 1.f / (float)p.D;
-    const int c0 = at.lane * V;                       // this lane's columns: c0 + j * G * V ..
+    const int c0 = at.c0;                             // this lane's columns: c0 + j * G * V ..
     constexpr bool KEEP = V * N <= 16 && G < 1024;    // weights stay in registers
     Vals<V> w[KEEP ? N : 1], bi[KEEP ? N : 1];
     auto weights = [&](auto type, int j, Vals<V>& wv, Vals<V>& bv) {
@@ -253,8 +327,8 @@ __global__ void __launch_bounds__(threads<G>(), V * N <= 8 ? 1024 / threads<G>()
         wv.all(1.f);
         bv.all(0.f);
         if (c < p.D) {
-            if (p.weight) wv = load_w<decltype(type), V>(p.weight, c);
-            if (p.bias) bv = load_w<decltype(type), V>(p.bias, c);
+            if (p.weight) wv = load_chunk_w<decltype(type), V, SHIFT>(p.weight, c, p.D);
+            if (p.bias) bv = load_chunk_w<decltype(type), V, SHIFT>(p.bias, c, p.D);
         }
     };
     if constexpr (KEEP) {
@@ -263,7 +337,7 @@ __global__ void __launch_bounds__(threads<G>(), V * N <= 8 ? 1024 / threads<G>()
             for (int j = 0; j < N; ++j) weights(type, j, w[j], bi[j]);
         });
     }
-    const size_t jump = (size_t)at.step * p.D, next = (size_t)at.PER * p.D;
+    const size_t jump = (size_t)at.step * p.D, next = (size_t)at.dist * p.D;
     const XT* x = static_cast<const XT*>(p.x) + (size_t)at.row * p.D + c0;      // the rows to fetch next
     YT* y = static_cast<YT*>(p.y) + (size_t)at.row * p.D + c0;
     Raw<XT, V> raw[U][N];
@@ -272,11 +346,27 @@ __global__ void __launch_bounds__(threads<G>(), V * N <= 8 ? 1024 / threads<G>()
         for (int u = 0; u < U; ++u)
 #pragma unroll
             for (int j = 0; j < N; ++j) {
-                if (r + u * at.PER < p.rows && c0 + j * G * V < p.D) raw[u][j].load(x + u * next + j * G * V);
+                const int c = c0 + j * G * V;
+                if (r + u * at.dist < p.rows && c < p.D && !at_end<V, SHIFT>(c, p.D, r + u * at.dist == p.rows - 1))
+                    raw[u][j].load(x + u * next + j * G * V);
                 else raw[u][j].zero();
             }
         x += jump;
     };
+    // the chunks' elements that are the row's, as bits of the raw words and as ones of the values
+    constexpr bool ONES = SHIFT && V * N <= 8;
+    Raw<XT, V> mx[SHIFT ? N : 1];
+    Vals<V> ones[ONES ? N : 1];
+    if constexpr (SHIFT) {
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            mx[j].ones(c0 + j * G * V, p.D);
+            if constexpr (ONES) {
+                ones[j].all(1.f);
+                only_row(ones[j], c0 + j * G * V, p.D);
+            }
+        }
+    }
     fetch(at.row);
     // every lane of a warp makes the same number of turns (the sums are warp-wide)
     const long long ahead = G > 32 ? 0 : (threadIdx.x & 31) / G;
@@ -287,6 +377,12 @@ __global__ void __launch_bounds__(threads<G>(), V * N <= 8 ? 1024 / threads<G>()
         for (int u = 0; u < U; ++u) {
 #pragma unroll
             for (int j = 0; j < N; ++j) {
+                if constexpr (SHIFT) {
+                    const int c = c0 + j * G * V;
+                    if (c < p.D && at_end<V, SHIFT>(c, p.D, r + u * at.dist == p.rows - 1))
+                        raw[u][j].load_part(x - jump + u * next + j * G * V, p.D - c);
+                    raw[u][j] &= mx[j];
+                }
                 v[u][j] = raw[u][j].vals();
                 s = j ? s + v[u][j] : v[u][j];
             }
@@ -302,7 +398,12 @@ __global__ void __launch_bounds__(threads<G>(), V * N <= 8 ? 1024 / threads<G>()
             s.all(0.f);
 #pragma unroll
             for (int j = 0; j < N; ++j) {
-                v[u][j] = v[u][j] + off;
+                if constexpr (ONES) {
+                    v[u][j] = fma(ones[j], off, v[u][j]);
+                } else {
+                    v[u][j] = v[u][j] + off;
+                    if (ragged<V, SHIFT>(c0 + j * G * V, p.D)) only_row(v[u][j], c0 + j * G * V, p.D);
+                }
                 if (c0 + j * G * V < p.D) s = fma(v[u][j], v[u][j], s);
             }
             rstd[u] = s.total();
@@ -310,13 +411,14 @@ __global__ void __launch_bounds__(threads<G>(), V * N <= 8 ? 1024 / threads<G>()
         grp.sum(rstd);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            if (r + u * at.PER >= p.rows) continue;
+            if (r + u * at.dist >= p.rows) continue;
             rstd[u] = rsqrtf(rstd[u] * inv + p.eps);
             Vals<V> rs;
             rs.all(rstd[u]);
             auto put = [&](int j, const Vals<V>& wv, const Vals<V>& bv) {
                 const Vals<V> o = fma(v[u][j] * rs, wv, bv);
-                if (c0 + j * G * V < p.D && GDR_INB(c0 + j * G * V + V <= p.D, 901)) store_v<YT, V>(y + u * next + j * G * V, o);
+                if (c0 + j * G * V < p.D && GDR_INB(SHIFT || c0 + j * G * V + V <= p.D, 901))
+                    store_chunk<SHIFT>(y + u * next + j * G * V, o, c0 + j * G * V, p.D);
             };
             if constexpr (KEEP) {
 #pragma unroll
@@ -332,8 +434,8 @@ __global__ void __launch_bounds__(threads<G>(), V * N <= 8 ? 1024 / threads<G>()
                 });
             }
             if (at.lane == 0) {
-                if (p.mean) p.mean[r + u * at.PER] = mean[u];
-                if (p.rstd) p.rstd[r + u * at.PER] = rstd[u];
+                if (p.mean) p.mean[r + u * at.dist] = mean[u];
+                if (p.rstd) p.rstd[r + u * at.dist] = rstd[u];
             }
         }
         y += jump;
@@ -341,28 +443,29 @@ __global__ void __launch_bounds__(threads<G>(), V * N <= 8 ? 1024 / threads<G>()
 }
 
 // Backward: dx, and the block's share of dweight and dbias.
-template <typename XT, typename YT, int V, int N, int G>
-__global__ void __launch_bounds__(threads<G>(), G <= 256 ? 512 / threads<G>() : 1) norm_bwd_kernel(NormParams p) {
+template <typename XT, typename YT, int V, int N, int G, bool SHIFT>
+__global__ void __launch_bounds__(threads<G>(), bwd_blocks(threads<G>())) norm_bwd_kernel(NormParams p) {
     constexpr int U = rows_at_once<V, N, G>();
     extern __shared__ float part[];                   // G <= 32: the groups' sums [PER][D], in turn
     __shared__ __align__(16) float sm[2][G > 32 ? G / 32 : 1][2 * U];
-    const Place<G, U> at;
+    const Place<V, G, U, SHIFT> at(p.D);
     Group<G, 2 * U> grp{sm, 0};
     const float inv = 1.f / (float)p.D;
-    const int c0 = at.lane * V;
+    const int c0 = at.c0;
     static_assert(V * N <= 8, "weights, rows and sums in registers");
     Vals<V> w[N];
     with_weights(p, [&](auto type) {
 #pragma unroll
         for (int j = 0; j < N; ++j) {
             w[j].all(1.f);
-            if (c0 + j * G * V < p.D && p.weight) w[j] = load_w<decltype(type), V>(p.weight, c0 + j * G * V);
+            if (c0 + j * G * V < p.D && p.weight)
+                w[j] = load_chunk_w<decltype(type), V, SHIFT>(p.weight, c0 + j * G * V, p.D);
         }
     });
     Vals<V> sw[N], sb[N];
 #pragma unroll
     for (int j = 0; j < N; ++j) { sw[j].all(0.f); sb[j].all(0.f); }
-    const size_t jump = (size_t)at.step * p.D, next = (size_t)at.PER * p.D, start = (size_t)at.row * p.D + c0;
+    const size_t jump = (size_t)at.step * p.D, next = (size_t)at.dist * p.D, start = (size_t)at.row * p.D + c0;
     const XT* x = static_cast<const XT*>(p.x) + start;
     const YT* dy = static_cast<const YT*>(p.dy) + start;
     XT* dx = static_cast<XT*>(p.dx) + start;
@@ -372,12 +475,13 @@ __global__ void __launch_bounds__(threads<G>(), G <= 256 ? 512 / threads<G>() : 
     auto fetch = [&](long long r) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const bool in = r + u * at.PER < p.rows;
-            mean[u] = in ? p.mean[r + u * at.PER] : 0.f;
-            rstd[u] = in ? p.rstd[r + u * at.PER] : 0.f;
+            const bool in = r + u * at.dist < p.rows;
+            mean[u] = in ? p.mean[r + u * at.dist] : 0.f;
+            rstd[u] = in ? p.rstd[r + u * at.dist] : 0.f;
 #pragma unroll
             for (int j = 0; j < N; ++j) {
-                if (in && c0 + j * G * V < p.D) {
+                const int c = c0 + j * G * V;
+                if (in && c < p.D && !at_end<V, SHIFT>(c, p.D, r + u * at.dist == p.rows - 1)) {
                     rx[u][j].load(x + u * next + j * G * V);
                     rd[u][j].load(dy + u * next + j * G * V);
                 } else { rx[u][j].zero(); rd[u][j].zero(); }
@@ -386,6 +490,15 @@ __global__ void __launch_bounds__(threads<G>(), G <= 256 ? 512 / threads<G>() : 
         x += jump;
         dy += jump;
     };
+    Raw<XT, V> mx[SHIFT ? N : 1];                      // the chunks' elements that are the row's
+    Raw<YT, V> my[SHIFT ? N : 1];
+    if constexpr (SHIFT) {
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            mx[j].ones(c0 + j * G * V, p.D);
+            my[j].ones(c0 + j * G * V, p.D);
+        }
+    }
     fetch(at.row);
     const long long ahead = G > 32 ? 0 : (threadIdx.x & 31) / G;
     for (long long r = at.row; r - ahead < p.rows; r += at.step) {
@@ -399,6 +512,15 @@ __global__ void __launch_bounds__(threads<G>(), G <= 256 ? 512 / threads<G>() : 
             off.all(-mean[u]);
 #pragma unroll
             for (int j = 0; j < N; ++j) {             // columns behind D: dy is zero
+                if constexpr (SHIFT) {
+                    const int c = c0 + j * G * V;
+                    if (c < p.D && at_end<V, SHIFT>(c, p.D, r + u * at.dist == p.rows - 1)) {
+                        rx[u][j].load_part(x - jump + u * next + j * G * V, p.D - c);
+                        rd[u][j].load_part(dy - jump + u * next + j * G * V, p.D - c);
+                    }
+                    rx[u][j] &= mx[j];
+                    rd[u][j] &= my[j];
+                }
                 xh[u][j] = (rx[u][j].vals() + off) * rs;
                 d[u][j] = rd[u][j].vals();
                 sw[j] = fma(d[u][j], xh[u][j], sw[j]);
@@ -415,7 +537,7 @@ __global__ void __launch_bounds__(threads<G>(), G <= 256 ? 512 / threads<G>() : 
             grp.sum(c);
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                if (r + u * at.PER >= p.rows) continue;
+                if (r + u * at.dist >= p.rows) continue;
                 Vals<V> m1, m2, rs;
                 rs.all(here[u]);
                 m1.all(-c[2 * u] * inv);
@@ -423,8 +545,8 @@ __global__ void __launch_bounds__(threads<G>(), G <= 256 ? 512 / threads<G>() : 
 #pragma unroll
                 for (int j = 0; j < N; ++j) {
                     const Vals<V> o = (d[u][j] + fma(xh[u][j], m2, m1)) * rs;
-                    if (c0 + j * G * V < p.D && GDR_INB(c0 + j * G * V + V <= p.D, 911))
-                        store_v<XT, V>(dx + u * next + j * G * V, o);
+                    if (c0 + j * G * V < p.D && GDR_INB(SHIFT || c0 + j * G * V + V <= p.D, 911))
+                        store_chunk<SHIFT>(dx + u * next + j * G * V, o, c0 + j * G * V, p.D);
                 }
             }
             dx += jump;
@@ -437,8 +559,8 @@ __global__ void __launch_bounds__(threads<G>(), G <= 256 ? 512 / threads<G>() : 
         for (int j = 0; j < N; ++j) {
             const int c = c0 + j * G * V;
             if (c >= p.D) continue;
-            if (p.part_w) store_v<float, V>(p.part_w + base + c, sw[j]);
-            if (p.part_b) store_v<float, V>(p.part_b + base + c, sb[j]);
+            if (p.part_w) store_part<SHIFT>(p.part_w + base + c, sw[j], c, p.D);
+            if (p.part_b) store_part<SHIFT>(p.part_b + base + c, sb[j], c, p.D);
         }
     } else {
         // the block's groups, added column by column in the groups' order
@@ -450,7 +572,7 @@ __global__ void __launch_bounds__(threads<G>(), G <= 256 ? 512 / threads<G>() : 
 #pragma unroll
             for (int j = 0; j < N; ++j) {
                 const int c = c0 + j * G * V;
-                if (c < p.D) store_v<float, V>(part + (size_t)g * p.D + c, which ? sb[j] : sw[j]);
+                if (c < p.D) store_part<SHIFT>(part + (size_t)g * p.D + c, which ? sb[j] : sw[j], c, p.D);
             }
             __syncthreads();
             for (int c = threadIdx.x; c < p.D; c += WARP_NT) {

@@ -129,6 +129,57 @@ def test_tensors_that_start_on_no_16_bytes(G, x):
         assert (got.double() - ref.double()).abs().max() <= (2.0 ** -7 if got.dtype == torch.bfloat16 else 200 * U) * scale
 
 
+@pytest.mark.parametrize("x", ["bf16", "f32"])
+@pytest.mark.parametrize("D", [9, 10, 12, 13, 17, 33, 65, 129, 249, 333, 514, 761, 1025, 1530, 2052, 5001])
+@pytest.mark.parametrize("rows", [1, 2, 3, 9, 1201])
+def test_rows_that_start_anywhere(G, x, D, rows):
+    """Widths that are no multiple of 16 bytes: rows begin and end inside one."""
+    _check(G, rows, D, x=x)
+
+
+@pytest.mark.parametrize("x", ["bf16", "f32"])
+@pytest.mark.parametrize("D,rows", [(9, 50), (12, 33), (33, 21), (333, 11), (514, 9), (1025, 17), (5001, 10)])
+def test_rows_end_where_they_end(G, x, D, rows):
+    """Tensors inside of larger ones: what lies around them is neither used nor written, and rows of
+    NaN and infinities stay out of their neighbours."""
+    import ctypes
+
+    import torch
+    t, gen, n = _dt(x), torch.Generator("cuda").manual_seed(D), rows * D
+
+    def inside(fill):
+        whole = torch.full((n + 128,), fill, device="cuda", dtype=t)
+        return whole, whole[64:64 + n].view(rows, D)
+
+    _, a = inside(float("nan"))
+    _, dy = inside(float("inf"))
+    a.copy_(torch.randn(rows, D, generator=gen, device="cuda"))
+    dy.copy_(torch.randn(rows, D, generator=gen, device="cuda"))
+    w = torch.randn(D, generator=gen, device="cuda")
+    desc = G.norm_desc(rows, D, t, t)
+    lib, ptr = G.lib(), lambda v: ctypes.c_void_p(v.data_ptr())
+    flt = lambda v: ctypes.cast(ptr(v), ctypes.POINTER(ctypes.c_float))
+    st = ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+
+    def run():
+        (wy, y), (wx, dx) = inside(7.0), inside(7.0)
+        mean, rstd = torch.empty(rows, device="cuda"), torch.empty(rows, device="cuda")
+        assert lib.gdr_layernorm_fwd(ctypes.byref(desc), ptr(a), ptr(w), None, ptr(y), flt(mean), flt(rstd), st) == 0
+        assert lib.gdr_layernorm_bwd(ctypes.byref(desc), ptr(a), ptr(dy), ptr(w), flt(mean), flt(rstd), ptr(dx), None, None,
+                                     None, 0, st) == 0
+        for whole in (wy, wx):
+            assert (whole[:64] == 7).all() and (whole[64 + n:] == 7).all()
+        return y, dx
+
+    ref = run()
+    assert all(torch.isfinite(v).all() for v in ref)
+    bad = rows // 2
+    a[bad], dy[bad] = float("inf"), float("nan")
+    keep = [r for r in range(rows) if r != bad]
+    for got, want in zip(run(), ref):
+        assert torch.equal(got[keep], want[keep]) and torch.isnan(got[bad]).all()
+
+
 def test_rows_far_from_zero(G):
     """A row's offset is a hundred times its spread: the variance comes from the centred values."""
     _check(G, 30, 512, x="f32", offset=100.0)
