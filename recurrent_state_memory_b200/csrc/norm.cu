@@ -22,7 +22,7 @@ struct Plan { int V, N, G; bool shift; };
 // 39.7 us, in 128 54.2, rows of 6144 in 768 49.1, in 1024 56.6.
 static Plan plan_of(int D, int V, bool bwd, bool shift) {
     Plan q{V, 0, 32, shift};
-    const int nv = (D + (shift ? 2 * V - 2 : V - 1)) / V;       // loads of a row
+    const int nv = (D + (shift ? V - (D & -D) : 0) + V - 1) / V;     // loads of a row
     if (nv <= 32) {                             // one load a lane, as few lanes as hold the row
         q.N = 1;
         for (q.G = 1; q.G < nv; q.G *= 2) {}
@@ -43,14 +43,16 @@ static Plan plan_of(int D, int V, bool bwd, bool shift) {
     return q;
 }
 // Rows of D elements where 16-byte access takes V of them.  Rows that are not multiples of it:
-// shifted, where that holds no more elements than one by one, and forward with weights in registers
-// and, of fp32, one load a lane.  (33.5 M bf16 elements, shifted against one by one: backward rows of
-// 9 66 and 247 us, 333 60 and 73, 5001 68 and 117; but 250, a block in place of a warp, 77 and 52.
-// Forward 9 68 and 147, 5001 44 and 59; 16.8 M fp32, rows of 2047 64 and 23.)
+// shifted, where that holds no more elements than one by one, or takes few lanes; forward not by a
+// whole warp a row of one load each, of fp32 only by less than a warp, and with weights in registers.
+// (33.5 M bf16 elements, shifted against one by one: backward rows of 9 66 and 247 us, 14 83 and 161,
+// 333 60 and 73, 5001 68 and 117; but 2047, in 384 threads, 64 and 55.  Forward 9 67 and 146, 14 80
+// and 95, 5001 44 and 59, but 129 73 and 66; 16.8 M fp32, rows of 2047 64 and 23.)
 static Plan plan(int D, int V, bool bwd) {
     if (D % V == 0) return plan_of(D, V, bwd, false);
     const Plan one = plan_of(D, 1, bwd, false), q = plan_of(D, V, bwd, true);
-    const bool fits = q.N && q.V * q.N * q.G <= (one.N ? one.N * one.G : 1 << 20) && (bwd || (q.G < 1024 && (V == 8 || q.N == 1)));
+    const bool fits = q.N && (q.V * q.N * q.G <= (one.N ? one.N * one.G : 1 << 20) || q.G <= (bwd ? 16 : 4)) &&
+                      (bwd || q.G < 32 || (V == 8 && q.N * q.G > 32 && q.G < 1024));
     return D > V && fits ? q : one;             // D > V: a chunk reaches into one neighbouring row at most
 }
 static int rows_of_block(const Plan& q) { return q.N && q.G <= 32 ? WARP_NT / q.G : 1; }
@@ -79,7 +81,8 @@ static gdr_status launch_plan(const Plan& q, const NormParams& p, cudaStream_t s
 #define GDR_NORM(n, g) if (q.N == n && q.G == g) return launch_one<XT, YT, V, n, g, BWD, SHIFT>(p, st)
     constexpr int MOST = (BWD || V == 1 ? 8 : 16) / V;
     if constexpr (!SHIFT) GDR_NORM(1, 1);
-    GDR_NORM(1, 2); GDR_NORM(1, 4); GDR_NORM(1, 8); GDR_NORM(1, 16); GDR_NORM(1, 32);
+    GDR_NORM(1, 2); GDR_NORM(1, 4); GDR_NORM(1, 8); GDR_NORM(1, 16);
+    if constexpr (BWD || !SHIFT) GDR_NORM(1, 32);
     if constexpr (BWD || V != 4 || !SHIFT) {
         if constexpr (MOST >= 2) GDR_NORM(2, 32);
         if constexpr (MOST >= 4) GDR_NORM(4, 32);

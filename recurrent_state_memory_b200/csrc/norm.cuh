@@ -8,10 +8,12 @@
 // Bound: HBM; x (and dy) are read once and y (dx) written once.
 //
 // Split.  A row belongs to a group of lanes that holds all of it in registers, 16 bytes a lane and
-// load: G = 1 .. 32 lanes of a warp (several rows per warp), or a whole block for rows longer than
-// a warp's registers.  Groups walk the rows with the grid's stride; the next row's loads are in
-// flight while a row is reduced.  Rows that 16-byte access does not fit (D or a pointer off) take
-// one element per lane and load.  Rows beyond a block's registers are read again from L2 instead.
+// load: G = 1 .. 32 lanes of a warp (several rows per warp), or a whole block of 64 to 1024 threads
+// for rows longer than a warp's registers.  Groups walk the rows with the grid's stride, and the grid
+// is what the GPU holds at once; the next row's loads are in flight while a row is reduced.  Rows
+// that do not start on 16 bytes are taken in the tensor's 16-byte chunks or one by one (a pointer
+// off, or where the dispatch measured that better).  Rows beyond a block's registers are read again
+// from L2 instead.
 //
 // The gradients of weight and bias: a lane's columns are the same for all of its rows, so it sums
 // them in registers; a block adds its groups' sums in a fixed order and writes one partial row,
