@@ -14,6 +14,8 @@ namespace lnm {
 // of G threads); N = 0: the row is too long for a block's registers.  Shifted: rows of V-element
 // chunks that begin and end inside one.
 struct Plan { int V, N, G; bool shift; };
+// The backward of longer rows: in registers as they lie in memory, where 16-byte access fits.
+static bool wide(int D, int V, bool bwd) { return bwd && V > 1 && D % V == 0 && D > 8 * 1024 && D <= 16 * 1024; }
 
 // A warp while a lane holds at most 16 elements (one by one, and in the backward, which also holds
 // dy, the weights and two sums: 8), then the block that holds the fewest elements beside the row.
@@ -117,7 +119,13 @@ static gdr_status launch(const gdr_norm_desc* d, bool bwd, NormParams& p, cudaSt
     if (p.rows > 0) {
         if (q.N && bwd) s = launch_width<XT, YT, V, true>(q, p, st);
         else if (q.N) s = launch_width<XT, YT, V, false>(q, p, st);
-        else {
+        else if (wide(p.D, q.V, bwd)) {
+            const auto kernel = norm_bwd_wide_kernel<XT, YT, V, 16 / V>;
+            const size_t smem = p.part_w || p.part_b ? 2 * 16 * WIDE_NT * sizeof(float) : 0;
+            const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+            if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(layer norm)");
+            kernel<<<p.parts, WIDE_NT, smem, st>>>(p);
+        } else {
             const unsigned grid = (unsigned)(p.rows < 2 * device_sm_count() ? p.rows : 2 * device_sm_count());
             if (!bwd) norm_fwd_long_kernel<XT, YT><<<grid, LONG_NT, 0, st>>>(p);
             else {
@@ -157,7 +165,7 @@ static gdr_status launch(const gdr_norm_desc* d, bool bwd, NormParams& p, cudaSt
 static int parts_of(const gdr_norm_desc* d) {
     const Plan q = plan(d->D, vector_of(d), true);
     const long long per = rows_of_block(q), n = (d->rows + 8 * per - 1) / (8 * per);
-    const long long cap = (long long)device_sm_count() * (q.N ? bwd_blocks(q.G > 32 ? q.G : WARP_NT) : 2);
+    const long long cap = (long long)device_sm_count() * (q.N ? bwd_blocks(q.G > 32 ? q.G : WARP_NT) : wide(d->D, q.V, true) ? 1 : 2);
     // shifted rows of a block: blocks in multiples of V, but no more than stay on the GPU
     const long long M = q.shift && per % q.V ? q.V : 1, parts = n < cap ? n + M - 1 : cap;
     return (int)(parts < M ? M : (parts < cap ? parts : cap) / M * M);

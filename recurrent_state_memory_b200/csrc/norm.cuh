@@ -586,6 +586,102 @@ __global__ void __launch_bounds__(threads<G>(), bwd_blocks(threads<G>())) norm_b
     }
 }
 
+// Backward of rows of up to 16384 elements by a block of 1024 threads: x and dy stay as they lie in
+// memory in registers (64 a thread), the sums of dweight and dbias in shared memory, each thread's
+// columns its own, and x hat and w dy are formed twice.  The next row is on its way into L2
+// meanwhile.  (2048 rows of 16384 bf16: 83 us; by the three passes below 137.)
+constexpr int WIDE_NT = 1024;
+template <typename XT, typename YT, int V, int N>
+__global__ void __launch_bounds__(WIDE_NT) norm_bwd_wide_kernel(NormParams p) {
+    extern __shared__ __align__(16) float part[];      // the sums: dweight, then dbias, four of a thread at a time
+    __shared__ __align__(16) float sm[2][WIDE_NT / 32][2];
+    Group<WIDE_NT, 2> grp{sm, 0};
+    const float inv = 1.f / (float)p.D;
+    const int c0 = threadIdx.x * V;
+    const bool sums = p.part_w || p.part_b;
+    auto at = [&](int which, int j) { return part + ((which * N + j) * (V / 4) * WIDE_NT + threadIdx.x) * 4; };
+    auto get = [&](int which, int j) {
+        Vals<V> v;
+#pragma unroll
+        for (int h = 0; h < V / 4; ++h) {
+            const float4 a = *reinterpret_cast<const float4*>(at(which, j) + h * WIDE_NT * 4);
+            v.v[2 * h] = pair(a.x, a.y);
+            v.v[2 * h + 1] = pair(a.z, a.w);
+        }
+        return v;
+    };
+    auto put = [&](int which, int j, const Vals<V>& v) {
+#pragma unroll
+        for (int h = 0; h < V / 4; ++h)
+            *reinterpret_cast<float4*>(at(which, j) + h * WIDE_NT * 4) =
+                make_float4(v.get(4 * h), v.get(4 * h + 1), v.get(4 * h + 2), v.get(4 * h + 3));
+    };
+    auto each = [&](auto f) {
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+            if (c0 + j * WIDE_NT * V < p.D) f(j, j * WIDE_NT * V);
+    };
+    if (sums) {
+        Vals<V> z;
+        z.all(0.f);
+        each([&](int j, int) { put(0, j, z); put(1, j, z); });
+    }
+    for (long long r = blockIdx.x; r < p.rows; r += gridDim.x) {
+        const XT* x = static_cast<const XT*>(p.x) + (size_t)r * p.D + c0;
+        const YT* dy = static_cast<const YT*>(p.dy) + (size_t)r * p.D + c0;
+        const float mean = p.mean[r], rstd = p.rstd[r];
+        Raw<XT, V> rx[N];
+        Raw<YT, V> rd[N];
+        each([&](int j, int c) { rx[j].load(x + c); rd[j].load(dy + c); });
+        if (r + gridDim.x < p.rows) {
+            const size_t next = (size_t)gridDim.x * p.D;
+            each([&](int, int c) {
+                asm volatile("prefetch.global.L2 [%0];" ::"l"(x + next + c));
+                asm volatile("prefetch.global.L2 [%0];" ::"l"(dy + next + c));
+            });
+        }
+        Vals<V> off, rs, s1, s2;
+        off.all(-mean);
+        rs.all(rstd);
+        s1.all(0.f);
+        s2.all(0.f);
+        with_weights(p, [&](auto type) {
+            each([&](int j, int c) {
+                const Vals<V> xh = (rx[j].vals() + off) * rs;
+                Vals<V> d = rd[j].vals();
+                if (sums) {
+                    put(0, j, fma(d, xh, get(0, j)));
+                    put(1, j, get(1, j) + d);
+                }
+                if (p.weight) d = d * load_w<decltype(type), V>(p.weight, c0 + c);
+                s1 = s1 + d;
+                s2 = fma(d, xh, s2);
+            });
+        });
+        if (!p.dx) continue;
+        float c12[2] = {s1.total(), s2.total()};
+        grp.sum(c12);
+        Vals<V> m1, m2;
+        m1.all(-c12[0] * inv);
+        m2.all(-c12[1] * inv);
+        XT* dx = static_cast<XT*>(p.dx) + (size_t)r * p.D + c0;
+        with_weights(p, [&](auto type) {
+            each([&](int j, int c) {
+                const Vals<V> xh = (rx[j].vals() + off) * rs;
+                Vals<V> d = rd[j].vals();
+                if (p.weight) d = d * load_w<decltype(type), V>(p.weight, c0 + c);
+                if (GDR_INB(c0 + c + V <= p.D, 912)) store_v<XT, V>(dx + c, (d + fma(xh, m2, m1)) * rs);
+            });
+        });
+    }
+    asm volatile("griddepcontrol.launch_dependents;");
+    const size_t base = (size_t)blockIdx.x * p.D + c0;
+    each([&](int j, int c) {
+        if (p.part_w) store_v<float, V>(p.part_w + base + c, get(0, j));
+        if (p.part_b) store_v<float, V>(p.part_b + base + c, get(1, j));
+    });
+}
+
 // Rows beyond a block's registers: three passes over the row, two of them from L2.
 constexpr int LONG_NT = 1024;
 template <typename XT, typename YT>

@@ -85,6 +85,15 @@ def test_widths_in_32_bits(G, D):
     _check(G, 5, D, x="f32")
 
 
+@pytest.mark.parametrize("x,y", [("bf16", "bf16"), ("f32", "f32"), ("bf16", "f32"), ("f32", "bf16")])
+@pytest.mark.parametrize("D,rows", [(8200, 1), (9000, 160), (12288, 7), (16384, 330)])
+def test_wide_rows(G, x, y, D, rows):
+    _check(G, rows, D, x=x, y=y)
+    if rows == 7:
+        _check(G, rows, D, x=x, y=y, weight=False)
+        _check(G, rows, D, x=x, y=y, weight=False, bias=False)
+
+
 def test_the_widest_rows(G):
     _check(G, 2, 70001, x="f32")
     _check(G, 3, 131072)
