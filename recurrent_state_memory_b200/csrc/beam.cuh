@@ -10,9 +10,12 @@
 //      order by few more, so one sweep over the registers collects them all and a count of the
 //      larger ones ranks them.
 //   2. beam_group_kernel: a block per group merges its beams' pieces the same way.  Its sums hold
-//      fp32 exponentials; where two neighbours of the list from different beams are closer than
-//      those allow (TOL), the beams' sums are formed again from the logits in 64 bits and the
-//      merge is repeated, so that the order is the 64-bit one.
+//      fp32 exponentials, so two scores of different beams within TOL of each other may be in the
+//      wrong order.  Only candidates down to TOL below the M-th can belong to the M best; where two
+//      of these from different beams are that near (neighbours within the list, or any around its
+//      end), the beams' sums are formed again from the logits in 64 bits and the merge is repeated.
+//      A beam that is not summed again lies further than TOL from every other one's candidates, so
+//      the order is the 64-bit one.
 //
 // Bound: the read of the logits (one exponential and about ten instructions each); for one small
 // group the latency of the two launches.
@@ -314,7 +317,7 @@ __global__ void __launch_bounds__(GNT) beam_group_kernel(BeamParams p) {
     __shared__ unsigned the_mark;
     __shared__ int count;
     __shared__ Cand list[LIST];
-    __shared__ Cand first[MOST + 1];                // the best in order, and the one behind
+    __shared__ Cand first[MOST];                    // the best in order
     __shared__ double lse[MOST], top[MOST], red[GWARPS];
     __shared__ float score[MOST];
     __shared__ unsigned char kind[MOST], redo[MOST];
@@ -423,20 +426,20 @@ __global__ void __launch_bounds__(GNT) beam_group_kernel(BeamParams p) {
             }
         }
     };
-    // one more than asked for: the candidate behind the last may be too near to it
     const long long all = (long long)p.K * p.V;
-    const int want = (int)(all < p.M + 1 ? all : p.M + 1);
+    const int want = p.M;                           // at most `all`
     for (int turn = 0; turn < 2; ++turn) {
         unsigned mine = 0;
         each([&](const Cand& c) { mine = max(mine, key_of_score(c.s)); });
         const int active = FEW ? 32 * min(GWARPS, span) : GNT, lanes = group_lanes(active, want);
         put_marks(mine, lanes, active, marks);
         if (threadIdx.x == 0) { count = 0; the_mark = 0; }
-        if (threadIdx.x <= p.M) first[threadIdx.x] = Cand{-INFINITY, -1};
+        if (threadIdx.x < p.M) first[threadIdx.x] = Cand{-INFINITY, -1};
         __syncthreads();
         find_mark<GWARPS>(marks, active / lanes, want, &the_mark);
         __syncthreads();
-        const unsigned mark = the_mark;
+        // and down to TOL below it: the list also holds what may belong before its M-th
+        const unsigned mark = the_mark ? key_of_score((double)value_of(the_mark) - TOL) : 0u;
         each([&](const Cand& c) {
             if (key_of_score(c.s) < mark) return;
             const int slot = atomicAdd(&count, 1);
@@ -475,17 +478,23 @@ __global__ void __launch_bounds__(GNT) beam_group_kernel(BeamParams p) {
             }
         }
         if (turn == 1) break;
-        // neighbours of different beams that the fp32 sums cannot order
+        // candidates of different beams that the fp32 sums cannot order
         bool near = false;
-        if ((int)threadIdx.x + 1 < want) {
+        auto pair_up = [&](const Cand& a, const Cand& b) {
+            const int ka = a.at / p.V, kb = b.at / p.V;
+            if (ka == kb) return;
+            if (kind[ka] == LIVE) { redo[ka] = 1; near = true; }
+            if (kind[kb] == LIVE) { redo[kb] = 1; near = true; }
+        };
+        if ((int)threadIdx.x + 1 < want) {          // neighbours in the list
             const Cand a = first[threadIdx.x], b = first[threadIdx.x + 1];
-            if (b.at >= 0 && b.s > -INFINITY && a.s - b.s <= TOL) {
-                const int ka = a.at / p.V, kb = b.at / p.V;
-                if (ka != kb) {
-                    if (kind[ka] == LIVE) { redo[ka] = 1; near = true; }
-                    if (kind[kb] == LIVE) { redo[kb] = 1; near = true; }
-                }
-            }
+            if (b.s > -INFINITY && a.s - b.s <= TOL) pair_up(a, b);
+        }
+        const Cand end = first[want - 1];           // all around the M-th
+        auto around = [&](const Cand& c) { if (fabs(c.s - end.s) <= TOL) pair_up(c, end); };
+        if (end.s > -INFINITY) {
+            if (have > LIST) each(around);
+            else for (int i = threadIdx.x; i < have; i += GNT) around(list[i]);
         }
         if (!__syncthreads_or(near)) break;
         for (int k = 0; k < p.K; ++k) {
