@@ -40,25 +40,37 @@ inline int device_sm_count() {
 }
 
 // cuTensorMapEncodeTiled is a driver call; it is looked up through the runtime so that the
-// library does not link libcuda itself.
+// library does not link libcuda itself.  Unlike the runtime's calls it needs a current context, which
+// a host thread whose first CUDA call this is does not have yet: it gets its device's primary one.
+typedef CUresult (*CtxGetCurrentFn)(CUcontext*);
 typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
+inline gdr_status driver_fn(const char* name, void** fn) {
+    cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
+    const cudaError_t e = cudaGetDriverEntryPoint(name, fn, cudaEnableDefault, &q);
+    if (e != cudaSuccess) return cuda_fail(e, name);
+    return q == cudaDriverEntryPointSuccess && *fn ? GDR_OK : fail(GDR_ERR_CUDA, "the driver has no %s", name);
+}
+
 inline gdr_status encode_fn(EncodeTiledFn* out) {
     static std::mutex mu;
-    static EncodeTiledFn fn = nullptr;
-    std::lock_guard<std::mutex> lock(mu);
-    if (!fn) {
-        void* ptr = nullptr;
-        cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
-        cudaError_t e = cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &ptr, cudaEnableDefault, &q);
-        if (e != cudaSuccess) return cuda_fail(e, "cudaGetDriverEntryPoint(cuTensorMapEncodeTiled)");
-        if (q != cudaDriverEntryPointSuccess || !ptr)
-            return fail(GDR_ERR_CUDA, "the driver has no cuTensorMapEncodeTiled%s");
-        fn = reinterpret_cast<EncodeTiledFn>(ptr);
+    static void *encode = nullptr, *current = nullptr;
+    CUcontext context = nullptr;
+    {
+        std::lock_guard<std::mutex> lock(mu);
+        gdr_status s = encode ? GDR_OK : driver_fn("cuTensorMapEncodeTiled", &encode);
+        if (s == GDR_OK && !current) s = driver_fn("cuCtxGetCurrent", &current);
+        if (s != GDR_OK) return s;
+        *out = reinterpret_cast<EncodeTiledFn>(encode);
     }
-    *out = fn;
+    if (reinterpret_cast<CtxGetCurrentFn>(current)(&context) == CUDA_SUCCESS && !context) {
+        int dev = 0;
+        cudaError_t e = cudaGetDevice(&dev);
+        if (e == cudaSuccess) e = cudaSetDevice(dev);
+        if (e != cudaSuccess) return cuda_fail(e, "cudaSetDevice");
+    }
     return GDR_OK;
 }
 
