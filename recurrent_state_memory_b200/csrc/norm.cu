@@ -121,10 +121,11 @@ static gdr_status launch(const gdr_norm_desc* d, bool bwd, NormParams& p, cudaSt
         else if (q.N) s = launch_width<XT, YT, V, false>(q, p, st);
         else if (wide(p.D, q.V, bwd)) {
             const auto kernel = norm_bwd_wide_kernel<XT, YT, V, 16 / V>;
-            const size_t smem = p.part_w || p.part_b ? 2 * 16 * WIDE_NT * sizeof(float) : 0;
-            const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+            constexpr int SUMS = 2 * 16 * WIDE_NT * (int)sizeof(float);
+            // the kernel's limit, which calls on other host threads share: always the largest
+            const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SUMS);
             if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(layer norm)");
-            kernel<<<p.parts, WIDE_NT, smem, st>>>(p);
+            kernel<<<p.parts, WIDE_NT, p.part_w || p.part_b ? SUMS : 0, st>>>(p);
         } else {
             const unsigned grid = (unsigned)(p.rows < 2 * device_sm_count() ? p.rows : 2 * device_sm_count());
             if (!bwd) norm_fwd_long_kernel<XT, YT><<<grid, LONG_NT, 0, st>>>(p);

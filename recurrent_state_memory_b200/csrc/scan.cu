@@ -33,14 +33,16 @@ static gdr_status launch_clusters(KERN kern, const ScanParams& p, const ScanMaps
                                   cudaStream_t st) {
     const unsigned ct = (unsigned)((p.D + channels - 1) / channels);
     const int ncl = cluster_of((long long)ct * p.B, p.T, tok, device_sm_count());
-    smem += (size_t)2 * ncl * channels * sizeof(float2);
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    // the limit belongs to the kernel, not to the call: the same for every cluster, so that a call on
+    // another host thread never finds it lower than it needs
+    auto bytes = [&](int blocks) { return smem + (size_t)2 * blocks * channels * sizeof(float2); };
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes(MAX_CLUSTER));
     if (e == cudaSuccess && ncl > 8) e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(scan)");
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(ncl * p.B), ct);                // a sequence's cluster, its channels
     cfg.blockDim = dim3(NT);
-    cfg.dynamicSmemBytes = smem;
+    cfg.dynamicSmemBytes = bytes(ncl);
     cfg.stream = st;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeClusterDimension;
