@@ -5,6 +5,7 @@
 #include <dlfcn.h>
 
 #include <ATen/cuda/EmptyTensor.h>
+#include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Dtype.h>
@@ -100,18 +101,43 @@ int64_t row_stride(const Tensor& t, const char* name) {
     return st[n - 2];
 }
 
-// The call's device, current while this lives, and its stream: a handle, or None for the current one.
-struct Call {
-    c10::cuda::CUDAGuard guard;
+// A call: its device, current while this lives, and its stream, the given one or the current one.  With
+// a given stream, memory is allocated on it (nothing that is queued on the current one uses it
+// still), and none of the call's tensors gives its memory away before that stream, and for outputs
+// the current one, are done with it.
+class Call {
+public:
     gdr_stream_t stream;
-    Call(at::Device dev, const py::object& s)
-        : guard(dev), stream(s.is_none() ? reinterpret_cast<void*>(c10::cuda::getCurrentCUDAStream(dev.index()).stream())
-                                         : reinterpret_cast<void*>(s.attr("cuda_stream").cast<intptr_t>())) {}
+    Call(at::Device dev, const py::object& given)
+        : dev_(dev), device_(dev), here_(c10::cuda::getCurrentCUDAStream(dev.index())) {
+        stream = reinterpret_cast<void*>(here_.stream());
+        if (given.is_none()) return;
+        stream = reinterpret_cast<void*>(given.attr("cuda_stream").cast<intptr_t>());
+        if (stream == reinterpret_cast<void*>(here_.stream())) return;
+        there_.emplace(c10::cuda::getStreamFromExternal(reinterpret_cast<cudaStream_t>(stream), dev.index()));
+    }
+    // The caller's tensors of the call.
+    template <typename... T> void uses(const T&... t) const { if (there_) (used_on(t, there_->current_stream()), ...); }
+    Tensor scratch(at::IntArrayRef shape, at::ScalarType type) const {
+        return at::detail::empty_cuda(shape, type, dev_, std::nullopt);
+    }
+    Tensor output(at::IntArrayRef shape, at::ScalarType type) const {
+        Tensor t = scratch(shape, type);
+        if (there_) used_on(t, here_);
+        return t;
+    }
+
+private:
+    static void used_on(const Tensor& t, c10::Stream s) {
+        c10::cuda::CUDACachingAllocator::recordStream(t.storage().data_ptr(), c10::cuda::CUDAStream(s));
+    }
+    static void used_on(const MaybeTensor& t, c10::Stream s) { if (t) used_on(*t, s); }
+    const at::Device dev_;
+    const c10::cuda::CUDAGuard device_;
+    const c10::cuda::CUDAStream here_;
+    std::optional<c10::cuda::CUDAStreamGuard> there_;
 };
 
-Tensor make(at::IntArrayRef shape, at::ScalarType type, at::Device dev) {
-    return at::detail::empty_cuda(shape, type, dev, std::nullopt);
-}
 template <typename T = void> T* at_(const MaybeTensor& t) { return t ? static_cast<T*>(t->data_ptr()) : nullptr; }
 template <typename T = void> T* at_(const Tensor& t) { return static_cast<T*>(t.data_ptr()); }
 
@@ -155,10 +181,11 @@ py::tuple scan_fwd(const Tensor& x, const Tensor& g, const MaybeTensor& h0, int 
     const at::ScalarType out = dtype_of(out_dtype, x.scalar_type());
     const gdr_scan_desc d = scan_desc(x, g, T, out, gate_mode, tied);
     const Call call(dev, stream);
-    Tensor h = make({B, T, D}, out, dev);
+    call.uses(x, g, h0, lengths);
+    Tensor h = call.output({B, T, D}, out);
     MaybeTensor h_T, ckpt;
-    if (want_state) h_T = make({B, D}, at::kFloat, dev);
-    if (want_ckpt) ckpt = make({B, (T + GDR_SCAN_CKPT - 1) / GDR_SCAN_CKPT, D}, at::kFloat, dev);
+    if (want_state) h_T = call.output({B, D}, at::kFloat);
+    if (want_ckpt) ckpt = call.output({B, (T + GDR_SCAN_CKPT - 1) / GDR_SCAN_CKPT, D}, at::kFloat);
     check(api.scan_fwd(&d, at_(x), at_(g), at_<float>(h0), at_<int>(lengths), at_(h), at_<float>(h_T), at_<float>(ckpt),
                        call.stream), "gdr_scan_fwd");
     return want_ckpt ? py::make_tuple(h, h_T, ckpt) : py::make_tuple(h, h_T);
@@ -173,9 +200,10 @@ py::dict scan_bwd(const Tensor& x, const Tensor& g, const Tensor& ckpt, const Ma
     want(dh_T, "dh_T", {B, D}, at::kFloat, dev);
     const gdr_scan_desc d = scan_desc(x, g, T, dh ? dh->scalar_type() : x.scalar_type(), gate_mode, tied);
     const Call call(dev, stream);
-    Tensor dx = make({B, T, D}, x.scalar_type(), dev), dg = make({B, T, D}, g.scalar_type(), dev);
+    call.uses(x, g, ckpt, dh, dh_T, lengths);
+    Tensor dx = call.output({B, T, D}, x.scalar_type()), dg = call.output({B, T, D}, g.scalar_type());
     MaybeTensor dh0;
-    if (want_dh0) dh0 = make({B, D}, at::kFloat, dev);
+    if (want_dh0) dh0 = call.output({B, D}, at::kFloat);
     check(api.scan_bwd(&d, at_(x), at_(g), at_<float>(ckpt), at_<int>(lengths), at_(dh), at_<float>(dh_T), at_(dx),
                        at_(dg), at_<float>(dh0), call.stream), "gdr_scan_bwd");
     py::dict r;
@@ -191,7 +219,8 @@ Tensor scan_step(const Tensor& x, const Tensor& g, const Tensor& h, int gate_mod
     want(o, "o", x.sizes(), out, dev);
     const gdr_scan_desc d = scan_desc(x, g, 1, out, gate_mode, tied);
     const Call call(dev, stream);
-    const Tensor to = o ? *o : make(x.sizes(), out, dev);
+    call.uses(x, g, h, o);
+    const Tensor to = o ? *o : call.output(x.sizes(), out);
     check(api.scan_step(&d, at_(x), at_(g), at_<float>(h), at_(to), call.stream), "gdr_scan_step");
     return to;
 }
@@ -219,11 +248,12 @@ py::tuple layernorm_fwd(const Tensor& x, const MaybeTensor& weight, const MaybeT
     const gdr_norm_desc d = norm_desc(x, out, weight, bias, eps);
     const at::Device dev = x.device();
     const Call call(dev, stream);
-    Tensor y = make(x.sizes(), out, dev);
+    call.uses(x, weight, bias);
+    Tensor y = call.output(x.sizes(), out);
     MaybeTensor mean, rstd;
     if (want_stats) {
-        mean = make(x.sizes().slice(0, x.dim() - 1), at::kFloat, dev);
-        rstd = make(x.sizes().slice(0, x.dim() - 1), at::kFloat, dev);
+        mean = call.output(x.sizes().slice(0, x.dim() - 1), at::kFloat);
+        rstd = call.output(x.sizes().slice(0, x.dim() - 1), at::kFloat);
     }
     check(api.layernorm_fwd(&d, at_(x), at_(weight), at_(bias), at_(y), at_<float>(mean), at_<float>(rstd), call.stream),
           "gdr_layernorm_fwd");
@@ -238,14 +268,15 @@ py::dict layernorm_bwd(const Tensor& x, const Tensor& dy, const Tensor& mean, co
     want(dy, "dy", x.sizes(), at::ScalarType::Undefined, dev);
     want(mean, "mean", rows, at::kFloat, dev);
     want(rstd, "rstd", rows, at::kFloat, dev);
+    if (workspace) on(*workspace, "workspace", dev);
     const Call call(dev, stream);
+    call.uses(x, dy, mean, rstd, weight, workspace);
     MaybeTensor dx, dw, db;
-    if (want_dx) dx = make(x.sizes(), x.scalar_type(), dev);
-    if (weight) dw = make({x.size(-1)}, at::kFloat, dev);
-    if (with_bias) db = make({x.size(-1)}, at::kFloat, dev);
+    if (want_dx) dx = call.output(x.sizes(), x.scalar_type());
+    if (weight) dw = call.output({x.size(-1)}, at::kFloat);
+    if (with_bias) db = call.output({x.size(-1)}, at::kFloat);
     const size_t need = api.layernorm_bwd_workspace_bytes(&d, dw.has_value(), with_bias);
-    const MaybeTensor ws = workspace ? workspace : need ? MaybeTensor(make({static_cast<int64_t>(need)}, at::kByte, dev)) : MaybeTensor();
-    if (ws) on(*ws, "workspace", dev);
+    const MaybeTensor ws = workspace ? workspace : need ? MaybeTensor(call.scratch({static_cast<int64_t>(need)}, at::kByte)) : MaybeTensor();
     check(api.layernorm_bwd(&d, at_(x), at_(dy), at_(weight), at_<float>(mean), at_<float>(rstd), at_(dx), at_<float>(dw),
                             at_<float>(db), at_(ws), ws ? ws->nbytes() : 0, call.stream), "gdr_layernorm_bwd");
     py::dict r;
@@ -263,16 +294,17 @@ py::tuple beam_select(const Tensor& logits, const Tensor& scores, const std::opt
     const int64_t G = logits.size(0), K = logits.size(1), M = n_out.value_or(K);
     want(scores, "scores", {G, K}, at::kFloat, dev);
     want(finished, "finished", {G, K}, at::kBool, dev);
+    if (workspace) on(*workspace, "workspace", dev);
     gdr_beam_desc d;
     d.G = size32(G, "G"); d.K = size32(K, "K"); d.V = size32(logits.size(2), "V"); d.M = size32(std::max<int64_t>(M, 0), "n_out");
     d.row = row_stride(logits, "logits");
     d.x_dtype = code(logits.scalar_type());
     d.eos = eos < 0 || eos > INT32_MAX ? -1 : static_cast<int>(eos);
     const Call call(dev, stream);
+    call.uses(logits, scores, finished, workspace);
     const size_t need = api.beam_select_workspace_bytes(&d);
-    Tensor out = make({G, d.M}, at::kFloat, dev), parent = make({G, d.M}, at::kInt, dev), token = make({G, d.M}, at::kInt, dev);
-    const MaybeTensor ws = workspace ? workspace : need ? MaybeTensor(make({static_cast<int64_t>(need)}, at::kByte, dev)) : MaybeTensor();
-    if (ws) on(*ws, "workspace", dev);
+    Tensor out = call.output({G, d.M}, at::kFloat), parent = call.output({G, d.M}, at::kInt), token = call.output({G, d.M}, at::kInt);
+    const MaybeTensor ws = workspace ? workspace : need ? MaybeTensor(call.scratch({static_cast<int64_t>(need)}, at::kByte)) : MaybeTensor();
     check(api.beam_select(&d, at_(logits), at_<float>(scores), at_<unsigned char>(finished), at_<float>(out), at_<int>(parent),
                           at_<int>(token), at_(ws), ws ? ws->nbytes() : 0, call.stream), "gdr_beam_select");
     return py::make_tuple(out, parent, token);
@@ -293,6 +325,7 @@ Tensor state_reorder(const Tensor& S, const Tensor& parent, bool layers, const p
     d.L = size32(L, "L"); d.G = size32(G, "G"); d.K = size32(K, "K");
     d.state_bytes = n ? S.nbytes() / n : 0;
     const Call call(dev, stream);
+    call.uses(S, parent);
     check(api.state_reorder(&d, at_(S), at_<int>(parent), call.stream), "gdr_state_reorder");
     return S;
 }

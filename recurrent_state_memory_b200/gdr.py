@@ -496,7 +496,9 @@ def decode_step(q, k, v, g, beta, S, theta=None, *, gate_mode=GATE_NEG_SOFTPLUS,
 #
 # Checks, outputs and the C call of these are in csrc/binding.cpp: at serving sizes their kernels take
 # a few microseconds, less than the same steps in Python.  Tensors are CUDA tensors on one device,
-# the call is asynchronous on `stream` (default: that device's current stream).
+# the call is asynchronous on `stream` (default: that device's current stream).  A caller that passes
+# `stream` orders it behind the work that makes the call's tensors, and later work behind it; memory
+# of the call's tensors, outputs and workspace is not reused before that stream is done with it.
 
 _binding = None
 
