@@ -9,6 +9,7 @@ Layouts follow include/gdr.h: q, k [B,T,H,dk]; v, o [B,T,H,dv]; g [B,T,H,dk]
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import re
@@ -192,6 +193,25 @@ def _stream_handle(stream: Optional[torch.cuda.Stream], device) -> ctypes.c_void
     return ctypes.c_void_p(s.cuda_stream)
 
 
+def _memory(stream: Optional[torch.cuda.Stream]):
+    """Where a call's memory is allocated: on its stream, whose queued work is done with what it gets."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
+def _used(stream: Optional[torch.cuda.Stream], device, inputs, outputs=()):
+    """Keep the memory of a call on a passed stream, also where the caller drops a tensor before it has
+    run: inputs until that stream is done with them, outputs (allocated on it) until the current one is."""
+    if stream is None:
+        return
+    here = torch.cuda.current_stream(device)
+    if stream.cuda_stream == here.cuda_stream:
+        return
+    for tensors, by in ((inputs, stream), (outputs, here)):
+        for t in tensors:
+            if t is not None and t.is_cuda:
+                t.record_stream(by)
+
+
 def _need(t: torch.Tensor, name: str, dtype=None, device=None):
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
@@ -299,18 +319,21 @@ def chunk_fwd(q, k, v, g, beta, theta=None, S0=None, *, gate_mode=GATE_NEG_SOFTP
             raise ValueError("S0 has the wrong shape")
     # outputs it allocates are page-locked when the inputs are (asynchronous copies)
     pin = host and any(t.is_pinned() for t in (q, S0) if t is not None and t.numel() > 0)
-    if o is None:
-        o = torch.empty((B, T, H, dv), dtype=out_dtype, device=dev, pin_memory=pin)
+    theirs = (q, k, v, g, beta, theta, w, S0, o, S_T, chunk_mean, workspace)
+    with _memory(stream):
+        if o is None:
+            o = torch.empty((B, T, H, dv), dtype=out_dtype, device=dev, pin_memory=pin)
+        if S_T is None and want_state:
+            S_T = torch.empty((B, H, dv, dk), dtype=torch.float32, device=dev, pin_memory=pin)
     _need(o, "o", out_dtype, dev)
-    if S_T is None and want_state:
-        S_T = torch.empty((B, H, dv, dk), dtype=torch.float32, device=dev, pin_memory=pin)
     if S_T is not None:
         _need(S_T, "S_T", torch.float32, dev)
     with_mean = want_chunk_mean or chunk_mean is not None
     if with_mean:
         nc = (T + chunk - 1) // chunk
         if chunk_mean is None:
-            chunk_mean = torch.empty((B, nc, H, dv), dtype=torch.float32, device=dev, pin_memory=pin)
+            with _memory(stream):
+                chunk_mean = torch.empty((B, nc, H, dv), dtype=torch.float32, device=dev, pin_memory=pin)
         _need(chunk_mean, "chunk_mean", torch.float32, dev)
         if tuple(chunk_mean.shape) != (B, nc, H, dv):
             raise ValueError("chunk_mean has the wrong shape")
@@ -321,7 +344,8 @@ def chunk_fwd(q, k, v, g, beta, theta=None, S0=None, *, gate_mode=GATE_NEG_SOFTP
         cdev = torch.device("cuda", torch.cuda.current_device())
         need = host_workspace_bytes(desc, w is not None, S0 is not None, S_T is not None, with_mean)
         if workspace is None and need:
-            workspace = torch.empty(need, dtype=torch.uint8, device=cdev)
+            with _memory(stream):
+                workspace = torch.empty(need, dtype=torch.uint8, device=cdev)
         ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
         st = lib().gdr_chunk_fwd_host(ctypes.byref(desc), _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta),
                                       _ptr(w), _ptr(theta), _ptr(S0), _ptr(o), _ptr(S_T), _ptr(chunk_mean),
@@ -331,8 +355,10 @@ def chunk_fwd(q, k, v, g, beta, theta=None, S0=None, *, gate_mode=GATE_NEG_SOFTP
         return out
     need = workspace_bytes(desc)
     if need and workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        with _memory(stream):
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _used(stream, dev, theirs, out)
     if with_mean:
         st = lib().gdr_chunk_fwd_ex(ctypes.byref(desc), _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta),
                                     _ptr(w), _ptr(theta), _ptr(S0), _ptr(o), _ptr(S_T), _ptr(chunk_mean),
@@ -387,17 +413,21 @@ def chunk_bwd(q, k, v, g, beta, S0=None, dO=None, dS_T=None, *, gate_mode=GATE_N
         if tuple(dO.shape) != (B, T, H, dv):
             raise ValueError("dO has the wrong shape")
     f32 = dict(dtype=torch.float32, device=dev)
-    grads = {"q": torch.empty((B, T, H, dk), **f32), "k": torch.empty((B, T, H, dk), **f32),
-             "v": torch.empty((B, T, H, dv), **f32), "g": torch.empty((B, T, H, ng), **f32),
-             "beta": torch.empty((B, T, H), **f32), "w": None if w is None else torch.empty((B, T, H), **f32),
-             "theta": torch.empty((B, T, H, dk // 2), **f32) if rotation else None,
-             "S0": torch.empty((B, H, dv, dk), **f32) if want_dS0 else None}
+    with _memory(stream):
+        grads = {"q": torch.empty((B, T, H, dk), **f32), "k": torch.empty((B, T, H, dk), **f32),
+                 "v": torch.empty((B, T, H, dv), **f32), "g": torch.empty((B, T, H, ng), **f32),
+                 "beta": torch.empty((B, T, H), **f32), "w": None if w is None else torch.empty((B, T, H), **f32),
+                 "theta": torch.empty((B, T, H, dk // 2), **f32) if rotation else None,
+                 "S0": torch.empty((B, H, dv, dk), **f32) if want_dS0 else None}
     desc = fwd_desc(B, H, T, dk, dv, q.dtype, out_dtype, gate_mode, rotation, scale, "auto", chunk,
                     qk_l2norm=qk_l2norm)
     need = bwd_workspace_bytes(desc)
+    theirs = (q, k, v, g, beta, w, theta, S0, dO, dS_T, workspace)
     if need and workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        with _memory(stream):
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _used(stream, dev, theirs, grads.values())
     st = lib().gdr_chunk_bwd(ctypes.byref(desc), _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(w),
                              _ptr(theta), _ptr(S0), _ptr(dO), _ptr(dS_T), _ptr(grads["q"]), _ptr(grads["k"]),
                              _ptr(grads["v"]), _ptr(grads["g"]), _ptr(grads["beta"]), _ptr(grads["w"]),
@@ -445,14 +475,17 @@ def raven_fwd(q, k, v, z, g, S0k=None, S0v=None, *, topk, gate_mode=GATE_NEG_SOF
             _need(t, n, torch.float32, dev)
             if tuple(t.shape) != (B, H, 64, d):
                 raise ValueError(f"{n} has the wrong shape")
-    o = torch.empty((B, T, H, d), dtype=out_dtype, device=dev)
-    SkT = torch.empty((B, H, 64, d), dtype=torch.float32, device=dev) if want_state else None
-    SvT = torch.empty((B, H, 64, d), dtype=torch.float32, device=dev) if want_state else None
+    theirs = (q, k, v, z, g, S0k, S0v, workspace)
     desc = raven_desc(B, H, T, d, topk, out_dtype, gate_mode, scale, segments)
     need = raven_workspace_bytes(desc)
-    if need and workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    with _memory(stream):
+        o = torch.empty((B, T, H, d), dtype=out_dtype, device=dev)
+        SkT = torch.empty((B, H, 64, d), dtype=torch.float32, device=dev) if want_state else None
+        SvT = torch.empty((B, H, 64, d), dtype=torch.float32, device=dev) if want_state else None
+        if need and workspace is None:
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _used(stream, dev, theirs, (o, SkT, SvT))
     st = lib().gdr_raven_fwd(ctypes.byref(desc), _ptr(q), _ptr(k), _ptr(v), _ptr(z), _ptr(g), _ptr(S0k), _ptr(S0v),
                              _ptr(o), _ptr(SkT), _ptr(SvT), _ptr(workspace), ws_bytes, _stream_handle(stream, dev))
     _check(st, "gdr_raven_fwd")
@@ -478,8 +511,11 @@ def decode_step(q, k, v, g, beta, S, theta=None, *, gate_mode=GATE_NEG_SOFTPLUS,
         raise ValueError("S or g has the wrong shape")
     if theta is not None:
         _need(theta, "theta", torch.float32, dev)
+    theirs = (q, k, v, g, beta, S, theta, w, o)
     if o is None:
-        o = torch.empty((N, H, dv), dtype=out_dtype, device=dev)
+        with _memory(stream):
+            o = torch.empty((N, H, dv), dtype=out_dtype, device=dev)
+    _used(stream, dev, theirs, (o,))
     desc = DecDesc(N, H, dk, dv, _dtype_code(q.dtype), _dtype_code(out_dtype), int(gate_mode),
                    int(rotation), float(scale), int(bool(qk_l2norm)))
     if w is not None:

@@ -24,8 +24,19 @@ def _calls(G):
     _, mean, rstd = G.layernorm_fwd(y, w)
     nd = G.norm_desc(3000, 512, y.dtype, dy.dtype)
     z, sc = r(16, 8, 20000), r(16, 8)
+    q, k, v, rk = (torch.nn.functional.normalize(r(2, 512, 4, 128), dim=-1).bfloat16() for _ in range(4))
+    a, beta, S = r(2, 512, 4, 128), torch.rand((2, 512, 4), generator=gen, device="cuda"), r(2, 4, 128, 128) * 0.1
+    fd = G.fwd_desc(2, 4, 512, 128, 128, q.dtype, q.dtype)
+    rv, zr, gr = r(2, 512, 4, 128).bfloat16(), r(2, 512, 4, 64), r(2, 512, 4)
     parent = torch.randint(0, 8, (16, 8), generator=gen, device="cuda", dtype=torch.int32)
     return {
+        "chunk_fwd": ((q, k, v, a, beta), G.chunk_fwd, G.workspace_bytes(fd)),
+        "chunk_bwd": ((q, k, v, a, beta, S, v), lambda *a, **k: [t for t in G.chunk_bwd(*a, **k).values() if t is not None],
+                      G.bwd_workspace_bytes(fd)),
+        "decode_step": ((q[:, 0].contiguous(), k[:, 0].contiguous(), v[:, 0].contiguous(), a[:, 0].contiguous(),
+                         beta[:, 0].contiguous(), S), lambda *a, **k: (G.decode_step(*a, **k),), 0),
+        "raven_fwd": ((rk, k, rv, zr, gr), lambda *a, **k: G.raven_fwd(*a, topk=8, **k),
+                      G.raven_workspace_bytes(G.raven_desc(2, 4, 512, 128, 8))),
         "scan_fwd": ((x, g, h0), lambda x, g, h0, **k: G.scan_fwd(x, g, h0, want_ckpt=True, **k), 0),
         "scan_bwd": ((x, g, ck, dh, h0), lambda *a, **k: list(G.scan_bwd(*a, **k).values()), 0),
         "scan_step": ((x[:, 0].contiguous(), g[:, 0].contiguous(), h0), lambda *a, **k: (G.scan_step(*a, **k),), 0),
@@ -38,7 +49,8 @@ def _calls(G):
     }
 
 
-NAMES = ["scan_fwd", "scan_bwd", "scan_step", "layernorm_fwd", "layernorm_bwd", "beam_select", "state_reorder"]
+NAMES = ["chunk_fwd", "chunk_bwd", "decode_step", "raven_fwd", "scan_fwd", "scan_bwd", "scan_step", "layernorm_fwd",
+         "layernorm_bwd", "beam_select", "state_reorder"]
 
 
 @pytest.mark.parametrize("name", NAMES)
@@ -56,7 +68,7 @@ def test_memory_stays_until_the_stream_is_done(G, name):
             torch.cuda._sleep(2_000_000)
         stream = torch.cuda.ExternalStream(side.cuda_stream) if external else side
         got = list(call(*theirs, stream=stream))
-        if name not in ("scan_step", "state_reorder"):      # outputs that are dropped at once
+        if name not in ("scan_step", "state_reorder", "decode_step"):      # outputs that are dropped at once
             call(*theirs, stream=stream)
         del theirs
         sizes = {v.numel() * v.element_size() for v in (*inputs, *want)} | ({ws} if ws else set())
