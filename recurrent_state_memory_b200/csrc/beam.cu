@@ -100,7 +100,7 @@ static gdr_status launch_reorder(int L, ReorderParams p, size_t bytes, cudaStrea
 
 }  // namespace bms
 
-cudaError_t beam_take_status(unsigned int* word, unsigned int* site) { return take_status_here(word, site); }
+cudaError_t beam_status(StatusWords* w) { return status_here(w); }
 
 }  // namespace gdr
 

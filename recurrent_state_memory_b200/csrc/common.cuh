@@ -33,19 +33,11 @@ __device__ __forceinline__ bool in_bounds(bool c, unsigned site) {
 #define GDR_INB(cond, site) true
 #endif
 
-// Read and clear this translation unit's status word / first bounds site (NULL: not asked for).
-static inline cudaError_t take_status_here(unsigned int* word, unsigned int* site) {
-    const unsigned int zero = 0;
-    cudaError_t e = cudaSuccess;
-    if (word) {
-        e = cudaMemcpyFromSymbol(word, g_device_status, sizeof(zero));
-        if (e == cudaSuccess && *word) e = cudaMemcpyToSymbol(g_device_status, &zero, sizeof(zero));
-    }
-    if (site && e == cudaSuccess) {
-        e = cudaMemcpyFromSymbol(site, g_bounds_site, sizeof(zero));
-        if (e == cudaSuccess && *site) e = cudaMemcpyToSymbol(g_bounds_site, &zero, sizeof(zero));
-    }
-    return e;
+// Where this translation unit's status word and first bounds site are on the current device.
+struct StatusWords { unsigned int *word, *site; };
+static inline cudaError_t status_here(StatusWords* w) {
+    const cudaError_t e = cudaGetSymbolAddress(reinterpret_cast<void**>(&w->word), g_device_status);
+    return e == cudaSuccess ? cudaGetSymbolAddress(reinterpret_cast<void**>(&w->site), g_bounds_site) : e;
 }
 
 // Element loads/stores with the storage type chosen at compile time.

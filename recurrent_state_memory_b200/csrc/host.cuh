@@ -74,10 +74,11 @@ inline gdr_status encode_fn(EncodeTiledFn* out) {
     return GDR_OK;
 }
 
-// Every translation unit has a status word and a bounds site of its own (common.cuh); these read
-// and clear the ones of the files named.  *site is only written in the debug build.
-cudaError_t scan_take_status(unsigned int* word, unsigned int* site);
-cudaError_t norm_take_status(unsigned int* word, unsigned int* site);
-cudaError_t beam_take_status(unsigned int* word, unsigned int* site);
+// Every translation unit has a status word and a bounds site of its own (common.cuh): the ones of the
+// files named.
+struct StatusWords;
+cudaError_t scan_status(StatusWords* w);
+cudaError_t norm_status(StatusWords* w);
+cudaError_t beam_status(StatusWords* w);
 
 }  // namespace gdr

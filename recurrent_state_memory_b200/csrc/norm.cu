@@ -193,7 +193,7 @@ static gdr_status check_desc(const gdr_norm_desc* d) {
 
 }  // namespace lnm
 
-cudaError_t norm_take_status(unsigned int* word, unsigned int* site) { return take_status_here(word, site); }
+cudaError_t norm_status(StatusWords* w) { return status_here(w); }
 
 }  // namespace gdr
 

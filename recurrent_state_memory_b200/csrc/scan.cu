@@ -205,7 +205,7 @@ static gdr_status copy_state(float* dst, const float* src, size_t n, cudaStream_
 
 }  // namespace scn
 
-cudaError_t scan_take_status(unsigned int* word, unsigned int* site) { return take_status_here(word, site); }
+cudaError_t scan_status(StatusWords* w) { return status_here(w); }
 
 }  // namespace gdr
 
