@@ -1,5 +1,6 @@
 """Build libgdr.so (the CUDA library) in-tree for sm_100a with nvcc, and _binding.so (the host side of
-some of its Python calls) with g++.
+some of its Python calls) with g++.  The library needs nvcc alone; the binding needs g++ and the
+headers of the installed torch, and without those it is left out with a warning.
 
     python -m recurrent_state_memory_b200.build [--force]
 """
@@ -7,6 +8,7 @@ import os
 import subprocess
 import sys
 import sysconfig
+import warnings
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -22,6 +24,7 @@ CXX = os.environ.get("CXX", "g++")
 
 SOURCES = ["gdr.cu", "scan.cu", "norm.cu", "beam.cu"]
 OBJ = os.path.join(PKG, "_build")                   # object files, one folder per build kind
+BINDING_MADE_FOR = os.path.join(OBJ, "binding.txt") # the torch and Python that _binding.so was built against
 
 
 def _deps():
@@ -40,25 +43,39 @@ def _fresh(out, dep):
     return all(os.path.exists(f) and os.path.getmtime(f) <= made for f in files + [os.path.abspath(__file__)])
 
 
+def _torch_and_python() -> str:
+    import torch
+    return f"torch {torch.__version__} {sysconfig.get_config_var('SOABI')}"
+
+
 def build_binding(force: bool = False) -> str:
-    """Build _binding.so (csrc/binding.cpp) against the installed torch."""
+    """Build _binding.so (csrc/binding.cpp) against the installed torch; built again when that changes."""
+    import torch
     src = os.path.join(CSRC, "binding.cpp")
     made_from = [src, os.path.join(INCLUDE, "gdr.h"), os.path.abspath(__file__)]
-    if not force and os.path.exists(BINDING) and os.path.getmtime(BINDING) >= max(map(os.path.getmtime, made_from)):
+    made_for = _torch_and_python()
+    if not force and os.path.exists(BINDING) and os.path.getmtime(BINDING) >= max(map(os.path.getmtime, made_from)) \
+            and os.path.exists(BINDING_MADE_FOR) and open(BINDING_MADE_FOR).read() == made_for:
         return BINDING
-    import torch
     from torch.utils import cpp_extension
     paths = cpp_extension.include_paths() + [sysconfig.get_paths()["include"], os.path.join(os.path.dirname(
         os.path.dirname(NVCC)), "include")]
+    for header in ("torch/extension.h", "Python.h"):
+        if not any(os.path.exists(os.path.join(p, header)) for p in paths):
+            raise FileNotFoundError(f"{header} is not installed")
     libs = os.path.join(os.path.dirname(torch.__file__), "lib")
     tmp = BINDING + ".tmp"
     cmd = [CXX, "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-I", INCLUDE]
     for p in paths:
         cmd += ["-isystem", p]
-    cmd += [f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", src, "-o", tmp, "-L", libs,
+    cmd += [f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+            f'-DGDR_BUILT_WITH_TORCH="{torch.__version__}"', src, "-o", tmp, "-L", libs,
             "-ltorch", "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python", "-lc10", "-lc10_cuda", "-ldl"]
     subprocess.run(cmd, check=True)
     os.replace(tmp, BINDING)
+    os.makedirs(OBJ, exist_ok=True)
+    with open(BINDING_MADE_FOR, "w") as f:
+        f.write(made_for)
     return BINDING
 
 
@@ -66,9 +83,17 @@ def build(force: bool = False, verbose: bool = False, debug: bool = False) -> st
     """Build libgdr.so (and _binding.so), or with debug=True libgdr_debug.so (-DGDR_BOUNDS_CHECK: every kernel
     tests the indices of the global-memory accesses it computes and reports a failure through
     the status word instead of making the access)."""
-    lib = LIB_DEBUG if debug else LIB
-    if not debug:
+    if debug:
+        return _build_library(LIB_DEBUG, force, verbose, True)
+    lib = _build_library(LIB, force, verbose, False)
+    try:
         build_binding(force)
+    except (ImportError, FileNotFoundError) as e:       # no torch, no headers, no compiler
+        warnings.warn(f"_binding.so is not built, gdr's calls of the scan, layer norm and beam search will not work: {e}")
+    return lib
+
+
+def _build_library(lib, force, verbose, debug) -> str:
     if not force and os.path.exists(lib):
         newest = max(os.path.getmtime(f) for f in _deps())
         if os.path.getmtime(lib) >= newest:

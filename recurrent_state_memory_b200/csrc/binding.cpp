@@ -333,6 +333,7 @@ Tensor state_reorder(const Tensor& S, const Tensor& parent, bool layers, const p
 }  // namespace
 
 PYBIND11_MODULE(_binding, m) {
+    m.attr("torch_version") = GDR_BUILT_WITH_TORCH;
     m.def("load", &load);
     m.def("row_stride", &row_stride);
     m.def("scan_fwd", &scan_fwd);

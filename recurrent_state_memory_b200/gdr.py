@@ -548,6 +548,9 @@ def _ops():
             raise RuntimeError(f"{BINDING_PATH} is missing: build it with "
                                "`python -m recurrent_state_memory_b200.build`")
         from . import _binding as module
+        if module.torch_version != torch.__version__:
+            raise RuntimeError(f"{BINDING_PATH} was built against torch {module.torch_version}, this is "
+                               f"{torch.__version__}: build it again with `python -m recurrent_state_memory_b200.build`")
         module.load(LIB_PATH)
         _binding = module
     return _binding
