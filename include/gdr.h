@@ -611,9 +611,10 @@ GDR_API gdr_status gdr_state_reorder(const gdr_reorder_desc* desc, void* S, cons
  * memory and returns, and gdr_query_device_status reports GDR_ERR_TIMEOUT.  Outputs of
  * such a launch are not valid.  Nothing faults or traps.
  */
-/* Debug build (libgdr_debug.so, compiled with -DGDR_BOUNDS_CHECK): every kernel tests the
- * index of each global-memory access that it computes (ring slots and flags, outputs, the
- * states, beta) before making it; a failing test skips the access, records its site number and
+/* Debug build (libgdr_debug.so, compiled with -DGDR_BOUNDS_CHECK): the kernels test the indices
+ * that they compute for global memory (ring slots and flags, outputs, the states, beta; rows and
+ * chunks of the layer norm, candidates, checkpoints) where their source marks it, before the
+ * access; a failing test skips the access, records its site number and
  * sets the status word's bounds bit (gdr_query_device_status -> GDR_ERR_BOUNDS).  Returns and
  * clears the first failing site (0: none), or -1 in the default build, which has no checks. */
 GDR_API int gdr_debug_bounds_site(void);

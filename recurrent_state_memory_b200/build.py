@@ -16,7 +16,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libgdr.so")
-LIB_DEBUG = os.path.join(PKG, "libgdr_debug.so")    # every kernel's computed indices checked
+LIB_DEBUG = os.path.join(PKG, "libgdr_debug.so")    # with the kernels' index checks
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 
 BINDING = os.path.join(PKG, "_binding.so")
@@ -80,9 +80,10 @@ def build_binding(force: bool = False) -> str:
 
 
 def build(force: bool = False, verbose: bool = False, debug: bool = False) -> str:
-    """Build libgdr.so (and _binding.so), or with debug=True libgdr_debug.so (-DGDR_BOUNDS_CHECK: every kernel
-    tests the indices of the global-memory accesses it computes and reports a failure through
-    the status word instead of making the access)."""
+    """Build libgdr.so (and _binding.so), or with debug=True libgdr_debug.so (-DGDR_BOUNDS_CHECK: the kernels
+    test the indices at their GDR_INB marks, which stand at global-memory accesses whose index is
+    computed, and report a failure through the status word instead of making the access; what a tensor
+    map or a loop's own bound keeps inside has no mark)."""
     if debug:
         return _build_library(LIB_DEBUG, force, verbose, True)
     lib = _build_library(LIB, force, verbose, False)

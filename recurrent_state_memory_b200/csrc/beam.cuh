@@ -166,15 +166,15 @@ __global__ void __launch_bounds__(NT, E > 8 && sizeof(XT) == 4 ? 4 : 6) beam_row
     for (int j = 0; j < E / W; ++j) {
         const int o = (j * NT + (int)threadIdx.x) * W;
         if constexpr (VEC) {
-            if (o + W <= n) {
+            if (o + W <= n && GDR_INB(v0 + o + W <= p.V, 1001)) {
                 const uint4 q = *reinterpret_cast<const uint4*>(x + o);
                 v.set(4 * j, q.x); v.set(4 * j + 1, q.y); v.set(4 * j + 2, q.z); v.set(4 * j + 3, q.w);
             } else {
 #pragma unroll
-                for (int i = 0; i < W; ++i) v.one(j * W + i, o + i < n ? ld_f32(x + o + i) : -INFINITY);
+                for (int i = 0; i < W; ++i) v.one(j * W + i, o + i < n && GDR_INB(v0 + o + i < p.V, 1002) ? ld_f32(x + o + i) : -INFINITY);
             }
         } else {
-            v.one(j, o < n ? ld_f32(x + o) : -INFINITY);
+            v.one(j, o < n && GDR_INB(v0 + o < p.V, 1004) ? ld_f32(x + o) : -INFINITY);
         }
     }
     if (threadIdx.x == 0) { count = 0; the_mark = 0; }
@@ -240,7 +240,7 @@ __global__ void __launch_bounds__(NT, E > 8 && sizeof(XT) == 4 ? 4 : 6) beam_row
             int rank = 0;
             for (int j = threadIdx.x & 7; j < have; j += 8) rank += list[j] > c;
             rank = sum8(rank);
-            if (i < have && (threadIdx.x & 7) == 0 && rank < p.M) {
+            if (i < have && (threadIdx.x & 7) == 0 && rank < p.M && GDR_INB(rank >= 0 && piece < p.pieces, 1003)) {
                 best[rank] = value_of((unsigned)(c >> 32));
                 token[rank] = v0 + (int)~(unsigned)c;
             }
@@ -347,7 +347,7 @@ __global__ void __launch_bounds__(GNT) beam_group_kernel(BeamParams p) {
         const int i = index(u);
         hk[u] = i / per;
         hj[u] = i - hk[u] * per;
-        if (i < n) {
+        if (i < n && GDR_INB(i >= 0 && hk[u] < p.K && g < p.G, 1012)) {
             const size_t at = (size_t)g * n + i;
             ht[u] = p.token[at];
             hx[u] = p.best[at];
@@ -416,7 +416,7 @@ __global__ void __launch_bounds__(GNT) beam_group_kernel(BeamParams p) {
 #pragma unroll
             for (int u = 0; u < 4; ++u) {           // four loads in flight
                 const int i = i0 + u * GNT;
-                if (i < n) { t[u] = p.token[(size_t)g * n + i]; x[u] = p.best[(size_t)g * n + i]; }
+                if (i < n && GDR_INB(i >= 0 && g < p.G, 1013)) { t[u] = p.token[(size_t)g * n + i]; x[u] = p.best[(size_t)g * n + i]; }
             }
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
@@ -426,8 +426,7 @@ __global__ void __launch_bounds__(GNT) beam_group_kernel(BeamParams p) {
             }
         }
     };
-    const long long all = (long long)p.K * p.V;
-    const int want = p.M;                           // at most `all`
+    const int want = p.M;                           // at most K * V
     for (int turn = 0; turn < 2; ++turn) {
         unsigned mine = 0;
         each([&](const Cand& c) { mine = max(mine, key_of_score(c.s)); });
@@ -507,7 +506,7 @@ __global__ void __launch_bounds__(GNT) beam_group_kernel(BeamParams p) {
     for (int m = threadIdx.x; m < p.M; m += GNT) {
         const size_t at = (size_t)g * p.M + m;
         const Cand c = first[m];
-        if (!GDR_INB(c.at >= 0 && (long long)c.at < all, 1011)) continue;
+        if (!GDR_INB(c.at >= 0 && c.at < (long long)p.K * p.V, 1011)) continue;
         p.out_scores[at] = (float)c.s;
         p.out_parent[at] = c.at / p.V;
         p.out_token[at] = c.at % p.V;
@@ -541,7 +540,7 @@ __global__ void __launch_bounds__(NT) reorder_kernel(ReorderParams p) {
 #pragma unroll
         for (int j = 0; j < KMAX; ++j) {
             const int q = j < p.K ? parent[j] : j;
-            moves[j] = q != j && q >= 0 && q < p.K;
+            moves[j] = q != j && q >= 0 && q < p.K && GDR_INB(j < p.K && i < p.n, 1021);
             if (moves[j]) v[j] = S[(size_t)q * p.n + i];
         }
 #pragma unroll

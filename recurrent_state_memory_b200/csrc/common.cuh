@@ -29,8 +29,10 @@ __device__ __forceinline__ bool in_bounds(bool c, unsigned site) {
     return c;
 }
 #define GDR_INB(cond, site) ::gdr::in_bounds((cond), (site))
+#define GDR_AND_INB(cond, site) && ::gdr::in_bounds((cond), (site))
 #else
 #define GDR_INB(cond, site) true
+#define GDR_AND_INB(cond, site)         // behind a condition whose code should not notice the mark
 #endif
 
 // Where this translation unit's status word and first bounds site are on the current device.

@@ -274,6 +274,14 @@ template <int V> __device__ __forceinline__ void only_row(Vals<V>& v, int c, int
     for (int i = 0; i < V; ++i)
         if ((unsigned)(c + i) >= (unsigned)D) v.set(i, 0.f);
 }
+// Debug build: n elements from column c of row r on lie in the tensor; a chunk that begins there, in a
+// shifted row perhaps outside of it, holds some of the row.
+__device__ __forceinline__ bool in_tensor(const NormParams& p, long long r, int c, int n) {
+    return r >= 0 && r < p.rows && r * p.D + c >= 0 && r * p.D + c + n <= p.rows * p.D;
+}
+template <int V, bool SHIFT> __device__ __forceinline__ bool in_row(const NormParams& p, long long r, int c) {
+    return r >= 0 && r < p.rows && (SHIFT ? c + V > 0 && c < p.D : c >= 0 && c + V <= p.D);
+}
 // A row's last chunk at the tensor's end: left out of the loads ahead (a load within a branch would
 // wait there), read by elements where it is used.  Elsewhere a chunk is read whole; its other
 // columns are the neighbouring rows'.
@@ -349,7 +357,8 @@ __global__ void __launch_bounds__(threads<G>(), fwd_blocks<SHIFT>(V, N, threads<
 #pragma unroll
             for (int j = 0; j < N; ++j) {
                 const int c = c0 + j * G * V;
-                if (r + u * at.dist < p.rows && c < p.D && !at_end<V, SHIFT>(c, p.D, r + u * at.dist == p.rows - 1))
+                if (r + u * at.dist < p.rows && c < p.D && !at_end<V, SHIFT>(c, p.D, r + u * at.dist == p.rows - 1)
+                    GDR_AND_INB(in_tensor(p, r + u * at.dist, c, V), 902))
                     raw[u][j].load(x + u * next + j * G * V);
                 else raw[u][j].zero();
             }
@@ -381,7 +390,8 @@ __global__ void __launch_bounds__(threads<G>(), fwd_blocks<SHIFT>(V, N, threads<
             for (int j = 0; j < N; ++j) {
                 if constexpr (SHIFT) {
                     const int c = c0 + j * G * V;
-                    if (c < p.D && at_end<V, SHIFT>(c, p.D, r + u * at.dist == p.rows - 1))
+                    if (c < p.D && at_end<V, SHIFT>(c, p.D, r + u * at.dist == p.rows - 1)
+                        GDR_AND_INB(in_tensor(p, r + u * at.dist, c, p.D - c), 903))
                         raw[u][j].load_part(x - jump + u * next + j * G * V, p.D - c);
                     raw[u][j] &= mx[j];
                 }
@@ -419,7 +429,7 @@ __global__ void __launch_bounds__(threads<G>(), fwd_blocks<SHIFT>(V, N, threads<
             rs.all(rstd[u]);
             auto put = [&](int j, const Vals<V>& wv, const Vals<V>& bv) {
                 const Vals<V> o = fma(v[u][j] * rs, wv, bv);
-                if (c0 + j * G * V < p.D && GDR_INB(SHIFT || c0 + j * G * V + V <= p.D, 901))
+                if (c0 + j * G * V < p.D && GDR_INB((in_row<V, SHIFT>(p, r + u * at.dist, c0 + j * G * V)), 901))
                     store_chunk<SHIFT>(y + u * next + j * G * V, o, c0 + j * G * V, p.D);
             };
             if constexpr (KEEP) {
@@ -483,7 +493,8 @@ __global__ void __launch_bounds__(threads<G>(), bwd_blocks(threads<G>())) norm_b
 #pragma unroll
             for (int j = 0; j < N; ++j) {
                 const int c = c0 + j * G * V;
-                if (in && c < p.D && !at_end<V, SHIFT>(c, p.D, r + u * at.dist == p.rows - 1)) {
+                if (in && c < p.D && !at_end<V, SHIFT>(c, p.D, r + u * at.dist == p.rows - 1)
+                    GDR_AND_INB(in_tensor(p, r + u * at.dist, c, V), 913)) {
                     rx[u][j].load(x + u * next + j * G * V);
                     rd[u][j].load(dy + u * next + j * G * V);
                 } else { rx[u][j].zero(); rd[u][j].zero(); }
@@ -516,7 +527,8 @@ __global__ void __launch_bounds__(threads<G>(), bwd_blocks(threads<G>())) norm_b
             for (int j = 0; j < N; ++j) {             // columns behind D: dy is zero
                 if constexpr (SHIFT) {
                     const int c = c0 + j * G * V;
-                    if (c < p.D && at_end<V, SHIFT>(c, p.D, r + u * at.dist == p.rows - 1)) {
+                    if (c < p.D && at_end<V, SHIFT>(c, p.D, r + u * at.dist == p.rows - 1)
+                        GDR_AND_INB(in_tensor(p, r + u * at.dist, c, p.D - c), 914)) {
                         rx[u][j].load_part(x - jump + u * next + j * G * V, p.D - c);
                         rd[u][j].load_part(dy - jump + u * next + j * G * V, p.D - c);
                     }
@@ -547,7 +559,7 @@ __global__ void __launch_bounds__(threads<G>(), bwd_blocks(threads<G>())) norm_b
 #pragma unroll
                 for (int j = 0; j < N; ++j) {
                     const Vals<V> o = (d[u][j] + fma(xh[u][j], m2, m1)) * rs;
-                    if (c0 + j * G * V < p.D && GDR_INB(SHIFT || c0 + j * G * V + V <= p.D, 911))
+                    if (c0 + j * G * V < p.D && GDR_INB((in_row<V, SHIFT>(p, r + u * at.dist, c0 + j * G * V)), 911))
                         store_chunk<SHIFT>(dx + u * next + j * G * V, o, c0 + j * G * V, p.D);
                 }
             }
@@ -560,7 +572,7 @@ __global__ void __launch_bounds__(threads<G>(), bwd_blocks(threads<G>())) norm_b
 #pragma unroll
         for (int j = 0; j < N; ++j) {
             const int c = c0 + j * G * V;
-            if (c >= p.D) continue;
+            if (!(c < p.D GDR_AND_INB((int)blockIdx.x < p.parts && (SHIFT || c + V <= p.D), 915))) continue;
             if (p.part_w) store_part<SHIFT>(p.part_w + base + c, sw[j], c, p.D);
             if (p.part_b) store_part<SHIFT>(p.part_b + base + c, sb[j], c, p.D);
         }
@@ -574,13 +586,13 @@ __global__ void __launch_bounds__(threads<G>(), bwd_blocks(threads<G>())) norm_b
 #pragma unroll
             for (int j = 0; j < N; ++j) {
                 const int c = c0 + j * G * V;
-                if (c < p.D) store_part<SHIFT>(part + (size_t)g * p.D + c, which ? sb[j] : sw[j], c, p.D);
+                if (c < p.D GDR_AND_INB(g < at.PER && (SHIFT || c + V <= p.D), 916)) store_part<SHIFT>(part + (size_t)g * p.D + c, which ? sb[j] : sw[j], c, p.D);
             }
             __syncthreads();
             for (int c = threadIdx.x; c < p.D; c += WARP_NT) {
                 float s = 0.f;
                 for (int i = 0; i < at.PER; ++i) s += part[(size_t)i * p.D + c];
-                to[base + c] = s;
+                if (GDR_INB((int)blockIdx.x < p.parts, 917)) to[base + c] = s;
             }
         }
     }
@@ -632,7 +644,7 @@ __global__ void __launch_bounds__(WIDE_NT) norm_bwd_wide_kernel(NormParams p) {
         const float mean = p.mean[r], rstd = p.rstd[r];
         Raw<XT, V> rx[N];
         Raw<YT, V> rd[N];
-        each([&](int j, int c) { rx[j].load(x + c); rd[j].load(dy + c); });
+        each([&](int j, int c) { if (GDR_INB(c0 + c + V <= p.D, 918)) { rx[j].load(x + c); rd[j].load(dy + c); } });
         if (r + gridDim.x < p.rows) {
             const size_t next = (size_t)gridDim.x * p.D;
             each([&](int, int c) {
@@ -677,6 +689,7 @@ __global__ void __launch_bounds__(WIDE_NT) norm_bwd_wide_kernel(NormParams p) {
     asm volatile("griddepcontrol.launch_dependents;");
     const size_t base = (size_t)blockIdx.x * p.D + c0;
     each([&](int j, int c) {
+        if (!GDR_INB((int)blockIdx.x < p.parts && c0 + c + V <= p.D, 919)) return;
         if (p.part_w) store_v<float, V>(p.part_w + base + c, get(0, j));
         if (p.part_b) store_v<float, V>(p.part_b + base + c, get(1, j));
     });
@@ -754,6 +767,7 @@ __global__ void __launch_bounds__(256) norm_part_long_kernel(NormParams p) {
         w = fmaf(dy, (ld_f32(static_cast<const XT*>(p.x) + (size_t)r * p.D + c) - p.mean[r]) * p.rstd[r], w);
         b += dy;
     }
+    if (!GDR_INB((int)blockIdx.y < p.parts, 920)) return;
     if (p.part_w) p.part_w[(size_t)blockIdx.y * p.D + c] = w;
     if (p.part_b) p.part_b[(size_t)blockIdx.y * p.D + c] = b;
 }

@@ -181,9 +181,9 @@ __device__ __forceinline__ void skews(const Phases<T, TOK, CH>& ph, const void* 
     for (int q = 0; q < ph.P; ++q) skew[q] = (int)(ph.start(base, row, c0, n0, q) % ph.P) + c;
 }
 template <typename T, int R>
-__device__ __forceinline__ void read_run_global(const T* src, long long row, int have, float (&v)[R][1]) {
+__device__ __forceinline__ void read_run_global(const T* src, long long row, int have, int limit, float (&v)[R][1]) {
 #pragma unroll
-    for (int r = 0; r < R; ++r) v[r][0] = r < have ? ld_f32(src + r * row) : 0.f;
+    for (int r = 0; r < R; ++r) v[r][0] = r < have && GDR_INB(r < limit, 804) ? ld_f32(src + r * row) : 0.f;
 }
 
 // Compose a warp's runs: in (A, H) of this thread's run; out the composition of the runs before
@@ -367,8 +367,8 @@ __global__ void __launch_bounds__(NT, V > 1 ? 2 : 3) scan_fwd_kernel(ScanParams 
                 read_run(sm.g[st], skew_g, l.first_token(), a);
                 read_run(sm.x[st], skew_x, l.first_token(), bb);
             } else {
-                read_run_global(g + t0 * p.g_row, p.g_row, on ? len - t0 : 0, a);
-                read_run_global(x + t0 * p.x_row, p.x_row, on ? len - t0 : 0, bb);
+                read_run_global(g + t0 * p.g_row, p.g_row, on ? len - t0 : 0, p.T - t0, a);
+                read_run_global(x + t0 * p.x_row, p.x_row, on ? len - t0 : 0, p.T - t0, bb);
             }
         }
         with_mode(p, [&](auto mode, auto tied) {
@@ -532,7 +532,7 @@ __global__ void __launch_bounds__(NT, 2) scan_bwd_kernel(ScanParams p, const __g
         float state = 0.f;
         if (l.warp == 1) {
             const int j = (base + tile) / CKPT;
-            if (j < nck && lane_c < p.D) state = p.ckpt[((size_t)b * nck + j) * p.D + lane_c];
+            if (j < nck && lane_c < p.D && GDR_INB(j >= 0 && b < p.B, 812)) state = p.ckpt[((size_t)b * nck + j) * p.D + lane_c];
         }
         float a[R][V], rest[R][V], xv[R][V], d[R][V];
 #pragma unroll
@@ -556,9 +556,9 @@ __global__ void __launch_bounds__(NT, 2) scan_bwd_kernel(ScanParams p, const __g
                 if (with_dh) read_run(sm.dh[st], skew_d, l.first_token(), d);
             } else {
                 const int have = on ? len - t0 : 0;
-                read_run_global(g + t0 * p.g_row, p.g_row, have, a);
-                read_run_global(x + t0 * p.x_row, p.x_row, have, xv);
-                if (with_dh) read_run_global(dh + (size_t)t0 * p.D, p.D, have, d);
+                read_run_global(g + t0 * p.g_row, p.g_row, have, p.T - t0, a);
+                read_run_global(x + t0 * p.x_row, p.x_row, have, p.T - t0, xv);
+                if (with_dh) read_run_global(dh + (size_t)t0 * p.D, p.D, have, p.T - t0, d);
             }
         }
         float A[V], H[V], M[V], dA[V], exA[V], exH[V], exD[V], exM[V];
