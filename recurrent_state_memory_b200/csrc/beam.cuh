@@ -152,9 +152,10 @@ __global__ void __launch_bounds__(NT, E > 8 && sizeof(XT) == 4 ? 4 : 6) beam_row
     __shared__ int count;
     __shared__ unsigned long long pick[WARPS];
     __shared__ unsigned long long list[LIST];       // key, then the token's complement: larger is better
-    const int row = blockIdx.z * gridDim.y + blockIdx.y, piece = blockIdx.x;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    if (row >= p.G * p.K) return;
+    // unsigned: the last rows' grid reaches past 2^31 where G * K comes near it
+    const unsigned row = blockIdx.z * gridDim.y + blockIdx.y;
+    const int piece = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    if (row >= (unsigned)p.G * (unsigned)p.K) return;
     asm volatile("griddepcontrol.launch_dependents;");               // the groups' blocks may come; they wait
     const int v0 = piece * p.piece, n = min(p.piece, p.V - v0);      // this block's tokens
     const XT* x = static_cast<const XT*>(p.logits) + (size_t)row * p.row + v0;
