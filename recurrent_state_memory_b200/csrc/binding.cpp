@@ -89,6 +89,13 @@ void want(const MaybeTensor& t, const char* name, at::IntArrayRef shape, at::Sca
     if (t) want(*t, name, shape, type, dev);
 }
 
+// Its bytes are the memory that it has: an expanded or strided tensor has less, or other.
+void want_workspace(const MaybeTensor& t, at::Device dev) {
+    if (!t) return;
+    dense(*t, "workspace");
+    on(*t, "workspace", dev);
+}
+
 // Elements between the rows of t (dense: 0), whose rows are dense and evenly spaced (a slice along the
 // last dimension of a wider contiguous tensor is).
 int64_t row_stride(const Tensor& t, const char* name) {
@@ -268,7 +275,7 @@ py::dict layernorm_bwd(const Tensor& x, const Tensor& dy, const Tensor& mean, co
     want(dy, "dy", x.sizes(), at::ScalarType::Undefined, dev);
     want(mean, "mean", rows, at::kFloat, dev);
     want(rstd, "rstd", rows, at::kFloat, dev);
-    if (workspace) on(*workspace, "workspace", dev);
+    want_workspace(workspace, dev);
     const Call call(dev, stream);
     call.uses(x, dy, mean, rstd, weight, workspace);
     MaybeTensor dx, dw, db;
@@ -294,7 +301,7 @@ py::tuple beam_select(const Tensor& logits, const Tensor& scores, const std::opt
     const int64_t G = logits.size(0), K = logits.size(1), M = n_out.value_or(K);
     want(scores, "scores", {G, K}, at::kFloat, dev);
     want(finished, "finished", {G, K}, at::kBool, dev);
-    if (workspace) on(*workspace, "workspace", dev);
+    want_workspace(workspace, dev);
     gdr_beam_desc d;
     d.G = size32(G, "G"); d.K = size32(K, "K"); d.V = size32(logits.size(2), "V"); d.M = size32(std::max<int64_t>(M, 0), "n_out");
     d.row = row_stride(logits, "logits");

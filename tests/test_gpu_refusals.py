@@ -1,0 +1,30 @@
+"""Arguments of the scan, layer norm and beam calls that are refused before anything is allocated or launched."""
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def G():
+    from recurrent_state_memory_b200 import gdr
+    gdr.lib()
+    return gdr
+
+
+def test_a_workspace_that_is_less_memory_than_its_size(G):
+    """Expanded and strided tensors have other memory than numel * element_size bytes from their start on."""
+    import torch
+    x = torch.randn(64, 256, device="cuda")
+    _, mean, rstd = G.layernorm_fwd(x)
+    z, s = torch.randn(2, 4, 3000, device="cuda"), torch.randn(2, 4, device="cuda")
+    for ws in (torch.empty(1, dtype=torch.uint8, device="cuda").expand(1 << 24),
+               torch.empty(1 << 20, 64, dtype=torch.uint8, device="cuda")[:, ::2]):
+        with pytest.raises(ValueError, match="workspace must be contiguous"):
+            G.layernorm_bwd(x, x, mean, rstd, workspace=ws)
+        with pytest.raises(ValueError, match="workspace must be contiguous"):
+            G.beam_select(z, s, workspace=ws)
+    for ws in (torch.empty(1 << 24, dtype=torch.uint8), torch.empty(16, dtype=torch.uint8, device="cuda")):
+        with pytest.raises(ValueError if not ws.is_cuda else G.GdrError):
+            G.layernorm_bwd(x, x, mean, rstd, workspace=ws)
+        with pytest.raises(ValueError if not ws.is_cuda else G.GdrError):
+            G.beam_select(z, s, workspace=ws)
