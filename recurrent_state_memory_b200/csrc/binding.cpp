@@ -310,6 +310,8 @@ py::tuple beam_select(const Tensor& logits, const Tensor& scores, const std::opt
     const Call call(dev, stream);
     call.uses(logits, scores, finished, workspace);
     const size_t need = api.beam_select_workspace_bytes(&d);
+    if (!need)      // nothing to do, or sizes that are refused, before outputs of them are allocated
+        check(api.beam_select(&d, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, 0, call.stream), "gdr_beam_select");
     Tensor out = call.output({G, d.M}, at::kFloat), parent = call.output({G, d.M}, at::kInt), token = call.output({G, d.M}, at::kInt);
     const MaybeTensor ws = workspace ? workspace : need ? MaybeTensor(call.scratch({static_cast<int64_t>(need)}, at::kByte)) : MaybeTensor();
     check(api.beam_select(&d, at_(logits), at_<float>(scores), at_<unsigned char>(finished), at_<float>(out), at_<int>(parent),

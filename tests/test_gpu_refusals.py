@@ -28,3 +28,16 @@ def test_a_workspace_that_is_less_memory_than_its_size(G):
             G.layernorm_bwd(x, x, mean, rstd, workspace=ws)
         with pytest.raises(ValueError if not ws.is_cuda else G.GdrError):
             G.beam_select(z, s, workspace=ws)
+
+
+def test_more_candidates_than_there_may_be(G):
+    """Refused by the library's own error, without memory for as many outputs."""
+    import torch
+    z, s = torch.randn(64, 4, 300, device="cuda"), torch.randn(64, 4, device="cuda")
+    torch.cuda.reset_peak_memory_stats()
+    before = torch.cuda.memory_allocated()
+    for n in (0, -3, 65, 1 << 30):
+        with pytest.raises(G.GdrError, match="1 .. 64"):
+            G.beam_select(z, s, n)
+    assert torch.cuda.max_memory_allocated() == before
+    assert [t.shape for t in G.beam_select(z[:0], s[:0], 3)] == [(0, 3)] * 3
