@@ -103,13 +103,14 @@ template <typename XT, typename GT, typename OT, int V, int CH>
 static gdr_status launch_sequences(Pass pass, ScanParams& p, cudaStream_t st) {
     const int tok = pass == FWD ? Tile<V, fwd_elems<V>(), CH>::TOK : Tile<V, BWD_ELEMS, CH>::TOK;
     ScanMaps maps = {};
-    // V = 1: whole groups of 8 rows, where the copies' coordinates and sizes fit their types
+    // V = 1: whole groups of 8 rows, where the copies' coordinates (of 8 rows in 16 bits, of 4 in 32) and
+    // sizes fit their types
     const long long rows = (long long)p.B * p.T, wide = p.x_row > p.g_row ? p.x_row : p.g_row;
     auto inside = [&](const void* q, long long row, size_t el) {    // a long row does not reach into the next one
         const long long lead = (long long)(reinterpret_cast<uintptr_t>(q) % 16 / el);
         return lead == 0 || lead + p.D <= row;
     };
-    const bool fits = rows / 8 < (1LL << 31) - 1 && wide < (1LL << 27) && rows * wide < (1LL << 37) &&
+    const bool fits = rows / 4 < (1LL << 31) - 1 && wide < (1LL << 27) && rows * wide < (1LL << 37) &&
                       inside(p.x, p.x_row, sizeof(XT)) && inside(p.g, p.g_row, sizeof(GT)) &&
                       (pass != BWD || inside(p.dh, p.D, sizeof(OT)));
     p.covered = fits ? rows / 8 * 8 : 0;
