@@ -97,15 +97,22 @@ void want_workspace(const MaybeTensor& t, at::Device dev) {
 }
 
 // Elements between the rows of t (dense: 0), whose rows are dense and evenly spaced (a slice along the
-// last dimension of a wider contiguous tensor is).
+// last dimension of a wider contiguous tensor is).  What a dimension of one has for a stride is nothing.
 int64_t row_stride(const Tensor& t, const char* name) {
     if (t.is_contiguous()) return 0;
     const auto st = t.strides(), sh = t.sizes();
     const int64_t n = t.dim();
-    bool ok = n >= 2 && st[n - 1] == 1 && st[n - 2] >= sh[n - 1];
-    for (int64_t d = n - 3; ok && d >= 0; --d) ok = sh[d] == 1 || st[d] == st[d + 1] * sh[d + 1];
-    if (!ok) throw py::value_error(std::string(name) + " must be contiguous, or a slice of a contiguous tensor along its last dimension");
-    return st[n - 2];
+    bool ok = n >= 2 && (st[n - 1] == 1 || sh[n - 1] == 1);
+    int64_t row = -1, next = 0;             // the rows' distance, once known, and what the next dimension outwards must have
+    for (int64_t d = n - 2; ok && d >= 0; --d) {
+        if (sh[d] == 1) continue;
+        if (row < 0) row = next = st[d];
+        ok = st[d] == next;
+        next *= sh[d];
+    }
+    if (!ok || row < sh[n - 1])
+        throw py::value_error(std::string(name) + " must be contiguous, or a slice of a contiguous tensor along its last dimension");
+    return row;
 }
 
 // A call: its device, current while this lives, and its stream, the given one or the current one.  With
