@@ -102,3 +102,47 @@ def test_work_queued_on_the_current_stream_is_left_alone(G, name):
     keep = call(*theirs, stream=side)
     torch.cuda.synchronize()
     assert all(bool((c == 3).all()) for c in copies) and keep is not None
+
+
+@pytest.mark.parametrize("name", NAMES)
+def test_the_default_stream_from_another_one(G, name):
+    """The passed stream is the default one and the current stream is not."""
+    import torch
+    inputs, call, _ = _calls(G)[name]
+    want = [v.clone() for v in call(*(v.clone() for v in inputs))]
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        theirs = [v.clone() for v in inputs]
+        torch.cuda.default_stream().wait_stream(side)
+        got = call(*theirs, stream=torch.cuda.default_stream())
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("name", [n for n in NAMES if n not in ("scan_step", "state_reorder", "decode_step")])
+def test_captured_on_a_branch(G, name):
+    """A graph whose call runs on a stream that branches off the captured one; the graph's memory is its own
+    and replays give the same again."""
+    import torch
+    inputs, call, _ = _calls(G)[name]
+    want = [v.clone() for v in call(*inputs)]
+    side = torch.cuda.Stream()
+    call(*inputs, stream=side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        side.wait_stream(torch.cuda.current_stream())
+        got = list(call(*inputs, stream=side))
+        call(*inputs, stream=side)                      # its outputs go at once
+        torch.cuda.current_stream().wait_stream(side)
+        sums = [v.double().sum() for v in got]
+    for _ in range(3):
+        junk = [torch.full_like(v, 7) for v in got]
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want)) and len(sums) == len(got)
+        del junk
+    del got, sums
+    torch.cuda.synchronize()
+    assert [torch.equal(a, b) for a, b in zip(call(*inputs), want)] == [True] * len(want)
