@@ -11,11 +11,12 @@
 //      larger ones ranks them.
 //   2. beam_group_kernel: a block per group merges its beams' pieces the same way.  Its sums hold
 //      fp32 exponentials, so two scores of different beams within TOL of each other may be in the
-//      wrong order.  Only candidates down to TOL below the M-th can belong to the M best; where two
-//      of these from different beams are that near (neighbours within the list, or any around its
-//      end), the beams' sums are formed again from the logits in 64 bits and the merge is repeated.
-//      A beam that is not summed again lies further than TOL from every other one's candidates, so
-//      the order is the 64-bit one.
+//      wrong order.  Only candidates down to TOL below the M-th can belong to the M best; where one
+//      of the M has one of another beam that near, itself among the M or not, both beams' sums are
+//      formed again from the logits in 64 bits and the merge is repeated.  What stays in fp32 lies
+//      further than TOL from everything that it could change places with, so the order is the
+//      64-bit one.  (The beams that are summed again go one after another through one block: 300 us
+//      where all of 32 x 8 x 32000 are, 1.4 ms for 1 x 16 x 262144; 13 and 17 us where none is.)
 //
 // Bound: the read of the logits (one exponential and about ten instructions each); for one small
 // group the latency of the two launches.
@@ -279,7 +280,7 @@ __global__ void __launch_bounds__(NT, E > 8 && sizeof(XT) == 4 ? 4 : 6) beam_row
 }
 
 // Candidates of a group: the larger score, of equal ones the lower k * V + v, goes first.
-struct Cand { double s; int at; };
+struct Cand { double s; int at, beam; };
 __device__ __forceinline__ bool before(const Cand& a, const Cand& b) { return a.s > b.s || (a.s == b.s && a.at < b.at); }
 // A key of 32 bits that never orders two scores the other way round (it may merge near ones).
 __device__ __forceinline__ unsigned key_of_score(double s) { return key_of(__double2float_rd(s)); }
@@ -291,6 +292,7 @@ __device__ __forceinline__ unsigned key_of_score(double s) { return key_of(__dou
 // each) 44 u: together 97 u of the sum, as much in its logarithm, whose rounding adds 17 u (it is at
 // most 22).  114 u = 6.8e-6, twice that for two beams.
 constexpr double TOL = 1.4e-5;
+constexpr float BELOW = 1.5e-5f;        // more than TOL
 
 constexpr int HELD = 2;                 // candidates of a thread that stay in registers
 
@@ -389,6 +391,7 @@ __global__ void __launch_bounds__(GNT) beam_group_kernel(BeamParams p) {
     __syncthreads();
 
     auto score_of = [&](int k, int j, int t, float x, Cand& c) -> bool {
+        c.beam = k;
         if (kind[k] == LIVE) {
             c.s = (double)score[k] + ((double)x - lse[k]);
             c.at = k * p.V + t;
@@ -434,12 +437,12 @@ __global__ void __launch_bounds__(GNT) beam_group_kernel(BeamParams p) {
         const int active = FEW ? 32 * min(GWARPS, span) : GNT, lanes = group_lanes(active, want);
         put_marks(mine, lanes, active, marks);
         if (threadIdx.x == 0) { count = 0; the_mark = 0; }
-        if (threadIdx.x < p.M) first[threadIdx.x] = Cand{-INFINITY, -1};
+        if (threadIdx.x < p.M) first[threadIdx.x] = Cand{-INFINITY, -1, 0};
         __syncthreads();
         find_mark<GWARPS>(marks, active / lanes, want, &the_mark);
         __syncthreads();
         // and down to TOL below it: the list also holds what may belong before its M-th
-        const unsigned mark = the_mark ? key_of_score((double)value_of(the_mark) - TOL) : 0u;
+        const unsigned mark = the_mark ? key_of(__fsub_rd(value_of(the_mark), BELOW)) : 0u;
         each([&](const Cand& c) {
             if (key_of_score(c.s) < mark) return;
             const int slot = atomicAdd(&count, 1);
@@ -447,25 +450,33 @@ __global__ void __launch_bounds__(GNT) beam_group_kernel(BeamParams p) {
         });
         __syncthreads();
         const int have = count;
+        bool near = have > LIST;                    // a pair to look at: unknown of a list that overflowed
         if (have <= LIST) {
             for (int i0 = 0; i0 < have; i0 += GNT / 8) {
                 const int i = i0 + (int)threadIdx.x / 8;
-                const Cand c = i < have ? list[i] : Cand{0.0, 0};
+                const Cand c = i < have ? list[i] : Cand{0.0, 0, 0};
                 int rank = 0;
-                for (int j = threadIdx.x & 7; j < have; j += 8) rank += before(list[j], c);
+                bool close = false;
+                for (int j = threadIdx.x & 7; j < have; j += 8) {
+                    const Cand o = list[j];
+                    rank += before(o, c);
+                    close |= o.beam != c.beam && fabs(o.s - c.s) <= TOL;
+                }
                 rank = sum8(rank);
+                near |= close && i < have && rank < want;
                 if (i < have && (threadIdx.x & 7) == 0 && rank < want) first[rank] = c;
             }
             __syncthreads();
         } else {
             // too many equal ones for the list: the best, want times
-            Cand last = {INFINITY, -1};
+            Cand last = {INFINITY, -1, 0};
             for (int m = 0; m < want; ++m) {
-                Cand b = {-INFINITY, INT32_MAX};
+                Cand b = {-INFINITY, INT32_MAX, 0};
                 each([&](const Cand& c) { if (before(last, c) && before(c, b)) b = c; });
 #pragma unroll
                 for (int o = 16; o > 0; o >>= 1) {
-                    const Cand c = {__shfl_xor_sync(0xffffffffu, b.s, o), __shfl_xor_sync(0xffffffffu, b.at, o)};
+                    const Cand c = {__shfl_xor_sync(0xffffffffu, b.s, o), __shfl_xor_sync(0xffffffffu, b.at, o),
+                                    __shfl_xor_sync(0xffffffffu, b.beam, o)};
                     if (before(c, b)) b = c;
                 }
                 if (lane == 0) list[warp] = b;
@@ -478,25 +489,18 @@ __global__ void __launch_bounds__(GNT) beam_group_kernel(BeamParams p) {
             }
         }
         if (turn == 1) break;
-        // candidates of different beams that the fp32 sums cannot order
-        bool near = false;
-        auto pair_up = [&](const Cand& a, const Cand& b) {
-            const int ka = a.at / p.V, kb = b.at / p.V;
-            if (ka == kb) return;
-            if (kind[ka] == LIVE) { redo[ka] = 1; near = true; }
-            if (kind[kb] == LIVE) { redo[kb] = 1; near = true; }
-        };
-        if ((int)threadIdx.x + 1 < want) {          // neighbours in the list
-            const Cand a = first[threadIdx.x], b = first[threadIdx.x + 1];
-            if (b.s > -INFINITY && a.s - b.s <= TOL) pair_up(a, b);
-        }
-        const Cand end = first[want - 1];           // all around the M-th
-        auto around = [&](const Cand& c) { if (fabs(c.s - end.s) <= TOL) pair_up(c, end); };
-        if (end.s > -INFINITY) {
-            if (have > LIST) each(around);
-            else for (int i = threadIdx.x; i < have; i += GNT) around(list[i]);
-        }
+        // pairs of different beams that the fp32 sums cannot order, one of them among the M
         if (!__syncthreads_or(near)) break;
+        bool again = false;
+        for (int m = 0; m < want; ++m) {
+            const Cand a = first[m];
+            each([&](const Cand& c) {
+                if (c.beam == a.beam || !(fabs(c.s - a.s) <= TOL)) return;
+                if (kind[a.beam] == LIVE) { redo[a.beam] = 1; again = true; }
+                if (kind[c.beam] == LIVE) { redo[c.beam] = 1; again = true; }
+            });
+        }
+        if (!__syncthreads_or(again)) break;
         for (int k = 0; k < p.K; ++k) {
             if (!redo[k]) continue;
             const double l = exact_lse<XT, GNT>(p, g * p.K + k, top[k], red);
@@ -509,8 +513,8 @@ __global__ void __launch_bounds__(GNT) beam_group_kernel(BeamParams p) {
         const Cand c = first[m];
         if (!GDR_INB(c.at >= 0 && c.at < (long long)p.K * p.V, 1011)) continue;
         p.out_scores[at] = (float)c.s;
-        p.out_parent[at] = c.at / p.V;
-        p.out_token[at] = c.at % p.V;
+        p.out_parent[at] = c.beam;
+        p.out_token[at] = c.at - c.beam * p.V;
     }
 }
 
