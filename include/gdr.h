@@ -563,8 +563,9 @@ GDR_API gdr_status gdr_layernorm_bwd(const gdr_norm_desc* desc, const void* x, c
  * Where fewer than M candidates are above -inf, the list is filled with -inf ones by the lowest
  * k * V + v.
  *
- * The sums run in fp32; where two neighbours of the list that belong to different beams are
- * closer than that allows, the beams' sums are formed again in 64 bits before they are ordered.
+ * The sums run in fp32; where a candidate of the list and one of another beam, in the list or not,
+ * are closer than that allows, both beams' sums are formed again in 64 bits before they are
+ * ordered.  (Within a beam the order is that of its logits, which needs no sum.)
  */
 typedef struct {
     int G, K, V, M;       /* groups, beams (1..64), vocabulary, candidates out (1..64, <= K * V); K * V < 2^31,

@@ -30,7 +30,7 @@ namespace bms {
 constexpr int NT = 256;
 constexpr int WARPS = NT / 32;
 constexpr int MOST = 64;                // of K and M
-constexpr int LIST = 1024;              // candidates that reach the mark; more: M rounds of the largest
+constexpr int LIST = 1024;              // candidates that reach the mark; more (many equal, or a mark of -inf): M rounds of the largest
 
 struct BeamParams {
     int G, K, V, M;
@@ -252,7 +252,7 @@ __global__ void __launch_bounds__(NT, E > 8 && sizeof(XT) == 4 ? 4 : 6) beam_row
             token[i] = -1;
         }
     } else {
-        // too many equal ones for the list: the largest, M times
+        // too many for the list (equal ones, or all of a piece whose mark is -inf): the largest, M times
         unsigned long long last = ~0ull;
         for (int m = 0; m < p.M; ++m) {
             unsigned long long c = 0;
